@@ -276,3 +276,8 @@ class ExpertTable:
     @property
     def ptr(self) -> int:
         return self.desc.data_ptr()
+
+
+# The operators around the layer in a serving step.
+from .serve import (KVBatch, KVCache, SAMPLE_MAX_VOCAB, SERVE_EXPORTS, SERVE_MAX_BATCH,  # noqa: E402
+                    attention_workspace_bytes, kv_append, prefix_attention, rope_table, sample)

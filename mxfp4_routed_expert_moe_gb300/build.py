@@ -12,8 +12,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mxfp4.so")
-SOURCES = ["abi.cu", "route.cu", "route_tc.cu", "decode.cu", "decode_mx.cu", "prefill.cu"]
-HEADERS = ["common.cuh", "kernels.h", "async.cuh", "route_small.cuh", "tcgen05.cuh", "decode_mx.cuh"]
+SOURCES = ["abi.cu", "route.cu", "route_tc.cu", "decode.cu", "decode_mx.cu", "prefill.cu", "serve.cu",
+           "kv_append.cu", "attention.cu", "sample.cu"]
+HEADERS = ["common.cuh", "kernels.h", "async.cuh", "route_small.cuh", "tcgen05.cuh", "decode_mx.cuh", "serve.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC] + ARCH
@@ -21,7 +22,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS if os.path.exists(os.path.join(CSRC, f))]
-    files.append(os.path.join(INCLUDE, "moe_mxfp4.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("moe_mxfp4.h", "moe_serve.h")]
     return files
 
 

@@ -9,15 +9,16 @@
 
 using namespace moe;
 
-namespace moe {
-ProfHook g_prof = {};
-}
-
 namespace {
 // Cycles before a bounded device wait gives up (moe_set_wait_limit; the
 // default only ends waits that can never complete).
 long long g_wait_limit = kWaitCycles;
 }  // namespace
+
+namespace moe {
+ProfHook g_prof = {};
+long long wait_limit() { return g_wait_limit; }
+}
 
 namespace {
 

@@ -28,6 +28,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 int device_sm_count();
 
+// Cycles before a bounded device wait gives up (moe_set_wait_limit).
+long long wait_limit();
+
 // Raise a kernel's dynamic shared memory limit to at least `bytes` (once per
 // kernel and size; later calls are a table lookup).
 cudaError_t ensure_smem_attr(const void* kernel, size_t bytes);

@@ -1,0 +1,205 @@
+"""The operators around the layer in a serving step (``include/moe_serve.h``): new keys and values into
+a paged cache with rotary positions on the way, attention of a batch that shares a prefix over that cache,
+and sampling from logits.  Argument marshalling only, as in the package itself."""
+from __future__ import annotations
+
+import ctypes
+
+from . import MoeError, _check, _dtype_of, _ptr, _stream, lib
+
+__all__ = ["KVCache", "KVBatch", "kv_append", "prefix_attention", "attention_workspace_bytes", "sample",
+           "rope_table", "SERVE_EXPORTS", "SAMPLE_MAX_VOCAB", "SERVE_MAX_BATCH"]
+
+# Every symbol moe_serve.h declares (checked by the tests against the .so).
+SERVE_EXPORTS = ("moe_kv_append", "moe_attention_workspace_bytes", "moe_prefix_attention", "moe_sample")
+SAMPLE_MAX_VOCAB = 1 << 18   # MOE_SAMPLE_MAX_VOCAB
+SERVE_MAX_BATCH = 4096       # MOE_SERVE_MAX_BATCH
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("table_pages", ctypes.c_int32), ("prefix_len", ctypes.c_int32),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("prefix_table", ctypes.c_void_p)]
+
+
+_READY = None
+
+
+def _lib():
+    """The loaded library with the argument types of this module's calls."""
+    global _READY
+    if _READY is None:
+        L = lib()
+        vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        P = ctypes.POINTER
+        L.moe_kv_append.argtypes = [P(_Cache), P(_Batch), i32, vp, vp, vp, i32, i64, i64, i64, vp, i64, vp, i32, i32,
+                                    i32, vp, vp]
+        L.moe_attention_workspace_bytes.restype = sz
+        L.moe_attention_workspace_bytes.argtypes = [P(_Cache), P(_Batch), i32]
+        L.moe_prefix_attention.argtypes = [P(_Cache), P(_Batch), vp, i32, i64, f32, vp, i64, vp, vp, sz, vp, vp]
+        L.moe_sample.argtypes = [i32, i32, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        _READY = L
+    return _READY
+
+
+def _want(t, what, dtype, shape=None):
+    """Checks a tensor argument: its type, shape (None: any) and that it is contiguous."""
+    if str(t.dtype) != "torch." + dtype:
+        raise TypeError(f"{what} must be torch.{dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+class KVCache:
+    """A paged cache over two bf16 tensors [num_pages][page_size][kv_heads][head_dim].  Views of another
+    order (head-major pages, one tensor that holds both) are taken as they are, by their strides."""
+
+    def __init__(self, k, v):
+        for t, what in ((k, "k"), (v, "v")):
+            if str(t.dtype) != "torch.bfloat16":
+                raise TypeError(f"the cache's {what} must be torch.bfloat16, not {t.dtype}")
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"the cache's {what} must be [pages][page_size][kv_heads][head_dim], contiguous in the last")
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v of a cache must have the same shape and strides")
+        self.k, self.v = k, v
+        pages, size, heads, dim = k.shape
+        self.struct = _Cache(k.data_ptr(), v.data_ptr(), pages, size, heads, dim, *k.stride()[:3])
+        self.ref = ctypes.byref(self.struct)
+        self.heads, self.dim = heads, dim
+
+
+class KVBatch:
+    """A batch of sequences over one cache: their lengths and page tables on the device, and the prefix
+    that all of them share.
+
+    ``kv_len`` [B] int32: tokens of each sequence's own part, the new ones included; ``table`` [B][pages]
+    int32: their pages; ``q_start`` [B + 1] int32: first row of each sequence among the ``tokens`` new ones
+    (None: one token each), at most ``max_q`` a sequence; ``prefix_table`` int32: the pages of the first
+    ``prefix_len`` tokens that every sequence sees before its own.  The tensors are kept and may be updated
+    in place between calls."""
+
+    def __init__(self, kv_len, table, tokens=None, q_start=None, max_q=1, prefix_table=None, prefix_len=0):
+        B = kv_len.shape[0]
+        if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be [batch][pages], contiguous in the last")
+        if str(table.dtype) != "torch.int32":
+            raise TypeError(f"table must be torch.int32, not {table.dtype}")
+        if prefix_len > 0 and (prefix_table is None or prefix_table.numel() < 1):
+            raise ValueError("a prefix needs its page table")
+        stride = table.stride(0) if B > 1 else max(table.stride(0), table.shape[1])
+        self.kv_len, self.table, self.q_start, self.prefix_table = kv_len, table, q_start, prefix_table
+        self.struct = _Batch(B, B if tokens is None else tokens, max_q, stride, table.shape[1], prefix_len,
+                             None if q_start is None else _want(q_start, "q_start", "int32", (B + 1,)),
+                             _want(kv_len, "kv_len", "int32", (B,)), table.data_ptr(),
+                             None if prefix_table is None else _want(prefix_table, "prefix_table", "int32"))
+        self.prefix_tokens = 0 if prefix_table is None else prefix_table.numel()
+        self.ref = ctypes.byref(self.struct)
+        self.tokens = self.struct.tokens
+
+    def check_prefix(self, cache):
+        if self.struct.prefix_len > self.prefix_tokens * cache.struct.page_size:
+            raise ValueError("prefix_len is more than the prefix's pages hold")
+
+
+def _rows(x, what, tokens, heads, dim):
+    """[tokens][heads][dim] with the heads of a token side by side: the stride between tokens."""
+    if tuple(x.shape) != (tokens, heads, dim):
+        raise ValueError(f"{what} must have shape {(tokens, heads, dim)}, not {tuple(x.shape)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return x.stride(0) if tokens > 1 else heads * dim
+
+
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """Cosines and sines of positions 0 .. positions - 1 for :func:`kv_append`: fp32 [positions][rot_dim],
+    the rot_dim / 2 cosines of angles position * base^(-2i / rot_dim), then the sines (computed in fp64:
+    an angle of a long context has too few bits in fp32)."""
+    import torch
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, device=device, dtype=torch.float64) / rot_dim)
+    a = torch.arange(positions, device=device, dtype=torch.float64)[:, None] * inv
+    return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope=None, rot_dim=0, interleaved=False,
+              status=None, stream=None):
+    """moe_kv_append: k, v [tokens][kv_heads][dim] (fp32 or bf16, any token stride) into the cache at each
+    token's place, with the first ``rot_dim`` values of each key head, and of the queries q -> q_out, rotated
+    by the rows of ``rope`` (see :func:`rope_table`)."""
+    n, dim = batch.tokens, cache.dim
+    ks, vs = _rows(k, "k", n, cache.heads, dim), _rows(v, "v", n, cache.heads, dim)
+    dt = _dtype_of(k)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have one type")
+    qh = qs = os = 0
+    if q is not None:
+        qh = q.shape[1]
+        qs = _rows(q, "q", n, qh, dim)
+        if q_out is not None:
+            if str(q_out.dtype) != "torch.bfloat16":
+                raise TypeError(f"q_out must be torch.bfloat16, not {q_out.dtype}")
+            os = _rows(q_out, "q_out", n, qh, dim)
+    rows = 0
+    if rope is not None:
+        _want(rope, "rope", "float32", (rope.shape[0], rot_dim))
+        rows = rope.shape[0]
+    _check(_lib().moe_kv_append(cache.ref, batch.ref, dt, _ptr(q), k.data_ptr(), v.data_ptr(), qh, qs, ks, vs,
+                                _ptr(q_out), os, _ptr(rope), rows, int(rot_dim), int(bool(interleaved)), _ptr(status),
+                                _stream(stream)), "moe_kv_append")
+
+
+def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int) -> int:
+    """moe_attention_workspace_bytes; raises MoeError where moe_prefix_attention would refuse the arguments."""
+    n = int(_lib().moe_attention_workspace_bytes(cache.ref, batch.ref, int(q_heads)))
+    if n == 0:
+        raise MoeError(1, "moe_attention_workspace_bytes")
+    return n
+
+
+def prefix_attention(cache: KVCache, batch: KVBatch, q, out, ws, scale=None, lse=None, status=None, stream=None):
+    """moe_prefix_attention: q, out bf16 [tokens][q_heads][dim] (any token stride); ``scale`` defaults to
+    dim^-1/2; ``lse`` is None or fp32 [tokens][q_heads]; ``ws`` a uint8 tensor of at least
+    :func:`attention_workspace_bytes`."""
+    n, dim = batch.tokens, cache.dim
+    qh = q.shape[1]
+    qs, os = _rows(q, "q", n, qh, dim), _rows(out, "out", n, qh, dim)
+    for t, what in ((q, "q"), (out, "out")):
+        if str(t.dtype) != "torch.bfloat16":
+            raise TypeError(f"{what} must be torch.bfloat16, not {t.dtype}")
+    batch.check_prefix(cache)
+    if lse is not None:
+        _want(lse, "lse", "float32", (n, qh))
+    _check(_lib().moe_prefix_attention(cache.ref, batch.ref, q.data_ptr(), qh, qs,
+                                       dim ** -0.5 if scale is None else float(scale), out.data_ptr(), os, _ptr(lse),
+                                       ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)),
+           "moe_prefix_attention")
+
+
+def sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, kept=None,
+           probs=None, stream=None):
+    """moe_sample: one token per row of ``logits`` [rows][vocab] (fp32 or bf16, any row stride) into ``token``
+    [rows] int32, drawn by ``u`` [rows] in [0, 1).  ``temperature``, ``top_p``, ``min_p`` (fp32) and ``top_k``
+    (int32) are [rows] device tensors or None; ``logprob`` [rows] fp32, ``kept`` [rows] int32 and ``probs``
+    [rows][vocab] fp32 receive the token's log-probability, the number of tokens kept and their
+    probabilities."""
+    rows, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be contiguous in the last dimension")
+    opt = lambda t, what, dt, shape=(rows,): None if t is None else _want(t, what, dt, shape)  # noqa: E731
+    stride = logits.stride(0) if rows > 1 else vocab
+    _check(_lib().moe_sample(rows, vocab, logits.data_ptr(), _dtype_of(logits), stride, _want(u, "u", "float32", (rows,)),
+                             opt(temperature, "temperature", "float32"), opt(top_k, "top_k", "int32"),
+                             opt(top_p, "top_p", "float32"), opt(min_p, "min_p", "float32"),
+                             _want(token, "token", "int32", (rows,)), opt(logprob, "logprob", "float32"),
+                             opt(kept, "kept", "int32"), opt(probs, "probs", "float32", (rows, vocab)),
+                             _stream(stream)), "moe_sample")
