@@ -101,10 +101,18 @@ __global__ void __launch_bounds__(kWarpThreads, 2)
     sh.abort_flag = 0;
     mbar_init_fence();
   }
+  // After the Tensor Memory kernel (side 1), which starts it only when all
+  // earlier work is complete, this kernel overlaps that one's tail: they take
+  // different parts.  It then waits for it at its end, so that the joining
+  // kernel finds both complete.
+  const bool overlap = p.side[1].own || p.side[1].prefix;
+  if (!overlap) pdl_wait();
   pdl_trigger();
-  pdl_wait();
   AttnWalk w;
-  if (!attn_plan(p, sd, sh.plan, w)) return;  // its barriers also publish the mbarriers
+  if (!attn_plan(p, sd, sh.plan, w)) {  // its barriers also publish the mbarriers
+    if (overlap) pdl_wait();
+    return;
+  }
   AttnSeg g;
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer --
@@ -149,6 +157,7 @@ __global__ void __launch_bounds__(kWarpThreads, 2)
         const int n = use + (s < st ? 1 : 0);
         if (n > 0 && !mbar_wait(&sh.full[s], (n - 1) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
       }
+    if (overlap) pdl_wait();
     return;
   }
   // ------------------------------------------------------------- consumers --
@@ -330,6 +339,7 @@ __global__ void __launch_bounds__(kWarpThreads, 2)
       }
     }
   }
+  if (overlap) pdl_wait();
 }
 
 template <int D, int MT>

@@ -1,0 +1,396 @@
+// attention_tc.cu — attention over the paged cache on tcgen05 tensor cores,
+// for parts that many query rows share: the prefix of a batch, and long new
+// parts (prompts).
+//
+// Bound by the tensor cores from about 280 rows per key head on (2 * rows
+// operations per cache byte against the chip's ratio of the two rates), by HBM
+// below.  One CTA per SM takes a contiguous range of (row tile of 256, unit of
+// 128 tokens) work.  Roles:
+//   * a producer warp copies K and V units (128 tokens x head_dim) into a ring
+//     of shared-memory buffers with tensor-map boxes, one per page;
+//   * one thread issues the MMAs: S_t = Q_t K^T and O_t += P_t V for the two
+//     128-row halves t of the tile, S and O in Tensor Memory (S_0, S_1, O_0,
+//     O_1: 128 columns each, all 512 at head_dim 128);
+//   * warpgroup t turns S_t into P_t = 2^(S_t scale - m) in bf16, written over
+//     S_t, one row per thread, so that row sums and maxima need no exchange.
+// While one half's softmax runs, the other half's MMAs do.  The reference m of
+// a row moves only when its maximum grew by more than 2^8 (then the warpgroup
+// rescales O_t in Tensor Memory): any reference gives the same quotient, and
+// 2^8 keeps every partial sum far inside fp32.
+#include "serve.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kUnit = kAttnTcUnit;       // tokens
+constexpr int kHalfRows = 128;           // rows of an MMA tile
+constexpr int kThreads = 10 * 32;        // 2 x 4 softmax warps, producer, MMA
+constexpr int kBufs = 5;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kGrow = 8.f;             // log2 of the growth a stale reference may see
+
+template <int D>
+struct TcCfg {
+  static constexpr int kSub = kUnit * 128;           // 128 rows x 64 values
+  static constexpr int kMat = kSub * (D / 64);       // one operand tile
+  static constexpr int kSmem = (2 + kBufs) * kMat;   // Q_0, Q_1, ring
+};
+
+struct TcShared {
+  uint64_t full[kBufs], empty[kBufs];
+  uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  AttnPlanShared plan;
+};
+
+__device__ __forceinline__ bool tc_wait(TcShared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
+  const bool diag = p.wait_limit < kWaitCycles;
+  if (diag ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (diag ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int*)&sh.abort_flag) return false;
+    if (clock64() - t0 > p.wait_limit) {
+      set_status_word(p.status, MOE_ERR_TIMEOUT);
+      *(volatile int*)&sh.abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// V as B operand [N = 64 h + ..][K = tokens]: N contiguous (128-byte swizzle
+// atoms of 64 values x 8 tokens); 8-token groups 1024 bytes apart, 64-value
+// halves kSub apart.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(TcCfg<D>::kSub >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = TcCfg<D>;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ TcShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttnSide& sd = p.side[1];
+  if (warp == 9) {
+    tmem_alloc(&sh.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.q_ready[t], 4);
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_ready[t], 4);
+      mbar_init(&sh.o_done[t], 1);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort_flag = 0;
+    mbar_init_fence();
+  }
+  tc_fence_before();
+  // The kernels after this one may start once it has seen the work before it
+  // complete: the warp kernel, which takes the other parts, waits for nothing
+  // else (see k_attn_warp).
+  pdl_wait();
+  pdl_trigger();
+  AttnWalk w;
+  const bool work = attn_plan(p, sd, sh.plan, w);
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  AttnSeg g;
+  uint8_t* ring = dyn + 2 * C::kMat;
+  if (!work) {
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ producer --
+    const int box = attn_box(p.page_size, kUnit);
+    int bi = 0, use = 0;
+    bool ok = true;
+    while (ok && attn_next(p, sd, w, g)) {
+      for (int kv = g.kv0; kv < g.kv1 && ok; kv += kUnit) {
+        const int left = g.kv1 - kv < kUnit ? g.kv1 - kv : kUnit;
+        const int nb = (left + box - 1) / box;
+        int page = 0, y = 0;
+        if (lane < nb) {
+          const int tok = kv + lane * box;
+          page = __ldg(&w.a.table[tok >> p.page_shift]);
+          if (page < 0 || page >= p.num_pages) {
+            set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
+            page = p.num_pages;  // past the map: the box is filled with zeros
+          }
+          y = tok & (p.page_size - 1);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          bool got = true;
+          if (use > 0 && lane == 0) got = tc_wait(sh, &sh.empty[bi], (use - 1) & 1, p);
+          if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[bi], (uint32_t)(nb * box * D * 2));
+          __syncwarp();
+          if (lane < nb) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_4d(ring + bi * C::kMat + h * C::kSub + lane * box * 128, m ? &vmap : &kmap, h * 64, y, g.kvh,
+                          page, &sh.full[bi]);
+          }
+          __syncwarp();
+          if (++bi == kBufs) bi = 0, ++use;
+        }
+      }
+    }
+    // No copy may be in flight when the CTA exits.
+    if (lane == 0)
+      for (int i = 0; i < kBufs; ++i) {
+        const int n = use + (i < bi ? 1 : 0);
+        if (n > 0 && !mbar_wait(&sh.full[i], (n - 1) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+      }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------------- MMA --
+    const uint32_t id_s = idesc_bf16_f32(128, kUnit);
+    const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B: N contiguous
+    const uint32_t qb = smem_u32(dyn), rb = smem_u32(ring);
+    int bi = 0, use = 0;         // next ring buffer
+    uint32_t nq[2] = {0, 0};     // segments that used half t
+    uint32_t np[2] = {0, 0};     // P tiles of half t taken
+    bool ok = true;
+    auto take = [&](int& b) {    // the next ring buffer, filled
+      b = bi;
+      ok = ok && __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.full[bi], use & 1, p), 0);
+      if (++bi == kBufs) bi = 0, ++use;
+    };
+    auto scores = [&](int t, int b) {
+      if (lane == 0) {
+#pragma unroll
+        for (int kb = 0; kb < D / 16; ++kb) {
+          const uint32_t off = (kb >> 2) * C::kSub + 32 * (kb & 3);
+          umma_f16(tmem + 128 * t, sdesc_sw128(qb + t * C::kMat + off), sdesc_sw128(rb + b * C::kMat + off), id_s, kb > 0);
+        }
+        umma_commit(&sh.s_full[t]);
+      }
+      __syncwarp();
+    };
+    while (ok && attn_next(p, sd, w, g)) {
+      const int nt = (g.kv1 - g.kv0 + kUnit - 1) / kUnit;
+      if (nt == 0) continue;
+      const int halves = g.rows > kHalfRows ? 2 : 1;
+      int kbuf, vbuf;
+      take(kbuf);
+      for (int t = 0; t < halves && ok; ++t) {
+        ok = __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.q_ready[t], nq[t]++ & 1, p), 0);
+        tc_fence_after();
+        if (ok) scores(t, kbuf);
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(&sh.empty[kbuf]);
+      for (int j = 0; j < nt; ++j) {
+        take(vbuf);
+        if (!ok) break;
+        const int left = g.kv1 - g.kv0 - j * kUnit;
+        if (left < kUnit) {
+          // Rows of V past the length may hold anything, and 0 * NaN is NaN.
+          uint8_t* vb = ring + vbuf * C::kMat;
+          const int n16 = (kUnit - left) * 8;
+          for (int h = 0; h < D / 64; ++h)
+            for (int i = lane; i < n16; i += 32)
+              *reinterpret_cast<uint4*>(vb + h * C::kSub + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+        }
+        const bool more = j + 1 < nt;
+        if (more) take(kbuf);
+        for (int t = 0; t < halves && ok; ++t) {
+          ok = __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.p_ready[t], np[t]++ & 1, p), 0);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kb = 0; kb < kUnit / 16; ++kb)
+              umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kb, sdesc_v<D>(rb + vbuf * C::kMat + 2048 * kb), id_o,
+                          j > 0 || kb > 0);
+            if (!more) umma_commit(&sh.o_done[t]);
+          }
+          __syncwarp();
+          if (more) scores(t, kbuf);
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          umma_commit(&sh.empty[vbuf]);
+          if (more) umma_commit(&sh.empty[kbuf]);
+        }
+      }
+    }
+    // No MMA may be in flight when Tensor Memory is released.
+    if (lane == 0) {
+      umma_commit(&sh.drain);
+      if (!mbar_wait(&sh.drain, 0)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax --
+    const int t = warp >> 2, q = warp & 3;
+    const int r = t * kHalfRows + q * 32 + lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+    const float c = p.scale_log2;
+    uint32_t ns = 0, no = 0;
+    bool ok = true;
+    while (ok && attn_next(p, sd, w, g)) {
+      if (t == 1 && g.rows <= kHalfRows) continue;
+      float* slot = sd.slots + (int64_t)g.slot * sd.rows * (D + 2);
+      const bool in = r < g.rows;
+      const int i = (g.row0 + (in ? r : 0)) / p.group;
+      const int vis = in ? attn_visible(p, w.a, w.set, i) : 0;
+      const int vis_min = attn_visible(p, w.a, w.set, (g.row0 + t * kHalfRows) / p.group);
+      if (g.kv0 < g.kv1) {
+        // This thread's query row into the swizzled A tile.  The MMAs that
+        // read the previous one are complete: their scores came back.
+        const uint16_t* src = p.q + (int64_t)(w.a.tok0 + i) * p.q_stride +
+                              (int64_t)(g.kvh * p.group + (g.row0 + (in ? r : 0)) - i * p.group) * D;
+        uint8_t* qd = dyn + t * C::kMat;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = in ? __ldg(reinterpret_cast<const uint4*>(src + 64 * h) + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(qd + h * C::kSub + sw128_offset(r & 127, k)) = v[k];
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_ready[t]);
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int kv = g.kv0; kv < g.kv1; kv += kUnit) {
+        ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.s_full[t], ns++ & 1, p));
+        if (!ok) break;
+        tc_fence_after();
+        // Two passes over S in pieces of 64 columns: re-reading Tensor Memory
+        // costs less than the spills that 128 live scores would bring.
+        const bool edge = kv + kUnit > vis_min;
+        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t s[2][32];
+          tmem_ld32(ts + 64 * k, s[0]);
+          tmem_ld32(ts + 64 * k + 32, s[1]);
+          tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (kv + 64 * k + e >= vis) s[e >> 5][e & 31] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e >> 5][e & 31]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (kv == g.kv0) {
+          m = top;
+        } else if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
+          // O_t is complete up to the previous unit: its MMAs were issued
+          // before the scores that just arrived.
+          const float mn = top > m + kGrow ? top : m;
+          const float f = m == mn ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t v[32];
+            tmem_ld32(to + 32 * k, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st32(to + 32 * k, v);
+          }
+        }
+        const float ms = m == -CUDART_INF_F ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t s[2][32], v[32];
+          tmem_ld32(ts + 64 * k, s[0]);
+          tmem_ld32(ts + 64 * k + 32, s[1]);
+          tmem_ld_wait();
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (kv + 64 * k + e >= vis) s[e >> 5][e & 31] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ex2(fmaf(__uint_as_float(s[e >> 4][2 * (e & 15)]), c, -ms));
+            const float b = ex2(fmaf(__uint_as_float(s[e >> 4][2 * (e & 15) + 1]), c, -ms));
+            sum[e & 1] += a;
+            sum[2 + (e & 1)] += b;
+            v[e] = pack_bf16(a, b);
+          }
+          // P's columns 32 k .. lie below the scores still to be read.
+          tmem_st32(ts + 32 * k, v);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[t]);
+      }
+      if (!ok) break;
+      if (g.kv0 < g.kv1) {
+        ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.o_done[t], no++ & 1, p));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t v[32];
+          tmem_ld32(to + 32 * k, v);
+          tmem_ld_wait();
+          if (in)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(slot + (int64_t)r * D + 32 * k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        tc_fence_before();
+      }
+      if (in) {
+        slot[sd.rows * D + r] = m;
+        slot[sd.rows * (D + 1) + r] = l;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
+  cudaError_t err = ensure_smem_attr((const void*)k_attn_tc<D>, TcCfg<D>::kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k_attn_tc<D>, dim3(p.side[1].ctas), dim3(kThreads), TcCfg<D>::kSmem, s, p, km, vm);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
+  return p.head_dim == 128 ? launch<128>(p, km, vm, s) : launch<64>(p, km, vm, s);
+}
+
+}  // namespace moe

@@ -47,17 +47,25 @@ int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
   return t;
 }
 
-// Which kernel takes which part.  The warp kernel (16 to 64 rows a tile).
+// Which kernel takes which part.  The warp kernel takes parts of few rows (a
+// tile of 16, 32 or 64), the Tensor Memory kernel the others.
 void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)[2]) {
   memset(side, 0, sizeof side);
-  AttnSide& w = side[0];
-  w.own = 1;
-  w.prefix = b.prefix_len > 0;
-  const int64_t rows = (int64_t)b.max_q * group;
-  w.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t own_rows = (int64_t)b.max_q * group, prefix_rows = (int64_t)b.tokens * group;
+  const bool own_tc = own_rows > 64, prefix_tc = b.prefix_len > 0 && (own_tc || prefix_rows > 16);
+  AttnSide &w = side[0], &t = side[1];
+  w.own = !own_tc;
+  w.prefix = b.prefix_len > 0 && !prefix_tc;
+  w.rows = own_rows <= 16 ? 16 : own_rows <= 32 ? 32 : 64;
   w.unit = kAttnWarpUnit;
   w.ctas = kAttnWarpCtas;
   w.min_units = 2;
+  t.own = own_tc;
+  t.prefix = prefix_tc;
+  t.rows = kAttnTcRows;
+  t.unit = kAttnTcUnit;
+  t.ctas = kAttnTcCtas;
+  t.min_units = 1;
 }
 
 size_t side_layout(const moe_kv_batch& b, int group, int kv_heads, int head_dim, AttnSide (&side)[2], void* base) {
@@ -182,13 +190,13 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   p.status = status;
   p.wait_limit = wait_limit();
   cudaStream_t s = (cudaStream_t)stream;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 1; i >= 0; --i) {
     if (!p.side[i].own && !p.side[i].prefix) continue;
     CUtensorMap km, vm;
     const int box = attn_box(cache->page_size, p.side[i].unit);
     if ((st = cache_map(&km, cache, cache->k, box)) != MOE_OK || (st = cache_map(&vm, cache, cache->v, box)) != MOE_OK)
       return st;
-    if ((st = cuda_status(launch_attn_warp(p, km, vm, s))) != MOE_OK) return st;
+    if ((st = cuda_status(i ? launch_attn_tc(p, km, vm, s) : launch_attn_warp(p, km, vm, s))) != MOE_OK) return st;
   }
   return cuda_status(launch_attn_join(p, s));
 }

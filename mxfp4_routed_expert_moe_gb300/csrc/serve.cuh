@@ -301,10 +301,15 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnSide& s
 // Token rows of one tensor-map box: pages shorter than a unit give several.
 __host__ __device__ __forceinline__ int attn_box(int page_size, int unit) { return page_size < unit ? page_size : unit; }
 
+cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
 // CTAs of the warp kernel (two per SM).
 constexpr int kAttnWarpCtas = 2 * kNumSMs;
 constexpr int kAttnWarpUnit = 64;
+// The Tensor Memory kernel: one CTA per SM, tiles of 256 rows, units of 128 tokens.
+constexpr int kAttnTcCtas = kNumSMs;
+constexpr int kAttnTcRows = 256;
+constexpr int kAttnTcUnit = 128;
 
 }  // namespace moe
