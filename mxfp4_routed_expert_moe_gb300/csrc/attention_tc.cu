@@ -25,9 +25,13 @@ namespace {
 
 constexpr int kUnit = kAttnTcUnit;       // tokens
 constexpr int kHalfRows = 128;           // rows of an MMA tile
-constexpr int kThreads = 10 * 32;        // 2 x 4 softmax warps, producer, MMA
+constexpr int kThreads = 12 * 32;        // 2 x 4 softmax warps, producer, MMA, two idle
 constexpr int kBufs = 5;
 constexpr uint32_t kTmemCols = 512;
+// Registers: 168 a thread at launch (384 * 168 = 64,512); the softmax
+// warpgroups take 224 each, which holds a row of 128 scores, and the third
+// keeps 56: 128 * (224 + 224 + 56) = 64,512.
+constexpr int kRegsSoftmax = 224, kRegsRest = 56;
 constexpr float kGrow = 8.f;             // log2 of the growth a stale reference may see
 
 template <int D>
@@ -39,7 +43,7 @@ struct TcCfg {
 
 struct TcShared {
   uint64_t full[kBufs], empty[kBufs];
-  uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem_base;
   int abort_flag;
   AttnPlanShared plan;
@@ -60,18 +64,71 @@ __device__ __forceinline__ bool tc_wait(TcShared& sh, uint64_t* bar, uint32_t pa
   }
 }
 
-// V as B operand [N = 64 h + ..][K = tokens]: N contiguous (128-byte swizzle
-// atoms of 64 values x 8 tokens); 8-token groups 1024 bytes apart, 64-value
-// halves kSub apart.
+// The MMAs are issued by converged code of the whole warp with a predicate
+// that is true in one lane: in a divergent branch each operand goes through a
+// vector-to-uniform move of its own, which measured 125 cycles an MMA.
+// Descriptors are given by their low words (address >> 4, and the leading
+// offset above it).
+//
+// High words: stride offset 1024 bytes, fixed bit, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// Low word of a K-major operand (leading offset unused).
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+// V as B operand [N = values][K = tokens]: N contiguous (128-byte swizzle
+// atoms of 64 values x 8 tokens); 8-token groups 1024 bytes apart, the halves
+// of 64 values (leading offset) one sub-tile apart.
 template <int D>
-__device__ __forceinline__ uint64_t sdesc_v(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(TcCfg<D>::kSub >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
+__device__ __forceinline__ uint32_t desc_v(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(TcCfg<D>::kSub >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " mov.b64 da, {%1, %6};\n mov.b64 db, {%2, %6};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " mov.b64 db, {%2, %6};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
+  return r;
+}
+
+// Two fp32 values in one register pair, for the packed FMA and add.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <int D>
@@ -94,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.q_ready[t], 4);
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_ready[t], 4);
+      mbar_init(&sh.p_ready[t][0], 4);
+      mbar_init(&sh.p_ready[t][1], 4);
       mbar_init(&sh.o_done[t], 1);
     }
     mbar_init(&sh.drain, 1);
@@ -113,8 +171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
   AttnSeg g;
   uint8_t* ring = dyn + 2 * C::kMat;
-  if (!work) {
-  } else if (warp == 8) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (work && warp == 8) {
     // ------------------------------------------------------------ producer --
     const int box = attn_box(p.page_size, kUnit);
     int bi = 0, use = 0;
@@ -160,48 +219,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = use + (i < bi ? 1 : 0);
         if (n > 0 && !mbar_wait(&sh.full[i], (n - 1) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
       }
-  } else if (warp == 9) {
+    } else if (work && warp == 9) {
     // ----------------------------------------------------------------- MMA --
     const uint32_t id_s = idesc_bf16_f32(128, kUnit);
     const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B: N contiguous
     const uint32_t qb = smem_u32(dyn), rb = smem_u32(ring);
+    const uint32_t one = elect_one();  // commits track the electing lane's MMAs
     int bi = 0, use = 0;         // next ring buffer
     uint32_t nq[2] = {0, 0};     // segments that used half t
     uint32_t np[2] = {0, 0};     // P tiles of half t taken
     bool ok = true;
+    auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
     auto take = [&](int& b) {    // the next ring buffer, filled
       b = bi;
-      ok = ok && __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.full[bi], use & 1, p), 0);
+      ok = ok && all(tc_wait(sh, &sh.full[bi], use & 1, p));
       if (++bi == kBufs) bi = 0, ++use;
     };
     auto scores = [&](int t, int b) {
-      if (lane == 0) {
+      const uint32_t qa = desc_k(qb + t * C::kMat), ka = desc_k(rb + b * C::kMat);
 #pragma unroll
-        for (int kb = 0; kb < D / 16; ++kb) {
-          const uint32_t off = (kb >> 2) * C::kSub + 32 * (kb & 3);
-          umma_f16(tmem + 128 * t, sdesc_sw128(qb + t * C::kMat + off), sdesc_sw128(rb + b * C::kMat + off), id_s, kb > 0);
-        }
-        umma_commit(&sh.s_full[t]);
+      for (int kb = 0; kb < D / 16; ++kb) {
+        const uint32_t off = ((kb >> 2) * C::kSub + 32 * (kb & 3)) >> 4;
+        mma_ss(tmem + 128 * t, qa + off, ka + off, id_s, kb > 0, one);
       }
-      __syncwarp();
+      commit_one(&sh.s_full[t], one);
     };
+    // P_t V of one half: the two parts of 64 tokens as their weights arrive.
+    auto values = [&](int t, int b, bool first) {
+      const uint32_t va = desc_v<D>(rb + b * C::kMat);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ok = ok && all(tc_wait(sh, &sh.p_ready[t][k], np[t] & 1, p));
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kb = 4 * k; kb < 4 * k + 4; ++kb)
+          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kb, va + kb * (2048 >> 4), id_o, !first || kb > 0, one);
+      }
+      ++np[t];
+    };
+    // The buffers of the next unit are waited for while MMAs are queued: the
+    // time between the last scores of a unit and the next P V is tensor idle.
     while (ok && attn_next(p, sd, w, g)) {
       const int nt = (g.kv1 - g.kv0 + kUnit - 1) / kUnit;
       if (nt == 0) continue;
-      const int halves = g.rows > kHalfRows ? 2 : 1;
+      const bool two = g.rows > kHalfRows;
       int kbuf, vbuf;
       take(kbuf);
-      for (int t = 0; t < halves && ok; ++t) {
-        ok = __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.q_ready[t], nq[t]++ & 1, p), 0);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        ok = ok && all(tc_wait(sh, &sh.q_ready[t], nq[t]++ & 1, p));
+        if (!ok) break;
         tc_fence_after();
-        if (ok) scores(t, kbuf);
+        scores(t, kbuf);
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(&sh.empty[kbuf]);
-      for (int j = 0; j < nt; ++j) {
-        take(vbuf);
-        if (!ok) break;
+      commit_one(&sh.empty[kbuf], one);
+      take(vbuf);
+      if (nt > 1) take(kbuf);
+      for (int j = 0; j < nt && ok; ++j) {
         const int left = g.kv1 - g.kv0 - j * kUnit;
+        const bool more = j + 1 < nt;
         if (left < kUnit) {
           // Rows of V past the length may hold anything, and 0 * NaN is NaN.
           uint8_t* vb = ring + vbuf * C::kMat;
@@ -212,35 +289,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
         }
-        const bool more = j + 1 < nt;
-        if (more) take(kbuf);
-        for (int t = 0; t < halves && ok; ++t) {
-          ok = __shfl_sync(0xFFFFFFFFu, tc_wait(sh, &sh.p_ready[t], np[t]++ & 1, p), 0);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int kb = 0; kb < kUnit / 16; ++kb)
-              umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kb, sdesc_v<D>(rb + vbuf * C::kMat + 2048 * kb), id_o,
-                          j > 0 || kb > 0);
-            if (!more) umma_commit(&sh.o_done[t]);
-          }
-          __syncwarp();
-          if (more) scores(t, kbuf);
-        }
+        int vnext = 0, knext = 0;
+        values(0, vbuf, j == 0);
         if (!ok) break;
-        if (lane == 0) {
-          umma_commit(&sh.empty[vbuf]);
-          if (more) umma_commit(&sh.empty[kbuf]);
+        if (more) scores(0, kbuf);
+        else commit_one(&sh.o_done[0], one);
+        if (two) {
+          values(1, vbuf, j == 0);
+          if (!ok) break;
         }
+        commit_one(&sh.empty[vbuf], one);
+        if (more) {
+          take(vnext);
+          if (two) scores(1, kbuf);
+          commit_one(&sh.empty[kbuf], one);
+          if (j + 2 < nt) take(knext);
+        } else if (two) {
+          commit_one(&sh.o_done[1], one);
+        }
+        vbuf = vnext;
+        kbuf = knext;
       }
     }
     // No MMA may be in flight when Tensor Memory is released.
-    if (lane == 0) {
-      umma_commit(&sh.drain);
-      if (!mbar_wait(&sh.drain, 0)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+    commit_one(&sh.drain, one);
+    if (!mbar_wait(&sh.drain, 0)) set_status_word(p.status, MOE_ERR_TIMEOUT);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------- softmax --
     const int t = warp >> 2, q = warp & 3;
     const int r = t * kHalfRows + q * 32 + lane;  // row of the tile
@@ -248,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
     const float c = p.scale_log2;
     uint32_t ns = 0, no = 0;
-    bool ok = true;
+    bool ok = work;
     while (ok && attn_next(p, sd, w, g)) {
       if (t == 1 && g.rows <= kHalfRows) continue;
       float* slot = sd.slots + (int64_t)g.slot * sd.rows * (D + 2);
@@ -280,73 +356,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.s_full[t], ns++ & 1, p));
         if (!ok) break;
         tc_fence_after();
-        // Two passes over S in pieces of 64 columns: re-reading Tensor Memory
-        // costs less than the spills that 128 live scores would bring.
-        const bool edge = kv + kUnit > vis_min;
-        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        uint32_t s[kUnit];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t s[2][32];
-          tmem_ld32(ts + 64 * k, s[0]);
-          tmem_ld32(ts + 64 * k + 32, s[1]);
-          tmem_ld_wait();
-          if (edge) {
+        for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
+        tmem_ld_wait();
+        if (kv + kUnit > vis_min) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (kv + 64 * k + e >= vis) s[e >> 5][e & 31] = 0xFF800000u;
-          }
+          for (int e = 0; e < kUnit; ++e)
+            if (kv + e >= vis) s[e] = 0xFF800000u;
+        }
+        float mx[4];
 #pragma unroll
-          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e >> 5][e & 31]));
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = __uint_as_float(s[32 * k]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[32 * k + e])), __uint_as_float(s[32 * k + e + 1]));
+          mx[k] = fmaxf(mx[k], __uint_as_float(s[32 * k + 31]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (kv == g.kv0) {
-          m = top;
-        } else if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
-          // O_t is complete up to the previous unit: its MMAs were issued
-          // before the scores that just arrived.
-          const float mn = top > m + kGrow ? top : m;
-          const float f = m == mn ? 1.f : ex2(m - mn);
-          m = mn;
-          l *= f;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t v[32];
-            tmem_ld32(to + 32 * k, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st32(to + 32 * k, v);
-          }
-        }
-        const float ms = m == -CUDART_INF_F ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t s[2][32], v[32];
-          tmem_ld32(ts + 64 * k, s[0]);
-          tmem_ld32(ts + 64 * k + 32, s[1]);
-          tmem_ld_wait();
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (kv + 64 * k + e >= vis) s[e >> 5][e & 31] = 0xFF800000u;
-          }
+        // Weights of 64 tokens against the row's reference m.
+        const uint64_t c2 = pack2(c, c);
+        uint64_t sum[2] = {0, 0};
+        auto weights = [&](const uint32_t* x, uint32_t* v, float ref) {
+          const uint64_t r2 = pack2(-ref, -ref);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = ex2(fmaf(__uint_as_float(s[e >> 4][2 * (e & 15)]), c, -ms));
-            const float b = ex2(fmaf(__uint_as_float(s[e >> 4][2 * (e & 15) + 1]), c, -ms));
-            sum[e & 1] += a;
-            sum[2 + (e & 1)] += b;
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, r2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum[e & 1] = add2(sum[e & 1], pack2(a, b));
             v[e] = pack_bf16(a, b);
           }
-          // P's columns 32 k .. lie below the scores still to be read.
-          tmem_st32(ts + 32 * k, v);
+        };
+        auto give = [&](uint32_t* v, int k) {
+          tmem_st32(ts + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_ready[t][k]);
+        };
+        uint32_t v[32];
+        // The first half's weights against the old reference, while the
+        // maximum is still being found; kept unless the reference must move.
+        weights(s, v, m == -CUDART_INF_F ? 0.f : m);
+        if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
+          const float mn = top > m + kGrow ? top : m;
+          if (kv != g.kv0) {
+            // O_t is complete up to the previous unit: its MMAs were issued
+            // before the scores that just arrived.
+            const float f = m == mn ? 1.f : ex2(m - mn);
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              tmem_ld32(to + 32 * k, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+              tmem_st32(to + 32 * k, v);
+            }
+          }
+          m = mn;
+          sum[0] = sum[1] = 0;
+          weights(s, v, m == -CUDART_INF_F ? 0.f : m);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[t]);
+        give(v, 0);
+        weights(s + 64, v, m == -CUDART_INF_F ? 0.f : m);
+        give(v, 1);
+        float sa, sb;
+        unpack2(add2(sum[0], sum[1]), sa, sb);
+        l += sa + sb;
       }
       if (!ok) break;
       if (g.kv0 < g.kv1) {
