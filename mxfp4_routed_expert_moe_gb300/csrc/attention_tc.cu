@@ -46,7 +46,7 @@ struct TcShared {
   uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  AttnPlanShared plan;
+  AttnPlanShared<1> plan;
 };
 
 __device__ __forceinline__ bool tc_wait(TcShared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   AttnWalk w;
-  const bool work = attn_plan(p, sd, sh.plan, w);
+  long long total;
+  const long long per = attn_plan<1>(p, sd, sh.plan, total);
+  const bool work = attn_begin<1>(p, sd, sh.plan, 0, per, total, w);
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   AttnSeg g;
@@ -179,13 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int bi = 0, use = 0;
     bool ok = true;
     while (ok && attn_next(p, sd, w, g)) {
+      const int32_t* table = attn_table(p, g.set);
       for (int kv = g.kv0; kv < g.kv1 && ok; kv += kUnit) {
         const int left = g.kv1 - kv < kUnit ? g.kv1 - kv : kUnit;
         const int nb = (left + box - 1) / box;
         int page = 0, y = 0;
         if (lane < nb) {
           const int tok = kv + lane * box;
-          page = __ldg(&w.a.table[tok >> p.page_shift]);
+          page = __ldg(&table[tok >> p.page_shift]);
           if (page < 0 || page >= p.num_pages) {
             set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
             page = p.num_pages;  // past the map: the box is filled with zeros
@@ -328,24 +331,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && attn_next(p, sd, w, g)) {
       if (t == 1 && g.rows <= kHalfRows) continue;
       float* slot = sd.slots + (int64_t)g.slot * sd.rows * (D + 2);
+      uint8_t* qd = dyn + t * C::kMat;
       const bool in = r < g.rows;
-      const int i = (g.row0 + (in ? r : 0)) / p.group;
-      const int vis = in ? attn_visible(p, w.a, w.set, i) : 0;
-      const int vis_min = attn_visible(p, w.a, w.set, (g.row0 + t * kHalfRows) / p.group);
+      const int vis = in ? attn_visible(p, g, (g.row0 + r) / p.group) : 0;
+      const int vis_min = attn_visible(p, g, (g.row0 + t * kHalfRows) / p.group);
       if (g.kv0 < g.kv1) {
-        // This thread's query row into the swizzled A tile.  The MMAs that
-        // read the previous one are complete: their scores came back.
-        const uint16_t* src = p.q + (int64_t)(w.a.tok0 + i) * p.q_stride +
-                              (int64_t)(g.kvh * p.group + (g.row0 + (in ? r : 0)) - i * p.group) * D;
-        uint8_t* qd = dyn + t * C::kMat;
+        // The warp's 32 query rows into the swizzled A tile, whole rows at a
+        // time (one row per thread would take 32 lines per load).  The MMAs
+        // that read the previous ones are complete: their scores came back.
+        constexpr int L = D / 8, R = 32 / L;  // lanes of a row, rows of a pass
+        const int rl = q * 32 + lane / L, ch = lane % L;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
+        for (int b = 0; b < 32 / R; b += 8) {
           uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = in ? __ldg(reinterpret_cast<const uint4*>(src + 64 * h) + k) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) {
+            const int rr = g.row0 + t * kHalfRows + rl + (b + k) * R;
+            const int ii = rr / p.group;
+            v[k] = rr < g.row0 + g.rows
+                       ? __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(g.tok0 + ii) * p.q_stride +
+                                                              (int64_t)(g.kvh * p.group + rr - ii * p.group) * D + 8 * ch))
+                       : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(qd + h * C::kSub + sw128_offset(r & 127, k)) = v[k];
+            *reinterpret_cast<uint4*>(qd + (ch >> 3) * C::kSub + sw128_offset(rl + (b + k) * R, ch & 7)) = v[k];
         }
         fence_async_smem();
         __syncwarp();
@@ -399,16 +409,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint32_t v[32];
         // The first half's weights against the old reference, while the
-        // maximum is still being found; kept unless the reference must move.
-        weights(s, v, m == -CUDART_INF_F ? 0.f : m);
-        if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
+        // maximum is still being found; taken again if the reference moves.
+        for (;;) {
+          sum[0] = sum[1] = 0;
+          weights(s, v, m == -CUDART_INF_F ? 0.f : m);
+          if (!__any_sync(0xFFFFFFFFu, top > m + kGrow)) break;
           const float mn = top > m + kGrow ? top : m;
           if (kv != g.kv0) {
             // O_t is complete up to the previous unit: its MMAs were issued
             // before the scores that just arrived.
             const float f = m == mn ? 1.f : ex2(m - mn);
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
               tmem_ld32(to + 32 * k, v);
               tmem_ld_wait();
@@ -418,8 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           m = mn;
-          sum[0] = sum[1] = 0;
-          weights(s, v, m == -CUDART_INF_F ? 0.f : m);
         }
         give(v, 0);
         weights(s + 64, v, m == -CUDART_INF_F ? 0.f : m);
@@ -433,15 +443,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.o_done[t], no++ & 1, p));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
+        // Through this warp's part of the query tile, so that whole lines
+        // leave: row = lane in, 8 lanes of a row out.
+#pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           uint32_t v[32];
           tmem_ld32(to + 32 * k, v);
           tmem_ld_wait();
-          if (in)
+          uint8_t* st = qd + q * 4096;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(slot + (int64_t)r * D + 32 * k + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(st + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int rr = 4 * e + (lane >> 3), ro = t * kHalfRows + q * 32 + rr;
+            const uint4 x = *reinterpret_cast<const uint4*>(st + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (ro < g.rows) *reinterpret_cast<uint4*>(slot + (int64_t)ro * D + 32 * k + 4 * (lane & 7)) = x;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }

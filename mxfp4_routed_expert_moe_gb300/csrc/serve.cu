@@ -47,25 +47,32 @@ int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
   return t;
 }
 
-// Which kernel takes which part.  The warp kernel takes parts of few rows (a
-// tile of 16, 32 or 64), the Tensor Memory kernel the others.
-void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)[2]) {
+// Which kernel takes which part: the warp kernel takes parts of at most 16
+// rows per key head (one tile), the Tensor Memory kernel the others.
+void plan_sides(const moe_kv_batch& b, int group, AttnSide (&side)[2]) {
   memset(side, 0, sizeof side);
-  const int64_t own_rows = (int64_t)b.max_q * group, prefix_rows = (int64_t)b.tokens * group;
-  const bool own_tc = own_rows > 64, prefix_tc = b.prefix_len > 0 && (own_tc || prefix_rows > 16);
+  const bool own_tc = (int64_t)b.max_q * group > kAttnWarpRows, prefix = b.prefix_len > 0;
+  const bool prefix_tc = (int64_t)b.tokens * group > kAttnWarpRows;
   AttnSide &w = side[0], &t = side[1];
   w.own = !own_tc;
-  w.prefix = b.prefix_len > 0 && !prefix_tc;
-  w.rows = own_rows <= 16 ? 16 : own_rows <= 32 ? 32 : 64;
+  w.prefix = prefix && !prefix_tc;
+  w.rows = kAttnWarpRows;
   w.unit = kAttnWarpUnit;
   w.ctas = kAttnWarpCtas;
-  w.min_units = 2;
+  w.workers = kAttnWarpCtas * kAttnWarpWorkers;
+  w.min_units = 1;
+  w.tile_cost = 1;
   t.own = own_tc;
-  t.prefix = prefix_tc;
+  t.prefix = prefix && prefix_tc;
   t.rows = kAttnTcRows;
   t.unit = kAttnTcUnit;
-  t.ctas = kAttnTcCtas;
+  t.ctas = t.workers = kAttnTcCtas;
   t.min_units = 1;
+  t.tile_cost = 4;
+  for (AttnSide& s : side) {
+    while ((1 << s.rows_shift) < s.rows) ++s.rows_shift;
+    while ((1 << s.unit_shift) < s.unit) ++s.unit_shift;
+  }
 }
 
 size_t side_layout(const moe_kv_batch& b, int group, int kv_heads, int head_dim, AttnSide (&side)[2], void* base) {
@@ -78,9 +85,9 @@ size_t side_layout(const moe_kv_batch& b, int group, int kv_heads, int head_dim,
   for (int i = 0; i < 2; ++i) {
     AttnSide& s = side[i];
     if (!s.own && !s.prefix) continue;
-    const size_t slots = (size_t)s.ctas + (size_t)max_tiles(b, group, s) * kv_heads;
-    s.unit_start = (long long*)take((size_t)(b.batch + 3) * 8);
-    s.tile_start = (int32_t*)take((size_t)(b.batch + 3) * 4);
+    const size_t slots = (size_t)s.workers + (size_t)max_tiles(b, group, s) * kv_heads;
+    s.unit_start = (long long*)take((size_t)(b.batch + 2) * 8);
+    s.tile_start = (int32_t*)take((size_t)(b.batch + 1) * 4);
     s.slots = (float*)take(slots * s.rows * (head_dim + 2) * 4);
   }
   return off;
@@ -154,7 +161,7 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_bat
   if (check_cache(cache) != MOE_OK || check_batch(batch) != MOE_OK || check_heads(cache, q_heads) != MOE_OK) return 0;
   AttnSide side[2];
   const int group = q_heads / cache->kv_heads;
-  plan_sides(*batch, group, cache->head_dim, side);
+  plan_sides(*batch, group, side);
   return side_layout(*batch, group, cache->kv_heads, cache->head_dim, side, nullptr);
 }
 
@@ -171,7 +178,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   AttnParams p;
   memset(&p, 0, sizeof p);
   p.group = q_heads / cache->kv_heads;
-  plan_sides(*batch, p.group, cache->head_dim, p.side);
+  plan_sides(*batch, p.group, p.side);
   if (ws_bytes < side_layout(*batch, p.group, cache->kv_heads, cache->head_dim, p.side, ws)) return MOE_ERR_WORKSPACE;
   p.q = (const uint16_t*)q;
   p.out = (uint16_t*)out;

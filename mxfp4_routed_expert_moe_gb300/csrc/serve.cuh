@@ -76,17 +76,22 @@ cudaError_t launch_sample(const SampleParams& p, int dtype, cudaStream_t s);
 // all rows).  Rows of a set for one key head: (token, head of the group), in
 // tiles of `rows`; its tokens in units of `unit`.  The units of all sets, in
 // (set, key head, row tile, unit) order, are cut into equal contiguous ranges,
-// one per CTA; a CTA's piece of one tile is a segment.  Its partial sums go to
-// slot CTA + tile, which is unique because every step to the next segment
-// raises the CTA or the tile by one.
+// one per worker (a warp of the warp kernel, a CTA of the other); a worker's
+// piece of one tile is a segment.  Its partial sums go to slot worker + tile,
+// which is unique because every step to the next segment raises the worker or
+// the tile by one.  A tile counts tile_cost units more than its tokens have,
+// at its start: what loading its queries and storing its sums cost, so that
+// ranges of many short tiles take as long as ranges of few long ones.
 struct AttnSide {
   int own, prefix;       // which sets this kernel takes
-  int rows, unit;        // query rows of a tile, tokens of a unit
-  int ctas;              // CTAs launched
-  int min_units;         // least units of a CTA's range
-  float* slots;          // [ctas + tiles][rows * (head_dim + 2)]
-  long long* unit_start; // [batch + 2] first unit of each set, then the total; [batch + 2]: units per CTA
-  int32_t* tile_start;   // [batch + 2] first tile of each set
+  int rows, unit;        // query rows of a tile, tokens of a unit (powers of two)
+  int rows_shift, unit_shift;
+  int ctas, workers;     // CTAs launched, workers of all
+  int min_units;         // least units of a worker's range
+  int tile_cost;         // units that a tile counts beside its tokens'
+  float* slots;          // [workers + tiles][rows * (head_dim + 2)]
+  long long* unit_start; // [batch + 1] first unit of each set; [batch + 1]: units per worker
+  int32_t* tile_start;   // [batch + 1] first tile of each set
 };
 
 struct AttnParams {
@@ -103,6 +108,24 @@ struct AttnParams {
   long long wait_limit;
 };
 
+// What a set's entries say, as loaded.
+struct AttnRaw {
+  int q0, q1, len;
+};
+
+__device__ __forceinline__ AttnRaw attn_load(const AttnParams& p, int s) {
+  AttnRaw r;
+  r.q0 = 0;
+  r.q1 = p.b.tokens;
+  r.len = p.b.prefix_len;
+  if (s < p.b.batch) {
+    r.q0 = p.b.q_start ? __ldg(&p.b.q_start[s]) : s;
+    r.q1 = p.b.q_start ? __ldg(&p.b.q_start[s + 1]) : s + 1;
+    r.len = __ldg(&p.b.kv_len[s]);
+  }
+  return r;
+}
+
 // One set as an attention kernel sees it.
 struct AttnSet {
   int rows;      // query rows per key head
@@ -110,44 +133,33 @@ struct AttnSet {
   int len;       // tokens of the set
   int first_vis; // tokens the first query token sees (each later one sees one more); len for the prefix
   int tiles;     // row tiles per key head
-  int units;     // units per row tile
-  const int32_t* table;
+  int units;     // units per row tile, with the tile's own cost
 };
 
-__device__ __forceinline__ AttnSet attn_set(const AttnParams& p, const AttnSide& sd, int s) {
+__device__ __forceinline__ AttnSet attn_set(const AttnParams& p, const AttnSide& sd, int s, const AttnRaw& r) {
   AttnSet a;
   a.rows = a.tok0 = a.len = a.first_vis = a.tiles = a.units = 0;
-  a.table = nullptr;
-  int ql;
-  if (s == p.b.batch) {
-    if (!sd.prefix) return a;
-    ql = p.b.tokens;
-    a.len = a.first_vis = p.b.prefix_len;
-    a.table = p.b.prefix_table;
-  } else {
-    if (!sd.own) return a;
-    int q0 = s, q1 = s + 1;
-    if (p.b.q_start) {
-      q0 = __ldg(&p.b.q_start[s]);
-      q1 = __ldg(&p.b.q_start[s + 1]);
-    }
-    const int len = __ldg(&p.b.kv_len[s]);
-    if (q0 < 0 || q1 < q0 || q1 > p.b.tokens || q1 - q0 > p.b.max_q || len < 0 ||
-        len > (long long)p.b.table_pages * p.page_size) {
-      set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
-      return a;
-    }
-    ql = q1 - q0;
-    a.tok0 = q0;
-    a.len = len;
-    a.first_vis = len - ql + 1;
-    a.table = p.b.table + (int64_t)s * p.b.table_stride;
+  const bool prefix = s == p.b.batch;
+  if (!(prefix ? sd.prefix : sd.own)) return a;
+  const int ql = r.q1 - r.q0;
+  if (!prefix && (r.q0 < 0 || ql < 0 || r.q1 > p.b.tokens || ql > p.b.max_q || r.len < 0 ||
+                  r.len > (long long)p.b.table_pages * p.page_size)) {
+    set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
+    return a;
   }
-  if (ql == 0 || a.len == 0) return a;
+  if (ql == 0 || r.len == 0) return a;
+  a.tok0 = r.q0;
+  a.len = r.len;
+  a.first_vis = prefix ? r.len : r.len - ql + 1;
   a.rows = ql * p.group;
-  a.tiles = (a.rows + sd.rows - 1) / sd.rows;
-  a.units = (a.len + sd.unit - 1) / sd.unit;
+  a.tiles = (a.rows + sd.rows - 1) >> sd.rows_shift;
+  a.units = ((a.len + sd.unit - 1) >> sd.unit_shift) + sd.tile_cost;
   return a;
+}
+
+// The page table of set s.
+__device__ __forceinline__ const int32_t* attn_table(const AttnParams& p, int s) {
+  return s == p.b.batch ? p.b.prefix_table : p.b.table + (int64_t)s * p.b.table_stride;
 }
 
 // Tokens that query token i (of the set's tokens) sees, in [0, len].
@@ -163,27 +175,34 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// A CTA's walk over its range of units.
+// A worker's walk over its range of units.  The entries of the next set are
+// loaded one set ahead, so that stepping to it waits for no memory.
 struct AttnWalk {
   int set;
   AttnSet a;
-  long long unit0;  // first unit of the set
-  int tile0;        // first tile of the set
-  long long u, u1;  // next unit, end of the range
+  AttnRaw next;
+  long long unit0;   // first unit of the set
+  int tile0;         // first tile of the set
+  int worker;
+  long long u, u1;   // next unit, end of the range
 };
 
+template <int W>
 struct AttnPlanShared {
   long long part_u[32];
   int part_t[32];
-  long long total;
-  int set, tile0;
-  long long unit0;
+  long long unit0[W];
+  int set[W], tile0[W];
 };
 
-// All threads of the CTA: add up the sets' units, cut them into gridDim.x
-// ranges and find where this CTA's begins.  CTA 0 writes the plan for the
-// joining kernel.  False (CTA-uniform): nothing to do.
-__device__ __forceinline__ bool attn_plan(const AttnParams& p, const AttnSide& sd, AttnPlanShared& sh, AttnWalk& w) {
+// All threads of the CTA: add up the sets' units, cut them into ranges for
+// W * gridDim.x workers (worker w of CTA c is number w * gridDim.x + c, so
+// that few units spread over the SMs) and find where the ranges of this CTA's
+// workers begin.  CTA 0 writes the plan for the joining kernel.  Returns the
+// units per worker.
+template <int W>
+__device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSide& sd, AttnPlanShared<W>& sh,
+                                               long long& total) {
   const int nsets = p.b.batch + 1, nt = blockDim.x, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
   const int per_thread = (nsets + nt - 1) / nt;
@@ -192,7 +211,7 @@ __device__ __forceinline__ bool attn_plan(const AttnParams& p, const AttnSide& s
   long long u = 0;
   int t = 0;
   for (int s = s0; s < s1; ++s) {
-    const AttnSet a = attn_set(p, sd, s);
+    const AttnSet a = attn_set(p, sd, s, attn_load(p, s));
     const int tiles = a.tiles * p.kv_heads;
     u += (long long)tiles * a.units;
     t += tiles;
@@ -213,86 +232,126 @@ __device__ __forceinline__ bool attn_plan(const AttnParams& p, const AttnSide& s
     sh.part_t[warp] = et;
   }
   __syncthreads();
-  long long total = 0, bu = 0;
-  int bt = 0;
+  total = 0;
+  eu -= u;  // exclusive
+  et -= t;
   for (int i = 0; i < nwarps; ++i) {
-    if (i == warp) {
-      bu = total;
+    const long long x = sh.part_u[i];
+    if (i < warp) {
+      eu += x;
+      et += sh.part_t[i];
     }
-    total += sh.part_u[i];
+    total += x;
   }
-  for (int i = 0; i < warp; ++i) bt += sh.part_t[i];
-  eu += bu - u;  // exclusive
-  et += bt - t;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long workers = (long long)W * gridDim.x;
+  long long per;
+  if (total < 0x7FFFFFFFll)
+    per = ((uint32_t)total + (uint32_t)workers - 1) / (uint32_t)workers;
+  else
+    per = (total + workers - 1) / workers;
   if (per < sd.min_units) per = sd.min_units;
-  const long long u0 = (long long)blockIdx.x * per;
-  long long su = eu;
-  int stl = et;
-  const bool mine = u0 >= eu && u0 < eu + u;
-  if (mine || blockIdx.x == 0) {
+  bool mine = blockIdx.x == 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const long long u0 = ((long long)w * gridDim.x + blockIdx.x) * per;
+    mine |= u0 >= eu && u0 < eu + u;
+  }
+  if (mine) {
+    long long su = eu;
+    int st = et;
     for (int s = s0; s < s1; ++s) {
-      const AttnSet a = attn_set(p, sd, s);
+      const AttnSet a = attn_set(p, sd, s, attn_load(p, s));
       const int tiles = a.tiles * p.kv_heads;
       const long long n = (long long)tiles * a.units;
-      if (u0 >= su && u0 < su + n) {
-        sh.set = s;
-        sh.unit0 = su;
-        sh.tile0 = stl;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const long long u0 = ((long long)w * gridDim.x + blockIdx.x) * per;
+        if (u0 >= su && u0 < su + n) {
+          sh.set[w] = s;
+          sh.unit0[w] = su;
+          sh.tile0[w] = st;
+        }
       }
       if (blockIdx.x == 0) {
         sd.unit_start[s] = su;
-        sd.tile_start[s] = stl;
+        sd.tile_start[s] = st;
       }
       su += n;
-      stl += tiles;
+      st += tiles;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    sd.unit_start[nsets] = total;
-    sd.unit_start[nsets + 1] = per;
-  }
+  if (blockIdx.x == 0 && tid == 0) sd.unit_start[nsets] = per;
   __syncthreads();
-  if (u0 >= total) return false;
-  w.set = sh.set;
-  w.unit0 = sh.unit0;
-  w.tile0 = sh.tile0;
-  w.a = attn_set(p, sd, w.set);
-  w.u = u0;
-  w.u1 = u0 + per < total ? u0 + per : total;
+  return per;
+}
+
+// The walk of this CTA's worker w; false: nothing to do.
+template <int W>
+__device__ __forceinline__ bool attn_begin(const AttnParams& p, const AttnSide& sd, const AttnPlanShared<W>& sh, int w,
+                                           long long per, long long total, AttnWalk& k) {
+  k.worker = w * gridDim.x + blockIdx.x;
+  k.u = k.worker * per;
+  if (k.u >= total) return false;
+  k.u1 = k.u + per < total ? k.u + per : total;
+  k.set = sh.set[w];
+  k.unit0 = sh.unit0[w];
+  k.tile0 = sh.tile0[w];
+  k.a = attn_set(p, sd, k.set, attn_load(p, k.set));
+  k.next = attn_load(p, k.set < p.b.batch ? k.set + 1 : k.set);
   return true;
 }
 
 // The next segment of the walk.
 struct AttnSeg {
+  int set, tok0, first_vis, len;  // the set
   int slot, kvh;
   int row0;      // first row of the tile in its set
   int rows;      // rows of the tile
   int kv0, kv1;  // token range [kv0, kv1) of the set, cut to what the tile's last row sees (may be empty)
 };
 
+__device__ __forceinline__ int attn_visible(const AttnParams& p, const AttnSeg& g, int i) {
+  if (g.set == p.b.batch) return g.len;
+  const int v = g.first_vis + i;
+  return v < 0 ? 0 : (v > g.len ? g.len : v);
+}
+
 __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnSide& sd, AttnWalk& w, AttnSeg& g) {
   if (w.u >= w.u1) return false;
-  long long set_units = (long long)w.a.tiles * p.kv_heads * w.a.units;
-  while (w.u >= w.unit0 + set_units) {
-    w.unit0 += set_units;
-    w.tile0 += w.a.tiles * p.kv_heads;
-    w.a = attn_set(p, sd, ++w.set);
-    set_units = (long long)w.a.tiles * p.kv_heads * w.a.units;
+  int tiles = w.a.tiles * p.kv_heads;
+  while (w.u >= w.unit0 + (long long)tiles * w.a.units) {
+    w.unit0 += (long long)tiles * w.a.units;
+    w.tile0 += tiles;
+    ++w.set;
+    w.a = attn_set(p, sd, w.set, w.next);
+    w.next = attn_load(p, w.set < p.b.batch ? w.set + 1 : w.set);
+    tiles = w.a.tiles * p.kv_heads;
   }
   const long long lu = w.u - w.unit0;
-  const int tile = (int)(lu / w.a.units);
-  const int k0 = (int)(lu - (long long)tile * w.a.units);
+  int tile, k0;
+  if (lu < 0x7FFFFFFFll) {
+    tile = (int)((uint32_t)lu / (uint32_t)w.a.units);
+    k0 = (int)((uint32_t)lu - (uint32_t)tile * (uint32_t)w.a.units);
+  } else {
+    tile = (int)(lu / w.a.units);
+    k0 = (int)(lu - (long long)tile * w.a.units);
+  }
   long long n = w.a.units - k0;
   if (n > w.u1 - w.u) n = w.u1 - w.u;
   w.u += n;
-  g.slot = (int)blockIdx.x + w.tile0 + tile;
+  g.set = w.set;
+  g.tok0 = w.a.tok0;
+  g.first_vis = w.a.first_vis;
+  g.len = w.a.len;
+  g.slot = w.worker + w.tile0 + tile;
   g.kvh = tile / w.a.tiles;
-  g.row0 = (tile % w.a.tiles) * sd.rows;
+  g.row0 = (tile - g.kvh * w.a.tiles) * sd.rows;
   g.rows = w.a.rows - g.row0 < sd.rows ? w.a.rows - g.row0 : sd.rows;
-  const int vis = attn_visible(p, w.a, w.set, (g.row0 + g.rows - 1) / p.group);
-  g.kv0 = k0 * sd.unit;
-  const long long e = (long long)(k0 + n) * sd.unit;
+  const int vis = attn_visible(p, g, (g.row0 + g.rows - 1) / p.group);
+  const int r0 = k0 > sd.tile_cost ? k0 - sd.tile_cost : 0;
+  const long long r1 = k0 + n > sd.tile_cost ? k0 + n - sd.tile_cost : 0;
+  g.kv0 = r0 << sd.unit_shift;
+  const long long e = r1 << sd.unit_shift;
   g.kv1 = e < vis ? (int)e : vis;
   if (g.kv1 < g.kv0) g.kv1 = g.kv0;
   return true;
@@ -304,9 +363,12 @@ __host__ __device__ __forceinline__ int attn_box(int page_size, int unit) { retu
 cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
-// CTAs of the warp kernel (two per SM).
-constexpr int kAttnWarpCtas = 2 * kNumSMs;
-constexpr int kAttnWarpUnit = 64;
+// The warp kernel: one CTA per SM, six workers in each, tiles of 16 rows,
+// units of 32 tokens.
+constexpr int kAttnWarpCtas = kNumSMs;
+constexpr int kAttnWarpWorkers = 6;
+constexpr int kAttnWarpRows = 16;
+constexpr int kAttnWarpUnit = 32;
 // The Tensor Memory kernel: one CTA per SM, tiles of 256 rows, units of 128 tokens.
 constexpr int kAttnTcCtas = kNumSMs;
 constexpr int kAttnTcRows = 256;
