@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
   const int box = attn_box(p.page_size, kUnit);
   const int my_box = lane >> 2, my_half = (lane >> 1) & 1, my_v = lane & 1;
   const bool my_lane = my_half < D / 64 && my_box * box < kUnit;
-  AttnSeg lg;
+  AttnSeg lg = {};
   int lkv = 0, lpage = 0;
   bool lready = false, lmore = true;         // a unit to load is known; there may be more segments
   uint32_t ln = 0, seg_in = 0, seg_out = 0;  // units loaded; segments passed on, taken
@@ -351,6 +351,22 @@ __device__ __forceinline__ JoinRow join_row(const AttnParams& p, const JoinPart&
   return j;
 }
 
+// The joined row, divided and rounded once, and its logarithm of the sum.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams& p, int n, int head, int lane, const float (&acc)[D / 32],
+                                          float l, float mx) {
+  constexpr int E = D / 32;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  uint16_t* dst = p.out + (int64_t)n * p.out_stride + head * D + lane * E;
+  if (E == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[E - 2] * inv, acc[E - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(int64_t)n * p.q_heads + head] = l == 0.f ? -CUDART_INF_F : (mx + log2f(l)) * 0.69314718055994531f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p) {
   __shared__ JoinPart sh_part[2];
@@ -387,7 +403,79 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
     if (lane == 0) sh_part[warp] = t;
   }
   __syncthreads();
-  for (int head = blockIdx.y * kJoinWarps + warp; head < p.q_heads; head += gridDim.y * kJoinWarps) {
+  constexpr int E = D / 32;
+  const int step = gridDim.y * kJoinWarps;
+  const int head0 = blockIdx.y * kJoinWarps + warp;
+  // Four heads at a time while each has at most 8 segments: lane 8 h + s looks
+  // after segment s of head h, and the loads of the four overlap.
+  int done = head0;  // first head of this warp that is still to do
+  for (; done < p.q_heads; done += 4 * step) {
+    const int head = done + (lane >> 3) * step, s = lane & 7;
+    JoinRow a, b;
+    a.n = b.n = 0;
+    int64_t fa = 0, fb = 0;
+    int rows = 0;
+    const float *src = nullptr, *ms = nullptr;
+    if (head < p.q_heads) {
+      fa = (int64_t)(D + 2) << sh_part[0].rows_shift;
+      fb = (int64_t)(D + 2) << sh_part[1].rows_shift;
+      a = join_row(p, sh_part[0], head, fa);
+      b = join_row(p, sh_part[1], head, fb);
+      if (s < a.n) {
+        src = a.first + s * fa;
+        ms = a.m + s * fa;
+        rows = 1 << sh_part[0].rows_shift;
+      } else if (s < a.n + b.n) {
+        src = b.first + (s - a.n) * fb;
+        ms = b.m + (s - a.n) * fb;
+        rows = 1 << sh_part[1].rows_shift;
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, a.n + b.n > 8)) break;
+    float m = -CUDART_INF_F, l = 0.f;
+    if (ms) {
+      m = *ms;
+      l = ms[rows];
+    }
+    float mx = m;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    const float f = m == -CUDART_INF_F ? 0.f : ex2(m - mx);
+    l *= f;  // a NaN sum stays one
+    // In segment order: the same order whichever way a row is joined.
+    float lt = 0.f;
+    float acc[4][E] = {};
+    const int most = __reduce_max_sync(0xFFFFFFFFu, a.n + b.n);
+    for (int k = 0; k < most; ++k) {
+      lt += __shfl_sync(0xFFFFFFFFu, l, (lane & 24) + k);
+      float v[4][E], fs[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        fs[h] = __shfl_sync(0xFFFFFFFFu, f, 8 * h + k);
+        const float* row = (const float*)__shfl_sync(0xFFFFFFFFu, (unsigned long long)src, 8 * h + k);
+        if (fs[h] > 0.f) {
+          if (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(row + lane * E);
+            v[h][0] = x.x, v[h][1] = x.y, v[h][E - 2] = x.z, v[h][E - 1] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(row + lane * E);
+            v[h][0] = x.x, v[h][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[h][e] = fs[h] > 0.f ? fmaf(fs[h], v[h][e], acc[h][e]) : acc[h][e];
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int hd = done + h * step;
+      if (hd >= p.q_heads) break;
+      store_row<D>(p, n, hd, lane, acc[h], __shfl_sync(0xFFFFFFFFu, lt, 8 * h), __shfl_sync(0xFFFFFFFFu, mx, 8 * h));
+    }
+  }
+  for (int head = done; head < p.q_heads; head += step) {
     JoinRow part[2];
     int64_t sf[2];
     int rows[2];
@@ -404,7 +492,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
       for (int s = lane; s < part[k].n; s += 32) mx = fmaxf(mx, part[k].m[s * sf[k]]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    constexpr int E = D / 32;
     float acc[E] = {}, l = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -436,15 +523,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
         }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint16_t* dst = p.out + (int64_t)n * p.out_stride + head * D + lane * E;
-    if (E == 4)
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[E - 2] * inv, acc[E - 1] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)n * p.q_heads + head] = l == 0.f ? -CUDART_INF_F : (mx + log2f(l)) * 0.69314718055994531f;
+    store_row<D>(p, n, head, lane, acc, l, mx);
   }
 }
 
