@@ -10,13 +10,20 @@
 // and the drawn token is found by a running sum in index order.
 //
 // A cluster of 1 to 8 CTAs takes a row; its scores are read from HBM once and
-// stay in shared memory.  K* comes from histograms (count and sum of W per
-// bin) that the CTAs of the cluster add up over distributed shared memory: the
-// first by m - z in 1,024 equal bins (a monotone function of z), then, only
-// if the bin that holds the bound has more than kList tokens, by 10 bits of K
-// at a time; a bin of at most kList tokens is ranked directly.
-// Bound by latency (a handful of cluster barriers) for few rows, by the passes
-// over shared memory and HBM for many.
+// stay in shared memory.  K* comes from histograms (count or sum of W per bin)
+// that the CTAs of the cluster add up over distributed shared memory: the
+// first by m - z in 1,024 equal bins (a monotone function of z); if the bin
+// that holds the bound has more than kList tokens, the next by 1,024 equal
+// parts of that bin; if one part still has more (ties), by 10 bits of K at a
+// time.  A bin of at most kList tokens is ranked directly.  Top-k is searched
+// first, by counts alone (no exponentials); what it drops, later passes skip.
+// When all tokens down to the end of the first bin found number at most kList
+// (small top-k, peaked rows), every CTA gets them all and finishes alone.
+// Bound by latency (cluster barriers of 0.8 us) for few rows, by the
+// instructions of the passes and the barriers for many: shared memory holds
+// some 38 rows of 128,000 scores on the chip at a time.  Reading the scores
+// again from L2 for each pass instead, with more CTAs resident, was slower
+// (512 rows of 128,000: 391 against 377 us; 64 rows: 74 against 64 us).
 #include <cooperative_groups.h>
 
 #include "serve.cuh"
@@ -29,39 +36,40 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 1024;
+constexpr int kList = 256;
 constexpr int kIdxBits = 18;             // MOE_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCl = 8;
+constexpr int kMostScores = 32768;       // of a CTA
 constexpr float kFix = 2147483648.f;     // 2^31
 constexpr float kBinScale = 46.f;        // W > 0 needs m - z < 22.2: bins 0 .. 1021
+constexpr float kCut = 22.25f;           // below m - kCut every W is 0, ...
+constexpr float kSure = 22.f;            // ... down to m - kSure none is (exp(-22) 2^31 = 0.599)
 constexpr unsigned long long kKeyAll = ~0ull;
 
 struct SampleShared {
-  // Histogram of this CTA (count, low and high 16 bits of W: native 32-bit
-  // shared-memory atomics; at most 2^15 tokens a CTA keep all three below
-  // 2^31), and, once the cluster has added them up, the list of one bin.
-  union {
-    struct {
-      uint32_t cnt[kBins], lo[kBins], hi[kBins];
-    } h;
-    struct {
-      unsigned long long key[kList];
-      uint32_t w[kList];
-    } list;
-  };
+  // Histogram of this CTA: count, low and high 16 bits of W (native 32-bit
+  // shared-memory atomics; at most kMostScores tokens a CTA keep all three
+  // within 32 bits, even if they share a bin).
+  uint32_t cnt[kBins], lo[kBins], hi[kBins];
   unsigned long long tsum[kBins];  // the cluster's totals
   uint32_t tcnt[kBins];
+  // The tokens of one bin of the cluster: one list for each search of a row.
+  struct {
+    unsigned long long key[kList];
+    uint32_t w[kList];
+  } list[2];
+  uint32_t list_n[2];  // rank 0's are the cluster's
   unsigned long long warp_best[kWarps];
   unsigned long long warp_sum[kWarps];
   uint32_t warp_cnt[kWarps];
   unsigned long long cl_best[kMaxCl];
   unsigned long long cl_sum[kMaxCl];
   uint32_t cl_cnt[kMaxCl];
-  uint32_t list_n;  // rank 0's is the cluster's
   // Where a search ended.
   uint32_t f_bin, f_cnt, f_before_cnt;
-  unsigned long long f_before_sum, f_key, f_sum;
+  unsigned long long f_before_sum, f_key;
 };
+static_assert(MOE_SAMPLE_MAX_VOCAB <= kMostScores * kMaxCl, "a cluster takes the longest row");
 static_assert(MOE_SAMPLE_MAX_VOCAB == 1 << kIdxBits, "index bits of the key");
 
 // Order-preserving bits of a float (ascending), -0 excluded.
@@ -75,25 +83,38 @@ __device__ __forceinline__ unsigned long long rank_key(float z, uint32_t idx) {
 
 struct Row {
   float m;       // largest scaled score
-  bool inf;      // m = +inf
+  float least;   // scores below have W = 0 or rank past K*
   float min_p;   // 0: off
+  bool inf;      // m = +inf
   unsigned long long key_max;  // K*
 
   // exp(z - m).  expf, not an approximation: the weights are part of the
   // definition, and the same function gives the same integers everywhere.
   __device__ __forceinline__ float w(float z) const { return inf ? (z == m ? 1.f : 0.f) : expf(z - m); }
   __device__ __forceinline__ static uint32_t fixed(float w) { return __float2uint_rn(w * kFix); }
-  __device__ __forceinline__ int bin(float z) const {
-    if (inf) return 0;
-    const int b = (int)((m - z) * kBinScale);
-    return b < kBins - 1 ? b : kBins - 1;
+  // Place of z on the axis of bins, and its bin and part of that bin: each
+  // step is monotone in z (the subtraction of the bin is exact).
+  __device__ __forceinline__ float place(float z) const { return inf ? 0.f : fminf((m - z) * kBinScale, (float)(kBins - 1)); }
+  __device__ __forceinline__ int bin(float z) const { return (int)place(z); }
+  __device__ __forceinline__ int part(float z) const {
+    const float t = place(z);
+    return (int)((t - (float)(int)t) * (float)kBins);
+  }
+  // Not dropped by the bound found so far (for z >= least).
+  __device__ __forceinline__ bool within(float z, uint32_t idx) const {
+    return key_max == kKeyAll || rank_key(z, idx) <= key_max;
+  }
+  __device__ __forceinline__ void set_max(unsigned long long key) {
+    key_max = key;
+    const uint32_t o = ~(uint32_t)(key >> kIdxBits);
+    least = fmaxf(least, __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o));
   }
   // Weight of a kept token, 0 for the others.
   __device__ __forceinline__ uint32_t kept(float z, uint32_t idx) const {
+    if (!(z >= least)) return 0u;
     const float e = w(z);
     if (min_p > 0.f && !(e >= min_p)) return 0u;
-    if (key_max != kKeyAll && rank_key(z, idx) > key_max) return 0u;
-    return fixed(e);
+    return within(z, idx) ? fixed(e) : 0u;
   }
 };
 
@@ -120,86 +141,113 @@ struct Target {
   }
 };
 
-// Tokens of the CTA that match the search so far: bin b0 of the first
-// histogram (-1: all), and the key's upper bits.
+// Tokens that match the search so far: level -1 those down to bin b0, 0 all, 1 those of bin b0, 2 of
+// its part b1, above that those whose key starts with `prefix` (shift bits
+// follow) among them.
 struct Match {
-  int b0;
-  int shift;                  // bits below the ones fixed so far
-  unsigned long long prefix;  // key >> shift of the fixed bits
+  int level, b0, b1, shift;
+  unsigned long long prefix;
 };
 
+__device__ __forceinline__ float scaled(float x, float inv) {
+  const float v = fmaf(x, inv, 0.f);  // + 0: no negative zeros
+  return v != v ? -CUDART_INF_F : v;
+}
 class Sampler {
  public:
   SampleShared& sh;
-  const float* z;  // this CTA's scaled scores
-  int n;           // how many
-  uint32_t first;  // index of the first in the row
+  const float4* z4;  // this CTA's scaled scores in groups of four, -inf around them
+  int n4;
+  uint32_t first;  // index in the row of the first entry
   int cl, rank;
   Row row;
   cg::cluster_group cluster;
 
-  __device__ Sampler(SampleShared& s, const float* zs, int n_, uint32_t f)
-      : sh(s), z(zs), n(n_), first(f), cluster(cg::this_cluster()) {
+  __device__ Sampler(SampleShared& s, const float4* scores, int n, uint32_t f)
+      : sh(s), z4(scores), n4((n + 3) / 4), first(f), cluster(cg::this_cluster()) {
     cl = (int)cluster.num_blocks();
     rank = (int)cluster.block_rank();
   }
 
-  template <typename T>
-  __device__ __forceinline__ T* remote(T* p, int r) {
+  template <typename U>
+  __device__ __forceinline__ U* remote(U* p, int r) {
     return cluster.map_shared_rank(p, r);
   }
 
-  __device__ __forceinline__ bool matches(const Match& mt, float zi, uint32_t idx) const {
-    if (mt.b0 >= 0 && row.bin(zi) != mt.b0) return false;
-    return (rank_key(zi, idx) >> mt.shift) == mt.prefix;
+  // f(score, index) for the CTA's scores that can have a weight, eight per
+  // thread and step.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const float kNone = -CUDART_INF_F;
+    for (int v = threadIdx.x; v < n4; v += 2 * kThreads) {
+      const float4 a = z4[v];
+      const float4 b = v + kThreads < n4 ? z4[v + kThreads] : make_float4(kNone, kNone, kNone, kNone);
+      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (x[e] >= row.least) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
+    }
   }
 
-  // Histogram of the matching tokens over the cluster into tcnt / tsum: by
-  // m - z (mt.b0 < 0), else by the 10 key bits below mt.shift.
-  __device__ void histogram(const Match& mt) {
+  __device__ __forceinline__ bool matches(const Match& mt, float zi, uint32_t idx) const {
+    if (!row.within(zi, idx)) return false;
+    if (mt.level == 0) return true;
+    if (mt.level < 0) return row.bin(zi) <= mt.b0;
+    if (row.bin(zi) != mt.b0) return false;
+    if (mt.level == 1) return true;
+    if (row.part(zi) != mt.b1) return false;
+    return mt.level == 2 || (rank_key(zi, idx) >> mt.shift) == mt.prefix;
+  }
+
+  // Histogram of the matching tokens over the cluster into tcnt / tsum, by
+  // the next level's bins; of counts alone where no sums are needed.
+  __device__ void histogram(const Match& mt, bool sums) {
     const int tid = threadIdx.x;
-    for (int b = tid; b < kBins; b += kThreads) sh.h.cnt[b] = sh.h.lo[b] = sh.h.hi[b] = 0u;
+    for (int b = tid; b < kBins; b += kThreads) sh.cnt[b] = sh.lo[b] = sh.hi[b] = 0u;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float zi = z[i];
-      const uint32_t w = Row::fixed(row.w(zi));
-      if (w == 0u) continue;
-      int b;
-      if (mt.b0 < 0) {
-        b = row.bin(zi);
-      } else {
-        if (!matches(mt, zi, first + i)) continue;
-        b = (int)(rank_key(zi, first + i) >> (mt.shift - 10)) & (kBins - 1);
+    each([&](float zi, uint32_t idx) {
+      uint32_t w = 1u;
+      if (sums || zi < row.m - kSure) w = Row::fixed(row.w(zi));
+      if (w == 0u || !matches(mt, zi, idx)) return;
+      const int b = mt.level == 0   ? row.bin(zi)
+                    : mt.level == 1 ? row.part(zi)
+                                    : (int)(rank_key(zi, idx) >> (mt.shift - 10)) & (kBins - 1);
+      atomicAdd(&sh.cnt[b], 1u);
+      if (sums) {
+        atomicAdd(&sh.lo[b], w & 0xFFFFu);
+        atomicAdd(&sh.hi[b], w >> 16);
       }
-      atomicAdd(&sh.h.cnt[b], 1u);
-      atomicAdd(&sh.h.lo[b], w & 0xFFFFu);
-      atomicAdd(&sh.h.hi[b], w >> 16);
-    }
+    });
     cluster.sync();
     // Each CTA adds up its share of the bins and gives every CTA the totals.
     const int share = kBins / cl;
     for (int b = rank * share + tid; b < (rank + 1) * share; b += kThreads) {
       uint32_t c = 0;
       unsigned long long s = 0;
-      for (int r = 0; r < cl; ++r) {
-        const SampleShared* o = remote(&sh, r);
-        c += o->h.cnt[b];
-        s += o->h.lo[b] + ((unsigned long long)o->h.hi[b] << 16);
+#pragma unroll
+      for (int r = 0; r < kMaxCl; ++r) {
+        if (r < cl) {
+          const SampleShared* o = remote(&sh, r);
+          c += o->cnt[b];
+          if (sums) s += o->lo[b] + ((unsigned long long)o->hi[b] << 16);
+        }
       }
-      for (int r = 0; r < cl; ++r) {
-        SampleShared* o = remote(&sh, r);
-        o->tcnt[b] = c;
-        o->tsum[b] = s;
+#pragma unroll
+      for (int r = 0; r < kMaxCl; ++r) {
+        if (r < cl) {
+          SampleShared* o = remote(&sh, r);
+          o->tcnt[b] = c;
+          o->tsum[b] = s;
+        }
       }
     }
-    if (tid == 0 && rank == 0) sh.list_n = 0;
     cluster.sync();
   }
 
   // The bin that holds the target, given what ranks before this histogram;
-  // false (uniform): there is none.  Also returns the histogram's totals.
-  __device__ bool find_bin(const Target& tg, uint32_t before_cnt, unsigned long long before_sum, uint32_t& all_cnt,
-                           unsigned long long& all_sum) {
+  // false (uniform): there is none.  A target by sum with `of_all` set has its
+  // bound set to bound * the histogram's total first.
+  __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, bool of_all) {
     constexpr int P = kBins / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t c = 0;
@@ -220,15 +268,16 @@ class Sampler {
     if (lane == 31) sh.warp_cnt[warp] = ic, sh.warp_sum[warp] = is;
     if (tid == 0) sh.f_bin = kBins;
     __syncthreads();
-    all_cnt = 0;
-    all_sum = 0;
+    unsigned long long all_sum = 0;
     uint32_t bc = before_cnt;
     unsigned long long bs = before_sum;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) bc += sh.warp_cnt[i], bs += sh.warp_sum[i];
-      all_cnt += sh.warp_cnt[i];
-      all_sum += sh.warp_sum[i];
+      const unsigned long long x = sh.warp_sum[i];
+      if (i < warp) bc += sh.warp_cnt[i], bs += x;
+      all_sum += x;
     }
+    if (of_all) tg.bound *= (double)all_sum;
     bc += ic - c;
     bs += is - s;
 #pragma unroll
@@ -248,63 +297,145 @@ class Sampler {
     return sh.f_bin < kBins;
   }
 
-  // After find_bin on the first histogram: the key of the target and the sum
-  // of W up to and including it.  `fresh` becomes false if the first
-  // histogram's totals were overwritten.
-  __device__ void resolve(const Target& tg, unsigned long long& key, unsigned long long& sum, bool& fresh) {
+  // Hand every CTA the list of the matching tokens (in any order).
+  __device__ void gather(const Match& mt, int which) {
+    uint32_t* cursor = remote(&sh.list_n[which], 0);
+    each([&](float zi, uint32_t idx) {
+      if (!matches(mt, zi, idx)) return;
+      const uint32_t w = Row::fixed(row.w(zi));
+      if (w == 0u) return;
+      const uint32_t at = atomicAdd(cursor, 1u);
+      const unsigned long long k = rank_key(zi, idx);
+      if (at < kList)
+        for (int r = 0; r < cl; ++r) {
+          SampleShared* o = remote(&sh, r);
+          o->list[which].key[at] = k;
+          o->list[which].w[at] = w;
+        }
+    });
+    cluster.sync();
+  }
+
+  // After find_bin on the first histogram: the key of the target.  `which`:
+  // the list to use, one for each search, so that no CTA fills a list that
+  // another still reads.
+  __device__ unsigned long long resolve(Target& tg, int which, bool sums) {
     Match mt;
+    mt.level = 1;
     mt.b0 = (int)sh.f_bin;
+    mt.b1 = 0;
     mt.shift = 50;
     mt.prefix = 0;
     uint32_t before_cnt = sh.f_before_cnt;
     unsigned long long before_sum = sh.f_before_sum;
     while (sh.f_cnt > kList) {  // uniform: every CTA of the cluster has the same totals
       __syncthreads();
-      fresh = false;
-      histogram(mt);
-      uint32_t ac;
-      unsigned long long as;
-      find_bin(tg, before_cnt, before_sum, ac, as);
-      mt.shift -= 10;
-      mt.prefix = (mt.prefix << 10) | sh.f_bin;
+      histogram(mt, sums);
+      find_bin(tg, before_cnt, before_sum, false);
+      if (mt.level == 1) {
+        mt.b1 = (int)sh.f_bin;
+      } else {
+        mt.shift -= 10;
+        mt.prefix = (mt.prefix << 10) | sh.f_bin;
+      }
+      ++mt.level;
       before_cnt = sh.f_before_cnt;
       before_sum = sh.f_before_sum;
     }
-    // Every CTA gets the list of the bin's tokens (in any order).
-    uint32_t* cursor = remote(&sh.list_n, 0);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float zi = z[i];
-      if (!matches(mt, zi, first + i)) continue;
-      const uint32_t w = Row::fixed(row.w(zi));
-      if (w == 0u) continue;
-      const uint32_t at = atomicAdd(cursor, 1u);
-      const unsigned long long k = rank_key(zi, first + i);
-      if (at < kList)
-        for (int r = 0; r < cl; ++r) {
-          SampleShared* o = remote(&sh, r);
-          o->list.key[at] = k;
-          o->list.w[at] = w;
-        }
-    }
-    cluster.sync();
+    gather(mt, which);
     const int cnt = (int)sh.f_cnt;
-    for (int i = threadIdx.x; i < cnt; i += kThreads) {
-      const unsigned long long k = sh.list.key[i];
+    const auto& list = sh.list[which];
+    static_assert(kList <= kThreads, "one token of the list per thread");
+    if ((int)threadIdx.x < cnt) {
+      const unsigned long long k = list.key[threadIdx.x];
       uint32_t c = before_cnt;
       unsigned long long s = before_sum;
-      for (int j = 0; j < cnt; ++j)
-        if (sh.list.key[j] < k) ++c, s += sh.list.w[j];
-      if (tg.holds(c, 1u, s, sh.list.w[i])) {
-        sh.f_key = k;
-        sh.f_sum = s + sh.list.w[i];
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        const bool better = list.key[j] < k;
+        c += better;
+        s += better ? list.w[j] : 0u;
+      }
+      const uint32_t w = list.w[threadIdx.x];
+      if (tg.holds(c, 1u, s, w)) sh.f_key = k;
+    }
+    __syncthreads();
+    return sh.f_key;
+  }
+
+  // All candidates are the cnt <= kList tokens of list `which`: apply the
+  // filters and draw, in every CTA alike (no cluster barrier).  Returns the
+  // total and the number kept; `mine` tells the thread whose token was drawn.
+  // The filters are top-k (k > 0), then top-p as a bound on the sum of better
+  // ranks: `bound`, or, where that is negative, tp times what top-k keeps.
+  __device__ void finish(int which, int cnt, int k, float tp, double bound, float u, unsigned long long& total,
+                         uint32_t& kept, bool& mine, uint32_t& idx, uint32_t& weight) {
+    const int tid = threadIdx.x;
+    auto& list = sh.list[which];
+    unsigned long long key = kKeyAll, before = 0;
+    uint32_t w = 0, c = 0;
+    if (tid < cnt) {
+      key = list.key[tid];
+      w = list.w[tid];
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        const bool better = list.key[j] < key;
+        c += better;
+        before += better ? list.w[j] : 0u;
       }
     }
-    if (threadIdx.x == 0 && rank == 0) sh.list_n = 0;
-    // The list may be filled again (by any CTA) only when all have read it.
-    cluster.sync();
-    key = sh.f_key;
-    sum = sh.f_sum;
+    bool in = tid < cnt && (k <= 0 || c < (uint32_t)k);
+    uint32_t n;
+    unsigned long long s = block_sum(in ? w : 0u, in, n);
+    if (tp < 1.f) in = in && ((double)before < (bound >= 0.0 ? bound : (double)tp * (double)s) || c == 0u);
+    if (row.min_p > 0.f && in) {
+      const uint32_t o = ~(uint32_t)(key >> kIdxBits);
+      in = row.w(__uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o)) >= row.min_p;
+    }
+    total = block_sum(in ? w : 0u, in, kept);
+    const unsigned long long target = draw(u, total);
+    // Running sum in index order: the weights of the others that are kept.
+    if (tid < cnt && !in) list.w[tid] = 0u;
+    // K*: the worst kept key (min-p also keeps a prefix).
+    if (tid == 0) sh.f_key = 0;
     __syncthreads();
+    idx = (uint32_t)key & ((1u << kIdxBits) - 1);
+    unsigned long long run = 0;
+    if (in) {
+      atomicMax(&sh.f_key, key);
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        const uint32_t oi = (uint32_t)list.key[j] & ((1u << kIdxBits) - 1);
+        run += oi < idx ? list.w[j] : 0u;
+      }
+    }
+    mine = in && target >= run && target < run + w;
+    weight = w;
+    __syncthreads();
+    row.set_max(sh.f_key);
+  }
+
+  // Sum of v and count of `one` over the CTA.
+  __device__ unsigned long long block_sum(uint32_t v, bool one, uint32_t& n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long s = v;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const uint32_t c = __popc(__ballot_sync(0xFFFFFFFFu, one));
+    __syncthreads();
+    if (lane == 0) sh.warp_sum[warp] = s, sh.warp_cnt[warp] = c;
+    __syncthreads();
+    s = 0;
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += sh.warp_sum[i], n += sh.warp_cnt[i];
+    return s;
+  }
+
+  // floor(u * total), in [0, total).
+  __device__ static unsigned long long draw(float u, unsigned long long total) {
+    const unsigned long long t = u > 0.f ? (unsigned long long)((double)fminf(u, 1.f) * (double)total) : 0ull;
+    return t >= total ? total - 1 : t;
   }
 };
 
@@ -332,11 +463,10 @@ struct Loader<uint16_t> {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   using L = Loader<T>;
   extern __shared__ __align__(32) uint8_t smp_dyn[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smp_dyn);
-  float* zbuf = reinterpret_cast<float*>(smp_dyn + ((sizeof(SampleShared) + 31) & ~(size_t)31));
   pdl_trigger();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -350,22 +480,22 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
   const bool valid = temp >= 0.f;
   const float inv = greedy ? 1.f : 1.f / temp;
   const T* src = (const T*)p.logits + r * p.stride + start;
-  // Shared memory takes the scores at the global address's offset within 16
-  // bytes, so that both sides of a vector are aligned.
-  const int mis = (int)(((uintptr_t)src / sizeof(T)) & (L::kVec - 1));
-  float* z = zbuf + mis;
   float best = -CUDART_INF_F;
   uint32_t besti = 0;
-  auto put = [&](float x, int i) {
-    float v = fmaf(x, inv, 0.f);  // + 0: no negative zeros
-    v = v != v ? -CUDART_INF_F : v;
+  auto put = [&](float v, int i) {
     if (v > best) best = v, besti = start + i;
     return v;
   };
-  const int head = n < ((L::kVec - mis) & (L::kVec - 1)) ? n : ((L::kVec - mis) & (L::kVec - 1));
-  const int nvec = (n - head) / L::kVec;
-  if (tid < head) z[tid] = put(L::one(src + tid), tid);
+  const int mis = (int)(((uintptr_t)src / sizeof(T)) & (L::kVec - 1));  // entries before the first score
+  float* zbuf = reinterpret_cast<float*>(smp_dyn + ((sizeof(SampleShared) + 31) & ~(size_t)31));
+  const float4* z4 = reinterpret_cast<const float4*>(zbuf);
   {
+    // Shared memory takes the scores at the global address's offset within 16
+    // bytes, so that both sides of a vector are aligned.
+    float* z = zbuf + mis;
+    const int head = n < ((L::kVec - mis) & (L::kVec - 1)) ? n : ((L::kVec - mis) & (L::kVec - 1));
+    const int nvec = (n - head) / L::kVec;
+    if (tid < head) z[tid] = put(scaled(L::one(src + tid), inv), tid);
     const typename L::Vec* v = reinterpret_cast<const typename L::Vec*>(src + head);
     constexpr int U = 4;
     for (int i0 = tid; i0 < nvec; i0 += kThreads * U) {
@@ -380,17 +510,18 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
           float f[L::kVec];
           L::unpack(x[j], f);
 #pragma unroll
-          for (int e = 0; e < L::kVec; ++e) f[e] = put(f[e], head + i * L::kVec + e);
+          for (int e = 0; e < L::kVec; ++e) f[e] = put(scaled(f[e], inv), head + i * L::kVec + e);
           float4* d = reinterpret_cast<float4*>(z + head + i * L::kVec);
 #pragma unroll
           for (int e = 0; e < L::kVec; e += 4) d[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
         }
       }
     }
-  }
-  {
     const int i = head + nvec * L::kVec + tid;
-    if (i < n) z[i] = put(L::one(src + i), i);
+    if (i < n) z[i] = put(scaled(L::one(src + i), inv), i);
+    // -inf around the scores: the passes take whole groups of four.
+    if (tid < mis) zbuf[tid] = -CUDART_INF_F;
+    if (tid < 4) z[n + tid] = -CUDART_INF_F;
   }
   // Best score of the row, lowest index among equals.
   unsigned long long b = ((unsigned long long)order_bits(best) << 32) | (0xFFFFFFFFu - besti);
@@ -401,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
     b = warp_max(lane < kWarps ? sh.warp_best[lane] : 0ull);
     if (lane < cl) cluster.map_shared_rank(&sh, lane)->cl_best[rank] = b;
   }
-  if (tid == 0) sh.list_n = 0;
+  if (tid < 2) sh.list_n[tid] = 0;
   cluster.sync();
   b = 0;
   for (int i = 0; i < cl; ++i) b = sh.cl_best[i] > b ? sh.cl_best[i] : b;
@@ -420,127 +551,158 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
       for (int i = tid; i < n; i += kThreads) probs[i] = !empty && start + i == (int)mi ? 1.f : 0.f;
     return;
   }
-  Sampler s(sh, z, n, (uint32_t)start);
+  Sampler s(sh, z4, mis + n, (uint32_t)(start - mis));
   s.row.m = m;
   s.row.inf = m == CUDART_INF_F;
+  s.row.least = m - kCut;  // +inf where m is: only those count
   const float mp = p.min_p ? __ldg(&p.min_p[r]) : 0.f;
   s.row.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;  // the best token passes
   s.row.key_max = kKeyAll;
   const int k = p.top_k ? __ldg(&p.top_k[r]) : 0;
   const float tp = p.top_p ? __ldg(&p.top_p[r]) : 1.f;
-  const bool use_k = k > 0 && k < p.vocab, use_p = tp < 1.f;
-  if (use_k || use_p) {
-    Match all;
-    all.b0 = -1;
-    all.shift = 50;
-    all.prefix = 0;
-    s.histogram(all);
-    bool fresh = true;
-    uint32_t ac = 0;
-    unsigned long long key_k = kKeyAll, sum_k = 0, as = 0;
-    Target tg;
-    tg.by_count = true;
-    tg.count = use_k ? (uint32_t)k : 0xFFFFFFFFu;
-    tg.bound = 0.0;
-    if (s.find_bin(tg, 0u, 0ull, ac, as)) s.resolve(tg, key_k, sum_k, fresh);
-    else sum_k = as;
-    if (use_p) {
-      tg.by_count = false;
-      tg.bound = (double)tp * (double)sum_k;
-      const unsigned long long key_best = rank_key(m, mi);
-      unsigned long long key_p = key_best, sum_p;
-      if (tg.bound > 0.0) {
-        if (!fresh) s.histogram(all);
-        if (s.find_bin(tg, 0u, 0ull, ac, as)) s.resolve(tg, key_p, sum_p, fresh);
-      }
-      key_k = key_p < key_k ? key_p : key_k;
-    }
-    s.row.key_max = key_k;
-  }
-  // Kept weight by warp: warp w owns a contiguous piece of the CTA's tokens.
-  const Row row = s.row;
-  const int piece = (((n + kWarps - 1) / kWarps) + 31) & ~31;
-  const int p0 = warp * piece < n ? warp * piece : n, p1 = p0 + piece < n ? p0 + piece : n;
-  unsigned long long sum = 0;
-  uint32_t cnt = 0;
-  for (int i = p0 + lane; i < p1; i += 32) {
-    const uint32_t w = row.kept(z[i], (uint32_t)(start + i));
-    sum += w;
-    cnt += w != 0u;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    cnt += __shfl_xor_sync(0xFFFFFFFFu, cnt, o);
-  }
-  __syncthreads();  // warp_sum, warp_cnt are also find_bin's
-  if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_cnt[warp] = cnt;
-  __syncthreads();
-  if (tid < cl) {
-    unsigned long long a = 0;
-    uint32_t c = 0;
-    for (int i = 0; i < kWarps; ++i) a += sh.warp_sum[i], c += sh.warp_cnt[i];
-    SampleShared* o = cluster.map_shared_rank(&sh, tid);
-    o->cl_sum[rank] = a;
-    o->cl_cnt[rank] = c;
-  }
-  cluster.sync();  // no remote access follows
-  unsigned long long total = 0, before = 0;
-  uint32_t kept = 0;
-  for (int i = 0; i < cl; ++i) {
-    if (i < rank) before += sh.cl_sum[i];
-    total += sh.cl_sum[i];
-    kept += sh.cl_cnt[i];
-  }
   const float u = __ldg(&p.u[r]);
-  unsigned long long target = u > 0.f ? (unsigned long long)((double)fminf(u, 1.f) * (double)total) : 0ull;
-  if (target >= total) target = total - 1;
-  for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
-  if (target >= before && target < before + sum) {  // one warp of the cluster
-    unsigned long long run = before;
-    for (int i0 = p0; i0 < p1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t w = i < p1 ? row.kept(z[i], (uint32_t)(start + i)) : 0u;
-      unsigned long long inc = w;
+  Match all;
+  all.level = all.b0 = all.b1 = all.shift = 0;
+  all.prefix = 0;
+  bool short_list = false;
+  unsigned long long total = 0;
+  uint32_t kept = 0;
+  const bool use_k = k > 0 && k < p.vocab, use_p = tp < 1.f && tp > 0.f;
+  if (tp <= 0.f) s.row.set_max(rank_key(m, mi));
+  for (int search = 0; search < 2 && !short_list; ++search) {  // 0: top-k, 1: top-p of what it left
+    if (search == 0 ? !use_k : !use_p) continue;
+    Target tg;
+    tg.by_count = search == 0;
+    tg.count = search == 0 ? (uint32_t)k : 0u;
+    tg.bound = (double)tp;
+    s.histogram(all, search == 1);
+    if (!s.find_bin(tg, 0u, 0ull, search == 1)) continue;
+    short_list = sh.f_before_cnt + sh.f_cnt <= kList;
+    if (short_list) {
+      Match to;
+      to.level = -1;
+      to.b0 = (int)sh.f_bin;
+      s.gather(to, search);  // no remote access follows
+      const int cnt = (int)(sh.f_before_cnt + sh.f_cnt);
+      bool mine;
+      uint32_t idx, w;
+      s.finish(search, cnt, search == 0 && use_k ? k : 0, tp, search == 1 ? tg.bound : -1.0, u, total, kept, mine, idx, w);
+      if (rank == 0 && mine) {
+        p.token[r] = (int)idx;
+        if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+      }
+    } else {
+      s.row.set_max(s.resolve(tg, search, search == 1));
+    }
+  }
+  // Kept weight by warp: warp w owns a contiguous piece of the CTA's groups
+  // of four.
+  const Row row = s.row;
+  const int base = start - mis;  // index in the row of the first entry
+  const int piece = (((s.n4 + kWarps - 1) / kWarps) + 31) & ~31;
+  const int p0 = warp * piece < s.n4 ? warp * piece : s.n4, p1 = p0 + piece < s.n4 ? p0 + piece : s.n4;
+  auto kept4 = [&](int v, uint32_t (&w)[4]) {
+    const float4 x = z4[v];
+    w[0] = row.kept(x.x, (uint32_t)(base + 4 * v));
+    w[1] = row.kept(x.y, (uint32_t)(base + 4 * v + 1));
+    w[2] = row.kept(x.z, (uint32_t)(base + 4 * v + 2));
+    w[3] = row.kept(x.w, (uint32_t)(base + 4 * v + 3));
+  };
+  if (!short_list) {
+    unsigned long long sum = 0;
+    uint32_t cnt = 0;
+#pragma unroll 2
+    for (int v = p0 + lane; v < p1; v += 32) {
+      uint32_t w[4];
+      kept4(v, w);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, target < run + inc);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          p.token[r] = start + i;
-          if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+      for (int e = 0; e < 4; ++e) sum += w[e], cnt += w[e] != 0u;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      cnt += __shfl_xor_sync(0xFFFFFFFFu, cnt, o);
+    }
+    __syncthreads();  // warp_sum, warp_cnt are also find_bin's
+    if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_cnt[warp] = cnt;
+    __syncthreads();
+    if (tid < cl) {
+      unsigned long long a = 0;
+      uint32_t c = 0;
+      for (int i = 0; i < kWarps; ++i) a += sh.warp_sum[i], c += sh.warp_cnt[i];
+      SampleShared* o = cluster.map_shared_rank(&sh, tid);
+      o->cl_sum[rank] = a;
+      o->cl_cnt[rank] = c;
+    }
+    cluster.sync();  // no remote access follows
+    unsigned long long before = 0;
+    for (int i = 0; i < cl; ++i) {
+      if (i < rank) before += sh.cl_sum[i];
+      total += sh.cl_sum[i];
+      kept += sh.cl_cnt[i];
+    }
+    const unsigned long long target = Sampler::draw(u, total);
+    for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
+    if (target >= before && target < before + sum) {  // one warp of the cluster
+      unsigned long long run = before;
+      for (int v0 = p0; v0 < p1; v0 += 32) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (v0 + lane < p1) kept4(v0 + lane, w);
+        const unsigned long long mine = (unsigned long long)w[0] + w[1] + w[2] + w[3];
+        unsigned long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += x;
         }
-        break;
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, target < run + inc);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            unsigned long long at = run + inc - mine;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (target >= at && target < at + w[e]) {
+                p.token[r] = base + 4 * (v0 + lane) + e;
+                if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w[e]) / __ull2float_rn(total));
+              }
+              at += w[e];
+            }
+          }
+          break;
+        }
+        run += __shfl_sync(0xFFFFFFFFu, inc, 31);
       }
-      run += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
   }
   if (rank == 0 && tid == 0 && p.kept) p.kept[r] = (int)kept;
   if (probs) {
     const float scale = 1.f / __ull2float_rn(total);
-    for (int i = tid; i < n; i += kThreads) {
-      const uint32_t w = row.kept(z[i], (uint32_t)(start + i));
-      __stcs(&probs[i], __uint2float_rn(w) * scale);
+    const bool aligned4 = (((uintptr_t)(probs - mis)) & 15) == 0;
+    for (int v = tid; v < s.n4; v += kThreads) {
+      uint32_t w[4];
+      kept4(v, w);
+      const int i = 4 * v - mis;
+      if (aligned4 && i >= 0 && i + 4 <= n) {
+        __stcs(reinterpret_cast<float4*>(probs + i), make_float4(__uint2float_rn(w[0]) * scale, __uint2float_rn(w[1]) * scale,
+                                                                 __uint2float_rn(w[2]) * scale, __uint2float_rn(w[3]) * scale));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e >= 0 && i + e < n) __stcs(&probs[i + e], __uint2float_rn(w[e]) * scale);
+      }
     }
   }
 }
 
 template <typename T>
 cudaError_t launch(SampleParams p, cudaStream_t s) {
-  // CTAs of a row: enough that its piece is small against shared memory (two
-  // CTAs an SM overlap one's loads with another's passes) and that few rows
-  // still spread over the chip; at least 2,048 scores each.
+  // CTAs of a row: two CTAs of up to 16,384 scores fit an SM; more a row while
+  // all of them still run at once, down to 2,048 scores each.
   int cl = 1;
-  while (cl < kMaxCl) {
-    const int piece = (p.vocab + cl - 1) / cl;
-    if (piece <= 12288 && ((long long)p.rows * cl >= kNumSMs || piece <= 2048)) break;
-    cl *= 2;
-  }
-  p.chunk = ((p.vocab + cl - 1) / cl + 7) & ~7;
-  const size_t smem = ((sizeof(SampleShared) + 31) & ~(size_t)31) + (size_t)(p.chunk + 8) * 4;
+  auto piece = [&](int c) { return (p.vocab + c - 1) / c; };
+  while (cl < kMaxCl && (piece(cl) > 16384 || (2ll * cl * p.rows <= 2 * kNumSMs && piece(cl) > 4096))) cl *= 2;
+  p.chunk = (piece(cl) + 7) & ~7;
+  const size_t smem = ((sizeof(SampleShared) + 31) & ~(size_t)31) + (size_t)(p.chunk + 16) * 4;
   auto kern = k_sample<T>;
   cudaError_t err = ensure_smem_attr((const void*)kern, smem);
   if (err != cudaSuccess) return err;
