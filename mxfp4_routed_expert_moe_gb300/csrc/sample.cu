@@ -12,12 +12,12 @@
 // A cluster of 1 to 8 CTAs takes a row; its scores are read from HBM once and
 // stay in shared memory.  K* comes from histograms (count or sum of W per bin)
 // that the CTAs of the cluster add up over distributed shared memory: the
-// first by m - z in 1,024 equal bins (a monotone function of z); if the bin
-// that holds the bound has more than kList tokens, the next by 1,024 equal
-// parts of that bin; if one part still has more (ties), by 10 bits of K at a
-// time.  A bin of at most kList tokens is ranked directly.  Top-k is searched
+// first by m - z in some 1,000 equal bins (a monotone function of z); if the
+// bin that holds the bound has more than kList tokens (ties), the next by equal
+// pieces of the range of its keys.  A bin of at most kList tokens goes to every CTA as
+// a list, which each searches alone, in the same way.  Top-k is searched
 // first, by counts alone (no exponentials); what it drops, later passes skip.
-// When all tokens down to the end of the first bin found number at most kList
+// When all tokens down to the end of the first bin found number at most kShort
 // (small top-k, peaked rows), every CTA gets them all and finishes alone.
 // Bound by latency (cluster barriers of 0.8 us) for few rows, by the
 // instructions of the passes and the barriers for many: shared memory holds
@@ -36,29 +36,42 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 256;
+constexpr int kList = 1024;             // tokens of one bin that go to every CTA
+constexpr int kShort = 256;             // candidates that every CTA finishes alone
+constexpr int kDirect = 128;            // tokens that are ranked pair by pair
 constexpr int kIdxBits = 18;             // MOE_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCl = 8;
-constexpr int kMostScores = 32768;       // of a CTA
+constexpr int kMostScores = 65536;       // of a CTA
+constexpr int kMostBytes = 84 << 10;
 constexpr float kFix = 2147483648.f;     // 2^31
-constexpr float kBinScale = 46.f;        // W > 0 needs m - z < 22.2: bins 0 .. 1021
+constexpr float kBinScale = 45.9f;       // times kCut: below kBins - 1
 constexpr float kCut = 22.25f;           // below m - kCut every W is 0, ...
 constexpr float kSure = 22.f;            // ... down to m - kSure none is (exp(-22) 2^31 = 0.599)
 constexpr unsigned long long kKeyAll = ~0ull;
 
 struct SampleShared {
-  // Histogram of this CTA: count, low and high 16 bits of W (native 32-bit
-  // shared-memory atomics; at most kMostScores tokens a CTA keep all three
-  // within 32 bits, even if they share a bin).
-  uint32_t cnt[kBins], lo[kBins], hi[kBins];
+  union {
+    // Histogram of this CTA: count, low and high 16 bits of W (native 32-bit
+    // shared-memory atomics; at most kMostScores tokens a CTA keep all three
+    // within 32 bits, even if they share a bin).
+    struct {
+      uint32_t cnt[kBins], lo[kBins], hi[kBins];
+    };
+    // After the cluster has added them up: the tokens of one bin.
+    struct {
+      unsigned long long key[kList];
+      uint32_t w[kList];
+    } list;
+  };
   unsigned long long tsum[kBins];  // the cluster's totals
   uint32_t tcnt[kBins];
-  // The tokens of one bin of the cluster: one list for each search of a row.
-  struct {
-    unsigned long long key[kList];
-    uint32_t w[kList];
-  } list[2];
-  uint32_t list_n[2];  // rank 0's are the cluster's
+  uint32_t list_n;  // rank 0's is the cluster's
+  struct {  // the tokens of the list that are left
+    unsigned long long key[kDirect];
+    uint32_t w[kDirect];
+  } few;
+  uint32_t few_n;
+  unsigned long long warp_low[kWarps], cl_low[kMaxCl];
   unsigned long long warp_best[kWarps];
   unsigned long long warp_sum[kWarps];
   uint32_t warp_cnt[kWarps];
@@ -72,6 +85,7 @@ struct SampleShared {
 static_assert(MOE_SAMPLE_MAX_VOCAB <= kMostScores * kMaxCl, "a cluster takes the longest row");
 static_assert(MOE_SAMPLE_MAX_VOCAB == 1 << kIdxBits, "index bits of the key");
 
+__device__ __forceinline__ float order_float(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o); }
 // Order-preserving bits of a float (ascending), -0 excluded.
 __device__ __forceinline__ uint32_t order_bits(float z) {
   const uint32_t b = __float_as_uint(z);
@@ -85,20 +99,16 @@ struct Row {
   float m;       // largest scaled score
   float least;   // scores below have W = 0 or rank past K*
   float min_p;   // 0: off
-  bool inf;      // m = +inf
   unsigned long long key_max;  // K*
 
   // exp(z - m).  expf, not an approximation: the weights are part of the
   // definition, and the same function gives the same integers everywhere.
-  __device__ __forceinline__ float w(float z) const { return inf ? (z == m ? 1.f : 0.f) : expf(z - m); }
+  __device__ __forceinline__ float w(float z) const { return expf(z - m); }
   __device__ __forceinline__ static uint32_t fixed(float w) { return __float2uint_rn(w * kFix); }
-  // Place of z on the axis of bins, and its bin and part of that bin: each
-  // step is monotone in z (the subtraction of the bin is exact).
-  __device__ __forceinline__ float place(float z) const { return inf ? 0.f : fminf((m - z) * kBinScale, (float)(kBins - 1)); }
-  __device__ __forceinline__ int bin(float z) const { return (int)place(z); }
-  __device__ __forceinline__ int part(float z) const {
-    const float t = place(z);
-    return (int)((t - (float)(int)t) * (float)kBins);
+  // Bin of a score that is not below m - kCut: adding 2^23 leaves the rounded
+  // product in the low bits (monotone in z; cheaper than a conversion).
+  __device__ __forceinline__ int bin(float z) const {
+    return (int)(__float_as_uint(fmaf(m - z, kBinScale, 8388608.f)) & (kBins - 1));
   }
   // Not dropped by the bound found so far (for z >= least).
   __device__ __forceinline__ bool within(float z, uint32_t idx) const {
@@ -106,8 +116,7 @@ struct Row {
   }
   __device__ __forceinline__ void set_max(unsigned long long key) {
     key_max = key;
-    const uint32_t o = ~(uint32_t)(key >> kIdxBits);
-    least = fmaxf(least, __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o));
+    least = fmaxf(least, order_float(~(uint32_t)(key >> kIdxBits)));
   }
   // Weight of a kept token, 0 for the others.
   __device__ __forceinline__ uint32_t kept(float z, uint32_t idx) const {
@@ -141,30 +150,67 @@ struct Target {
   }
 };
 
-// Tokens that match the search so far: level -1 those down to bin b0, 0 all, 1 those of bin b0, 2 of
-// its part b1, above that those whose key starts with `prefix` (shift bits
-// follow) among them.
+// Tokens that match the search so far: level -1 those down to bin b0, 0 all, 1
+// those of bin b0, 2 those of them with a key in [lo, hi].
 struct Match {
-  int level, b0, b1, shift;
-  unsigned long long prefix;
+  int level, b0;
+  unsigned long long lo, hi;
 };
 
+// 1,024 equal pieces of a range of keys.
+struct Pieces {
+  unsigned long long lo;
+  int shift;
+  __device__ __forceinline__ Pieces(unsigned long long low, unsigned long long high) : lo(low), shift(0) {
+    const int bits = 64 - __clzll((long long)(high - low));
+    if (bits > 10) shift = bits - 10;
+  }
+  __device__ __forceinline__ int piece(unsigned long long key) const { return (int)((key - lo) >> shift); }
+  __device__ __forceinline__ void narrow(int piece, unsigned long long& l, unsigned long long& h) const {
+    l = lo + ((unsigned long long)piece << shift);
+    h = l + (1ull << shift) - 1;
+  }
+};
+
+// NaN stays NaN: it is below every bound and never the largest.
 __device__ __forceinline__ float scaled(float x, float inv) {
-  const float v = fmaf(x, inv, 0.f);  // + 0: no negative zeros
-  return v != v ? -CUDART_INF_F : v;
+  return fmaf(x, inv, 0.f);  // + 0: no negative zeros
 }
+
+// A CTA's scores in shared memory, in groups of four, -inf around them: fp32
+// ones scaled, bf16 ones as they came (half the space; scaled when read).
+template <typename T>
+struct Scores;
+template <>
+struct Scores<float> {
+  const float4* g;
+  float inv;
+  __device__ __forceinline__ float4 get(int v) const { return g[v]; }
+};
+template <>
+struct Scores<uint16_t> {
+  const uint2* g;
+  float inv;
+  __device__ __forceinline__ float4 get(int v) const {
+    const uint2 x = g[v];
+    return make_float4(scaled(__uint_as_float(x.x << 16), inv), scaled(__uint_as_float(x.x & 0xFFFF0000u), inv),
+                       scaled(__uint_as_float(x.y << 16), inv), scaled(__uint_as_float(x.y & 0xFFFF0000u), inv));
+  }
+};
+
+template <typename T>
 class Sampler {
  public:
   SampleShared& sh;
-  const float4* z4;  // this CTA's scaled scores in groups of four, -inf around them
-  int n4;
+  Scores<T> sc;
+  int n4;          // groups
   uint32_t first;  // index in the row of the first entry
   int cl, rank;
   Row row;
   cg::cluster_group cluster;
 
-  __device__ Sampler(SampleShared& s, const float4* scores, int n, uint32_t f)
-      : sh(s), z4(scores), n4((n + 3) / 4), first(f), cluster(cg::this_cluster()) {
+  __device__ Sampler(SampleShared& s, const Scores<T>& scores, int n, uint32_t f)
+      : sh(s), sc(scores), n4((n + 3) / 4), first(f), cluster(cg::this_cluster()) {
     cl = (int)cluster.num_blocks();
     rank = (int)cluster.block_rank();
   }
@@ -180,8 +226,8 @@ class Sampler {
   __device__ __forceinline__ void each(F f) const {
     const float kNone = -CUDART_INF_F;
     for (int v = threadIdx.x; v < n4; v += 2 * kThreads) {
-      const float4 a = z4[v];
-      const float4 b = v + kThreads < n4 ? z4[v + kThreads] : make_float4(kNone, kNone, kNone, kNone);
+      const float4 a = sc.get(v);
+      const float4 b = v + kThreads < n4 ? sc.get(v + kThreads) : make_float4(kNone, kNone, kNone, kNone);
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -195,13 +241,13 @@ class Sampler {
     if (mt.level < 0) return row.bin(zi) <= mt.b0;
     if (row.bin(zi) != mt.b0) return false;
     if (mt.level == 1) return true;
-    if (row.part(zi) != mt.b1) return false;
-    return mt.level == 2 || (rank_key(zi, idx) >> mt.shift) == mt.prefix;
+    const unsigned long long k = rank_key(zi, idx);
+    return k >= mt.lo && k <= mt.hi;
   }
 
   // Histogram of the matching tokens over the cluster into tcnt / tsum, by
   // the next level's bins; of counts alone where no sums are needed.
-  __device__ void histogram(const Match& mt, bool sums) {
+  __device__ void histogram(const Match& mt, bool sums, const Pieces& pc) {
     const int tid = threadIdx.x;
     for (int b = tid; b < kBins; b += kThreads) sh.cnt[b] = sh.lo[b] = sh.hi[b] = 0u;
     __syncthreads();
@@ -209,9 +255,7 @@ class Sampler {
       uint32_t w = 1u;
       if (sums || zi < row.m - kSure) w = Row::fixed(row.w(zi));
       if (w == 0u || !matches(mt, zi, idx)) return;
-      const int b = mt.level == 0   ? row.bin(zi)
-                    : mt.level == 1 ? row.part(zi)
-                                    : (int)(rank_key(zi, idx) >> (mt.shift - 10)) & (kBins - 1);
+      const int b = mt.level == 0 ? row.bin(zi) : pc.piece(rank_key(zi, idx));
       atomicAdd(&sh.cnt[b], 1u);
       if (sums) {
         atomicAdd(&sh.lo[b], w & 0xFFFFu);
@@ -241,7 +285,29 @@ class Sampler {
         }
       }
     }
+    if (tid == 0) sh.list_n = 0;
     cluster.sync();
+  }
+
+  // Least and greatest key of the CTA's matching tokens (f visits them).
+  template <typename F>
+  __device__ void key_range(F visit, unsigned long long& low, unsigned long long& high) {
+    low = kKeyAll;
+    high = 0;
+    visit([&](unsigned long long k) {
+      low = k < low ? k : low;
+      high = k > high ? k : high;
+    });
+    low = ~warp_max(~low);
+    high = warp_max(high);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.warp_low[threadIdx.x >> 5] = low, sh.warp_best[threadIdx.x >> 5] = high;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      low = sh.warp_low[i] < low ? sh.warp_low[i] : low;
+      high = sh.warp_best[i] > high ? sh.warp_best[i] : high;
+    }
   }
 
   // The bin that holds the target, given what ranks before this histogram;
@@ -297,9 +363,11 @@ class Sampler {
     return sh.f_bin < kBins;
   }
 
-  // Hand every CTA the list of the matching tokens (in any order).
-  __device__ void gather(const Match& mt, int which) {
-    uint32_t* cursor = remote(&sh.list_n[which], 0);
+  // Hand every CTA the list of the matching tokens (in any order).  No CTA
+  // still reads the list of an earlier search: two cluster barriers of a
+  // histogram lie between.
+  __device__ void gather(const Match& mt) {
+    uint32_t* cursor = remote(&sh.list_n, 0);
     each([&](float zi, uint32_t idx) {
       if (!matches(mt, zi, idx)) return;
       const uint32_t w = Row::fixed(row.w(zi));
@@ -309,69 +377,110 @@ class Sampler {
       if (at < kList)
         for (int r = 0; r < cl; ++r) {
           SampleShared* o = remote(&sh, r);
-          o->list[which].key[at] = k;
-          o->list[which].w[at] = w;
+          o->list.key[at] = k;
+          o->list.w[at] = w;
         }
     });
     cluster.sync();
   }
 
-  // After find_bin on the first histogram: the key of the target.  `which`:
-  // the list to use, one for each search, so that no CTA fills a list that
-  // another still reads.
-  __device__ unsigned long long resolve(Target& tg, int which, bool sums) {
+  // After find_bin on the first histogram: the key of the target.
+  __device__ unsigned long long resolve(Target& tg, bool sums) {
     Match mt;
     mt.level = 1;
     mt.b0 = (int)sh.f_bin;
-    mt.b1 = 0;
-    mt.shift = 50;
-    mt.prefix = 0;
-    uint32_t before_cnt = sh.f_before_cnt;
+    mt.lo = 0;
+    mt.hi = kKeyAll;
+    uint32_t before_cnt = sh.f_before_cnt, cnt = sh.f_cnt;
     unsigned long long before_sum = sh.f_before_sum;
-    while (sh.f_cnt > kList) {  // uniform: every CTA of the cluster has the same totals
-      __syncthreads();
-      histogram(mt, sums);
-      find_bin(tg, before_cnt, before_sum, false);
-      if (mt.level == 1) {
-        mt.b1 = (int)sh.f_bin;
-      } else {
-        mt.shift -= 10;
-        mt.prefix = (mt.prefix << 10) | sh.f_bin;
+    while (cnt > kList) {  // uniform: every CTA of the cluster has the same totals
+      unsigned long long low, high;
+      key_range([&](auto f) { each([&](float zi, uint32_t idx) { if (matches(mt, zi, idx)) f(rank_key(zi, idx)); }); }, low, high);
+      if ((int)threadIdx.x < cl) {
+        SampleShared* o = remote(&sh, threadIdx.x);
+        o->cl_low[rank] = low;
+        o->cl_best[rank] = high;
       }
-      ++mt.level;
+      cluster.sync();
+      for (int r = 0; r < cl; ++r) {
+        low = sh.cl_low[r] < low ? sh.cl_low[r] : low;
+        high = sh.cl_best[r] > high ? sh.cl_best[r] : high;
+      }
+      const Pieces pc(low, high);
+      histogram(mt, sums, pc);
+      find_bin(tg, before_cnt, before_sum, false);
+      pc.narrow((int)sh.f_bin, mt.lo, mt.hi);
+      mt.level = 2;
       before_cnt = sh.f_before_cnt;
       before_sum = sh.f_before_sum;
+      cnt = sh.f_cnt;
     }
-    gather(mt, which);
-    const int cnt = (int)sh.f_cnt;
-    const auto& list = sh.list[which];
-    static_assert(kList <= kThreads, "one token of the list per thread");
-    if ((int)threadIdx.x < cnt) {
-      const unsigned long long k = list.key[threadIdx.x];
+    gather(mt);
+    // Each CTA narrows the list down by itself.
+    const auto& list = sh.list;
+    const int n = (int)cnt;
+    unsigned long long lo = 0, hi = kKeyAll;
+    auto left = [&](auto f) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const unsigned long long k = list.key[i];
+        if (k >= lo && k <= hi) f(k, list.w[i]);
+      }
+    };
+    while (cnt > kDirect) {
+      unsigned long long low, high;
+      key_range([&](auto f) { left([&](unsigned long long k, uint32_t) { f(k); }); }, low, high);
+      const Pieces pc(low, high);
+      for (int b = threadIdx.x; b < kBins; b += kThreads) {
+        sh.tcnt[b] = 0u;
+        sh.tsum[b] = 0ull;
+      }
+      __syncthreads();
+      left([&](unsigned long long k, uint32_t w) {
+        const int b = pc.piece(k);
+        atomicAdd(&sh.tcnt[b], 1u);
+        atomicAdd(&sh.tsum[b], (unsigned long long)w);
+      });
+      __syncthreads();
+      find_bin(tg, before_cnt, before_sum, false);
+      pc.narrow((int)sh.f_bin, lo, hi);
+      before_cnt = sh.f_before_cnt;
+      before_sum = sh.f_before_sum;
+      cnt = sh.f_cnt;
+    }
+    if (threadIdx.x == 0) sh.few_n = 0;
+    __syncthreads();
+    left([&](unsigned long long k, uint32_t w) {
+      const uint32_t at = atomicAdd(&sh.few_n, 1u);
+      sh.few.key[at] = k;
+      sh.few.w[at] = w;
+    });
+    __syncthreads();
+    if (threadIdx.x < cnt) {
+      const unsigned long long k = sh.few.key[threadIdx.x];
       uint32_t c = before_cnt;
       unsigned long long s = before_sum;
 #pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        const bool better = list.key[j] < k;
+      for (uint32_t j = 0; j < cnt; ++j) {
+        const bool better = sh.few.key[j] < k;
         c += better;
-        s += better ? list.w[j] : 0u;
+        s += better ? sh.few.w[j] : 0u;
       }
-      const uint32_t w = list.w[threadIdx.x];
-      if (tg.holds(c, 1u, s, w)) sh.f_key = k;
+      if (tg.holds(c, 1u, s, sh.few.w[threadIdx.x])) sh.f_key = k;
     }
     __syncthreads();
     return sh.f_key;
   }
 
-  // All candidates are the cnt <= kList tokens of list `which`: apply the
-  // filters and draw, in every CTA alike (no cluster barrier).  Returns the
+  // All candidates are the cnt <= kShort tokens of the list: apply the filters
+  // and draw, in every CTA alike (no cluster barrier).  Returns the
   // total and the number kept; `mine` tells the thread whose token was drawn.
   // The filters are top-k (k > 0), then top-p as a bound on the sum of better
   // ranks: `bound`, or, where that is negative, tp times what top-k keeps.
-  __device__ void finish(int which, int cnt, int k, float tp, double bound, float u, unsigned long long& total,
+  __device__ void finish(int cnt, int k, float tp, double bound, float u, unsigned long long& total,
                          uint32_t& kept, bool& mine, uint32_t& idx, uint32_t& weight) {
     const int tid = threadIdx.x;
-    auto& list = sh.list[which];
+    auto& list = sh.list;
+    static_assert(kShort <= kThreads, "one candidate per thread");
     unsigned long long key = kKeyAll, before = 0;
     uint32_t w = 0, c = 0;
     if (tid < cnt) {
@@ -389,8 +498,7 @@ class Sampler {
     unsigned long long s = block_sum(in ? w : 0u, in, n);
     if (tp < 1.f) in = in && ((double)before < (bound >= 0.0 ? bound : (double)tp * (double)s) || c == 0u);
     if (row.min_p > 0.f && in) {
-      const uint32_t o = ~(uint32_t)(key >> kIdxBits);
-      in = row.w(__uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o)) >= row.min_p;
+      in = row.w(order_float(~(uint32_t)(key >> kIdxBits))) >= row.min_p;
     }
     total = block_sum(in ? w : 0u, in, kept);
     const unsigned long long target = draw(u, total);
@@ -439,8 +547,7 @@ class Sampler {
   }
 };
 
-// Reads a CTA's scores into shared memory, scaled; returns the best
-// (order bits, inverted index) seen by this thread.
+// How scores of a type are read and kept.
 template <typename T>
 struct Loader;
 template <>
@@ -449,6 +556,14 @@ struct Loader<float> {
   using Vec = float4;
   __device__ static float one(const float* p) { return __ldcs(p); }
   __device__ static void unpack(const float4& v, float (&x)[4]) { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+  __device__ static float store(float z, float) { return z; }
+  __device__ static void store_vec(float* d, const float (&z)[4], const float4&) {
+    *reinterpret_cast<float4*>(d) = make_float4(z[0], z[1], z[2], z[3]);
+  }
+  static constexpr bool kScaled = true;  // kept as scaled scores
+  __device__ static float value(float x) { return x; }
+  __device__ static float none() { return -CUDART_INF_F; }
+  __device__ static float zero() { return 0.f; }
 };
 template <>
 struct Loader<uint16_t> {
@@ -460,6 +575,12 @@ struct Loader<uint16_t> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+  __device__ static uint16_t store(float, uint16_t x) { return x; }
+  __device__ static void store_vec(uint16_t* d, const float (&)[8], const uint4& x) { *reinterpret_cast<uint4*>(d) = x; }
+  static constexpr bool kScaled = false;
+  __device__ static float value(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+  __device__ static uint16_t none() { return 0xFF80u; }
+  __device__ static uint16_t zero() { return 0u; }
 };
 
 template <typename T>
@@ -481,21 +602,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   const float inv = greedy ? 1.f : 1.f / temp;
   const T* src = (const T*)p.logits + r * p.stride + start;
   float best = -CUDART_INF_F;
-  uint32_t besti = 0;
-  auto put = [&](float v, int i) {
-    if (v > best) best = v, besti = start + i;
+  auto put = [&](float v) {
+    best = fmaxf(best, v);
     return v;
   };
   const int mis = (int)(((uintptr_t)src / sizeof(T)) & (L::kVec - 1));  // entries before the first score
-  float* zbuf = reinterpret_cast<float*>(smp_dyn + ((sizeof(SampleShared) + 31) & ~(size_t)31));
-  const float4* z4 = reinterpret_cast<const float4*>(zbuf);
+  T* zbuf = reinterpret_cast<T*>(smp_dyn + ((sizeof(SampleShared) + 31) & ~(size_t)31));
+  Scores<T> sc;
+  sc.g = reinterpret_cast<decltype(sc.g)>(zbuf);
+  sc.inv = inv;
   {
     // Shared memory takes the scores at the global address's offset within 16
     // bytes, so that both sides of a vector are aligned.
-    float* z = zbuf + mis;
+    T* z = zbuf + mis;
     const int head = n < ((L::kVec - mis) & (L::kVec - 1)) ? n : ((L::kVec - mis) & (L::kVec - 1));
     const int nvec = (n - head) / L::kVec;
-    if (tid < head) z[tid] = put(scaled(L::one(src + tid), inv), tid);
+    auto one = [&](int i) { z[i] = L::store(put(scaled(L::one(src + i), inv)), src[i]); };
+    if (tid < head) one(tid);
     const typename L::Vec* v = reinterpret_cast<const typename L::Vec*>(src + head);
     constexpr int U = 4;
     for (int i0 = tid; i0 < nvec; i0 += kThreads * U) {
@@ -510,89 +633,102 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
           float f[L::kVec];
           L::unpack(x[j], f);
 #pragma unroll
-          for (int e = 0; e < L::kVec; ++e) f[e] = put(scaled(f[e], inv), head + i * L::kVec + e);
-          float4* d = reinterpret_cast<float4*>(z + head + i * L::kVec);
-#pragma unroll
-          for (int e = 0; e < L::kVec; e += 4) d[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          for (int e = 0; e < L::kVec; ++e) f[e] = put(scaled(f[e], inv));
+          L::store_vec(z + head + i * L::kVec, f, x[j]);
         }
       }
     }
     const int i = head + nvec * L::kVec + tid;
-    if (i < n) z[i] = put(scaled(L::one(src + i), inv), i);
+    if (i < n) one(i);
     // -inf around the scores: the passes take whole groups of four.
-    if (tid < mis) zbuf[tid] = -CUDART_INF_F;
-    if (tid < 4) z[n + tid] = -CUDART_INF_F;
+    if (tid < mis) zbuf[tid] = L::none();
+    if (tid < 4) z[n + tid] = L::none();
   }
-  // Best score of the row, lowest index among equals.
-  unsigned long long b = ((unsigned long long)order_bits(best) << 32) | (0xFFFFFFFFu - besti);
-  b = warp_max(b);
-  if (lane == 0) sh.warp_best[warp] = b;
+  // Largest score of the row.
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  if (lane == 0) sh.warp_best[warp] = order_bits(best);
   __syncthreads();
   if (warp == 0) {
-    b = warp_max(lane < kWarps ? sh.warp_best[lane] : 0ull);
+    const unsigned long long b = warp_max(lane < kWarps ? sh.warp_best[lane] : 0ull);
     if (lane < cl) cluster.map_shared_rank(&sh, lane)->cl_best[rank] = b;
   }
-  if (tid < 2) sh.list_n[tid] = 0;
   cluster.sync();
-  b = 0;
-  for (int i = 0; i < cl; ++i) b = sh.cl_best[i] > b ? sh.cl_best[i] : b;
-  const uint32_t ob = (uint32_t)(b >> 32);
-  const float m = __uint_as_float(ob & 0x80000000u ? ob & 0x7FFFFFFFu : ~ob);
-  const uint32_t mi = 0xFFFFFFFFu - (uint32_t)b;
+  unsigned long long ob = 0;
+  for (int i = 0; i < cl; ++i) ob = sh.cl_best[i] > ob ? sh.cl_best[i] : ob;
+  float m = order_float((uint32_t)ob);
   const bool empty = !valid || m == -CUDART_INF_F;
+  const int k = p.top_k ? __ldg(&p.top_k[r]) : 0;
+  const float tp = p.top_p ? __ldg(&p.top_p[r]) : 1.f;
   float* probs = p.probs ? p.probs + (int64_t)r * p.vocab + start : nullptr;
-  if (empty || greedy) {  // uniform over the cluster; no remote access follows
+  if (empty) {  // uniform over the cluster; no remote access follows
     if (rank == 0 && tid == 0) {
-      p.token[r] = empty ? -1 : (int)mi;
-      if (p.logprob) p.logprob[r] = empty ? -CUDART_INF_F : 0.f;
-      if (p.kept) p.kept[r] = empty ? 0 : 1;
+      p.token[r] = -1;
+      if (p.logprob) p.logprob[r] = -CUDART_INF_F;
+      if (p.kept) p.kept[r] = 0;
     }
     if (probs)
-      for (int i = tid; i < n; i += kThreads) probs[i] = !empty && start + i == (int)mi ? 1.f : 0.f;
+      for (int i = tid; i < n; i += kThreads) probs[i] = 0.f;
     return;
   }
-  Sampler s(sh, z4, mis + n, (uint32_t)(start - mis));
+  if (m == CUDART_INF_F) {
+    // Only the infinite ones count, all alike: make them 0 and the rest -inf.
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads)
+      zbuf[mis + i] = scaled(L::value(zbuf[mis + i]), L::kScaled ? 1.f : inv) == CUDART_INF_F ? L::zero() : L::none();
+    sc.inv = 1.f;
+    m = 0.f;
+    __syncthreads();
+  }
+  Sampler<T> s(sh, sc, mis + n, (uint32_t)(start - mis));
   s.row.m = m;
-  s.row.inf = m == CUDART_INF_F;
-  s.row.least = m - kCut;  // +inf where m is: only those count
+  s.row.least = m - kCut;
   const float mp = p.min_p ? __ldg(&p.min_p[r]) : 0.f;
   s.row.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;  // the best token passes
   s.row.key_max = kKeyAll;
-  const int k = p.top_k ? __ldg(&p.top_k[r]) : 0;
-  const float tp = p.top_p ? __ldg(&p.top_p[r]) : 1.f;
+  if (greedy || tp <= 0.f) {
+    // Only the best token, the lowest index among equals: the least key.
+    s.row.least = m;
+    unsigned long long low, high;
+    s.key_range([&](auto f) { s.each([&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
+    if (tid < cl) cluster.map_shared_rank(&sh, tid)->cl_low[rank] = low;
+    cluster.sync();
+    for (int i = 0; i < cl; ++i) low = sh.cl_low[i] < low ? sh.cl_low[i] : low;
+    s.row.set_max(low);
+  }
   const float u = __ldg(&p.u[r]);
   Match all;
-  all.level = all.b0 = all.b1 = all.shift = 0;
-  all.prefix = 0;
+  all.level = all.b0 = 0;
+  all.lo = all.hi = 0;
   bool short_list = false;
   unsigned long long total = 0;
   uint32_t kept = 0;
-  const bool use_k = k > 0 && k < p.vocab, use_p = tp < 1.f && tp > 0.f;
-  if (tp <= 0.f) s.row.set_max(rank_key(m, mi));
+  const bool one = s.row.key_max != kKeyAll;
+  const bool use_k = k > 0 && k < p.vocab && !one, use_p = tp < 1.f && !one;
   for (int search = 0; search < 2 && !short_list; ++search) {  // 0: top-k, 1: top-p of what it left
     if (search == 0 ? !use_k : !use_p) continue;
     Target tg;
     tg.by_count = search == 0;
     tg.count = search == 0 ? (uint32_t)k : 0u;
     tg.bound = (double)tp;
-    s.histogram(all, search == 1);
+    s.histogram(all, search == 1, Pieces(0, 0));
     if (!s.find_bin(tg, 0u, 0ull, search == 1)) continue;
-    short_list = sh.f_before_cnt + sh.f_cnt <= kList;
+    short_list = sh.f_before_cnt + sh.f_cnt <= kShort;
     if (short_list) {
       Match to;
       to.level = -1;
       to.b0 = (int)sh.f_bin;
-      s.gather(to, search);  // no remote access follows
+      s.gather(to);  // no remote access follows
       const int cnt = (int)(sh.f_before_cnt + sh.f_cnt);
       bool mine;
       uint32_t idx, w;
-      s.finish(search, cnt, search == 0 && use_k ? k : 0, tp, search == 1 ? tg.bound : -1.0, u, total, kept, mine, idx, w);
+      s.finish(cnt, search == 0 && use_k ? k : 0, tp, search == 1 ? tg.bound : -1.0, u, total, kept, mine, idx, w);
       if (rank == 0 && mine) {
         p.token[r] = (int)idx;
         if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
       }
     } else {
-      s.row.set_max(s.resolve(tg, search, search == 1));
+      s.row.set_max(s.resolve(tg, search == 1));
     }
   }
   // Kept weight by warp: warp w owns a contiguous piece of the CTA's groups
@@ -602,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   const int piece = (((s.n4 + kWarps - 1) / kWarps) + 31) & ~31;
   const int p0 = warp * piece < s.n4 ? warp * piece : s.n4, p1 = p0 + piece < s.n4 ? p0 + piece : s.n4;
   auto kept4 = [&](int v, uint32_t (&w)[4]) {
-    const float4 x = z4[v];
+    const float4 x = sc.get(v);
     w[0] = row.kept(x.x, (uint32_t)(base + 4 * v));
     w[1] = row.kept(x.y, (uint32_t)(base + 4 * v + 1));
     w[2] = row.kept(x.z, (uint32_t)(base + 4 * v + 2));
@@ -611,12 +747,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   if (!short_list) {
     unsigned long long sum = 0;
     uint32_t cnt = 0;
+    if (row.key_max == kKeyAll && row.min_p == 0.f) {  // no filter: exp and add
 #pragma unroll 2
-    for (int v = p0 + lane; v < p1; v += 32) {
-      uint32_t w[4];
-      kept4(v, w);
+      for (int v = p0 + lane; v < p1; v += 32) {
+        const float4 x = sc.get(v);
+        const float z[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += w[e], cnt += w[e] != 0u;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = Row::fixed(row.w(z[e]));
+          sum += w;
+          cnt += w != 0u;
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int v = p0 + lane; v < p1; v += 32) {
+        uint32_t w[4];
+        kept4(v, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += w[e], cnt += w[e] != 0u;
+      }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
@@ -641,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
       total += sh.cl_sum[i];
       kept += sh.cl_cnt[i];
     }
-    const unsigned long long target = Sampler::draw(u, total);
+    const unsigned long long target = Sampler<T>::draw(u, total);
     for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
     if (target >= before && target < before + sum) {  // one warp of the cluster
       unsigned long long run = before;
@@ -696,13 +846,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
 
 template <typename T>
 cudaError_t launch(SampleParams p, cudaStream_t s) {
-  // CTAs of a row: two CTAs of up to 16,384 scores fit an SM; more a row while
-  // all of them still run at once, down to 2,048 scores each.
+  // CTAs of a row: few enough scores that two CTAs fit an SM (kMostBytes); more
+  // a row while all of them still run at once, down to 2,048 scores each.
   int cl = 1;
   auto piece = [&](int c) { return (p.vocab + c - 1) / c; };
-  while (cl < kMaxCl && (piece(cl) > 16384 || (2ll * cl * p.rows <= 2 * kNumSMs && piece(cl) > 4096))) cl *= 2;
+  while (cl < kMaxCl && (piece(cl) > kMostScores || piece(cl) * (int)sizeof(T) > kMostBytes ||
+                         (2ll * cl * p.rows <= 2 * kNumSMs && piece(cl) > 4096)))
+    cl *= 2;
   p.chunk = (piece(cl) + 7) & ~7;
-  const size_t smem = ((sizeof(SampleShared) + 31) & ~(size_t)31) + (size_t)(p.chunk + 16) * 4;
+  const size_t smem = ((sizeof(SampleShared) + 31) & ~(size_t)31) + (size_t)(p.chunk + 16) * sizeof(T);
   auto kern = k_sample<T>;
   cudaError_t err = ensure_smem_attr((const void*)kern, smem);
   if (err != cudaSuccess) return err;
