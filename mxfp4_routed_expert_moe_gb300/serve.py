@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import MoeError, _check, _dtype_of, _ptr, _stream, lib
+from . import DT_BF16, DT_F32, MoeError, _check, _ptr, lib
 
 __all__ = ["KVCache", "KVBatch", "kv_append", "prefix_attention", "attention_workspace_bytes", "sample",
            "rope_table", "SERVE_EXPORTS", "SAMPLE_MAX_VOCAB", "SERVE_MAX_BATCH"]
@@ -29,13 +29,15 @@ class _Batch(ctypes.Structure):
                 ("prefix_table", ctypes.c_void_p)]
 
 
-_READY = None
+_READY = _TYPES = None
+torch = None  # imported with the library: a build needs neither
 
 
 def _lib():
     """The loaded library with the argument types of this module's calls."""
-    global _READY
+    global _READY, torch, _TYPES
     if _READY is None:
+        import torch as _torch
         L = lib()
         vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         P = ctypes.POINTER
@@ -45,15 +47,31 @@ def _lib():
         L.moe_attention_workspace_bytes.argtypes = [P(_Cache), P(_Batch), i32]
         L.moe_prefix_attention.argtypes = [P(_Cache), P(_Batch), vp, i32, i64, f32, vp, i64, vp, vp, sz, vp, vp]
         L.moe_sample.argtypes = [i32, i32, vp, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        torch = _torch
+        _TYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
         _READY = L
     return _READY
 
 
+def _stream(stream, t):
+    """The raw stream: the given one, or the current one of the tensor's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dtype_of(t, what):
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what} must be torch.float32 or torch.bfloat16, not {t.dtype}")
+    return dt
+
+
 def _want(t, what, dtype, shape=None):
-    """Checks a tensor argument: its type, shape (None: any) and that it is contiguous."""
-    if str(t.dtype) != "torch." + dtype:
-        raise TypeError(f"{what} must be torch.{dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    """Address of a tensor argument, after checks of its type, shape (None: any) and contiguity."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
@@ -65,8 +83,9 @@ class KVCache:
     order (head-major pages, one tensor that holds both) are taken as they are, by their strides."""
 
     def __init__(self, k, v):
+        _lib()
         for t, what in ((k, "k"), (v, "v")):
-            if str(t.dtype) != "torch.bfloat16":
+            if t.dtype is not torch.bfloat16:
                 raise TypeError(f"the cache's {what} must be torch.bfloat16, not {t.dtype}")
             if t.dim() != 4 or t.stride(3) != 1:
                 raise ValueError(f"the cache's {what} must be [pages][page_size][kv_heads][head_dim], contiguous in the last")
@@ -90,19 +109,20 @@ class KVBatch:
     in place between calls."""
 
     def __init__(self, kv_len, table, tokens=None, q_start=None, max_q=1, prefix_table=None, prefix_len=0):
+        _lib()
         B = kv_len.shape[0]
         if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("table must be [batch][pages], contiguous in the last")
-        if str(table.dtype) != "torch.int32":
+        if table.dtype is not torch.int32:
             raise TypeError(f"table must be torch.int32, not {table.dtype}")
         if prefix_len > 0 and (prefix_table is None or prefix_table.numel() < 1):
             raise ValueError("a prefix needs its page table")
         stride = table.stride(0) if B > 1 else max(table.stride(0), table.shape[1])
         self.kv_len, self.table, self.q_start, self.prefix_table = kv_len, table, q_start, prefix_table
         self.struct = _Batch(B, B if tokens is None else tokens, max_q, stride, table.shape[1], prefix_len,
-                             None if q_start is None else _want(q_start, "q_start", "int32", (B + 1,)),
-                             _want(kv_len, "kv_len", "int32", (B,)), table.data_ptr(),
-                             None if prefix_table is None else _want(prefix_table, "prefix_table", "int32"))
+                             None if q_start is None else _want(q_start, "q_start", torch.int32, (B + 1,)),
+                             _want(kv_len, "kv_len", torch.int32, (B,)), table.data_ptr(),
+                             None if prefix_table is None else _want(prefix_table, "prefix_table", torch.int32))
         self.prefix_tokens = 0 if prefix_table is None else prefix_table.numel()
         self.ref = ctypes.byref(self.struct)
         self.tokens = self.struct.tokens
@@ -114,11 +134,12 @@ class KVBatch:
 
 def _rows(x, what, tokens, heads, dim):
     """[tokens][heads][dim] with the heads of a token side by side: the stride between tokens."""
-    if tuple(x.shape) != (tokens, heads, dim):
+    if x.shape != (tokens, heads, dim):
         raise ValueError(f"{what} must have shape {(tokens, heads, dim)}, not {tuple(x.shape)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+    row, head, one = x.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return x.stride(0) if tokens > 1 else heads * dim
+    return row if tokens > 1 else heads * dim
 
 
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -138,29 +159,30 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope=Non
     by the rows of ``rope`` (see :func:`rope_table`)."""
     n, dim = batch.tokens, cache.dim
     ks, vs = _rows(k, "k", n, cache.heads, dim), _rows(v, "v", n, cache.heads, dim)
-    dt = _dtype_of(k)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    dt = _dtype_of(k, "k")
+    if v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
         raise TypeError("q, k and v must have one type")
-    qh = qs = os = 0
+    qh = qs = os = rows = 0
+    qp = op = rp = None
     if q is not None:
         qh = q.shape[1]
         qs = _rows(q, "q", n, qh, dim)
-        if q_out is not None:
-            if str(q_out.dtype) != "torch.bfloat16":
-                raise TypeError(f"q_out must be torch.bfloat16, not {q_out.dtype}")
-            os = _rows(q_out, "q_out", n, qh, dim)
-    rows = 0
+        qp = q.data_ptr()
+    if q_out is not None:
+        if q_out.dtype is not torch.bfloat16:
+            raise TypeError(f"q_out must be torch.bfloat16, not {q_out.dtype}")
+        os = _rows(q_out, "q_out", n, qh, dim)
+        op = q_out.data_ptr()
     if rope is not None:
-        _want(rope, "rope", "float32", (rope.shape[0], rot_dim))
         rows = rope.shape[0]
-    _check(_lib().moe_kv_append(cache.ref, batch.ref, dt, _ptr(q), k.data_ptr(), v.data_ptr(), qh, qs, ks, vs,
-                                _ptr(q_out), os, _ptr(rope), rows, int(rot_dim), int(bool(interleaved)), _ptr(status),
-                                _stream(stream)), "moe_kv_append")
+        rp = _want(rope, "rope", torch.float32, (rows, rot_dim))
+    _check(_READY.moe_kv_append(cache.ref, batch.ref, dt, qp, k.data_ptr(), v.data_ptr(), qh, qs, ks, vs, op, os, rp, rows,
+                                rot_dim, bool(interleaved), _ptr(status), _stream(stream, k)), "moe_kv_append")
 
 
 def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int) -> int:
     """moe_attention_workspace_bytes; raises MoeError where moe_prefix_attention would refuse the arguments."""
-    n = int(_lib().moe_attention_workspace_bytes(cache.ref, batch.ref, int(q_heads)))
+    n = int(_READY.moe_attention_workspace_bytes(cache.ref, batch.ref, int(q_heads)))
     if n == 0:
         raise MoeError(1, "moe_attention_workspace_bytes")
     return n
@@ -173,16 +195,13 @@ def prefix_attention(cache: KVCache, batch: KVBatch, q, out, ws, scale=None, lse
     n, dim = batch.tokens, cache.dim
     qh = q.shape[1]
     qs, os = _rows(q, "q", n, qh, dim), _rows(out, "out", n, qh, dim)
-    for t, what in ((q, "q"), (out, "out")):
-        if str(t.dtype) != "torch.bfloat16":
-            raise TypeError(f"{what} must be torch.bfloat16, not {t.dtype}")
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16:
+        raise TypeError(f"q and out must be torch.bfloat16, not {q.dtype} and {out.dtype}")
     batch.check_prefix(cache)
-    if lse is not None:
-        _want(lse, "lse", "float32", (n, qh))
-    _check(_lib().moe_prefix_attention(cache.ref, batch.ref, q.data_ptr(), qh, qs,
-                                       dim ** -0.5 if scale is None else float(scale), out.data_ptr(), os, _ptr(lse),
-                                       ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)),
-           "moe_prefix_attention")
+    lp = None if lse is None else _want(lse, "lse", torch.float32, (n, qh))
+    _check(_READY.moe_prefix_attention(cache.ref, batch.ref, q.data_ptr(), qh, qs, dim ** -0.5 if scale is None else scale,
+                                       out.data_ptr(), os, lp, ws.data_ptr(), ws.nbytes, _ptr(status),
+                                       _stream(stream, q)), "moe_prefix_attention")
 
 
 def sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None, kept=None,
@@ -192,14 +211,19 @@ def sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=Non
     (int32) are [rows] device tensors or None; ``logprob`` [rows] fp32, ``kept`` [rows] int32 and ``probs``
     [rows][vocab] fp32 receive the token's log-probability, the number of tokens kept and their
     probabilities."""
+    L = _lib()
     rows, vocab = logits.shape
-    if vocab > 1 and logits.stride(1) != 1:
+    stride, one = logits.stride()
+    if vocab > 1 and one != 1:
         raise ValueError("logits must be contiguous in the last dimension")
-    opt = lambda t, what, dt, shape=(rows,): None if t is None else _want(t, what, dt, shape)  # noqa: E731
-    stride = logits.stride(0) if rows > 1 else vocab
-    _check(_lib().moe_sample(rows, vocab, logits.data_ptr(), _dtype_of(logits), stride, _want(u, "u", "float32", (rows,)),
-                             opt(temperature, "temperature", "float32"), opt(top_k, "top_k", "int32"),
-                             opt(top_p, "top_p", "float32"), opt(min_p, "min_p", "float32"),
-                             _want(token, "token", "int32", (rows,)), opt(logprob, "logprob", "float32"),
-                             opt(kept, "kept", "int32"), opt(probs, "probs", "float32", (rows, vocab)),
-                             _stream(stream)), "moe_sample")
+    f32, i32, row = torch.float32, torch.int32, (rows,)
+    _check(L.moe_sample(rows, vocab, logits.data_ptr(), _dtype_of(logits, "logits"), stride if rows > 1 else vocab,
+                        _want(u, "u", f32, row),
+                        None if temperature is None else _want(temperature, "temperature", f32, row),
+                        None if top_k is None else _want(top_k, "top_k", i32, row),
+                        None if top_p is None else _want(top_p, "top_p", f32, row),
+                        None if min_p is None else _want(min_p, "min_p", f32, row), _want(token, "token", i32, row),
+                        None if logprob is None else _want(logprob, "logprob", f32, row),
+                        None if kept is None else _want(kept, "kept", i32, row),
+                        None if probs is None else _want(probs, "probs", f32, (rows, vocab)),
+                        _stream(stream, logits)), "moe_sample")
