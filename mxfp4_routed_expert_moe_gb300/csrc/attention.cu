@@ -1,5 +1,6 @@
 // attention.cu — attention over the paged cache: the warp kernel (few query
-// rows per key head) and the kernel that joins partial sums.
+// rows per key head), the kernel that joins partial sums, and the tile kernel
+// (small problems, in one launch).
 //
 // For a query row q and its tokens j, with t_j = scale log2(e) q.k_j:
 //   m = max t_j,  l = sum 2^(t_j - m),  o = sum 2^(t_j - m) v_j
@@ -7,11 +8,15 @@
 //   M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i,
 //   lse = (M + log2 l) ln 2.
 // A part without visible tokens has m = -inf, l = 0, o = 0 and drops out.
+#include <cooperative_groups.h>
+
 #include "serve.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------- warp kernel --
 // For parts of at most 16 query rows per key head: decode.  Bound by HBM: 4 *
@@ -66,6 +71,146 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t keep_tokens(uint32_t v, int t, int n) {
   return t + 1 < n ? v : (t < n ? v & 0xFFFFu : 0u);
 }
+
+// The rows of a 16-row tile as one warp holds them: lane l has rows l / 4 and
+// l / 4 + 8 in MMA fragments.
+template <int D>
+struct WarpRows {
+  static constexpr int NT = D / 8;
+  uint32_t qf[D / 16][4];
+  float o[NT][4];
+  float m[2], l[2];
+
+  // Rows row0 .. row0 + rows - 1 of a set whose first token is tok0.
+  __device__ __forceinline__ void load(const AttnParams& p, int tok0, int kvh, int row0, int rows) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      const bool in = r < rows;
+      const int rr = row0 + (in ? r : 0), i = rr / p.group;
+      const uint16_t* src = p.q + (int64_t)(tok0 + i) * p.q_stride + (int64_t)(kvh * p.group + rr - i * p.group) * D +
+                            2 * (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][h] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
+        qf[kk][h + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m[0] = m[1] = -CUDART_INF_F;
+    l[0] = l[1] = 0.f;
+  }
+
+  // One unit: 32 tokens of K at kb and V at vb.  With `edge`, row h sees its
+  // first see[h] tokens and the V rows from n on are not to be used.
+  __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, float scale_log2, bool edge, const int (&see)[2], int n) {
+    constexpr int kHalf = WarpCfg<D>::kHalf;
+    const int lane = threadIdx.x & 31;
+    float sc[kUnit / 8][4];
+#pragma unroll
+    for (int i = 0; i < kUnit / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+      for (int j = 0; j < kUnit / 16; ++j) {
+        const int tok = 16 * j + (lane & 7) + ((lane >> 4) << 3);
+        const int c = (kk & 3) * 2 + ((lane >> 3) & 1);
+        uint32_t b[4];
+        ldsm4(kb + (kk >> 2) * kHalf + tok * 128 + ((c ^ (tok & 7)) << 4), b);
+        mma_bf16(sc[2 * j], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b[0], b[1]);
+        mma_bf16(sc[2 * j + 1], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b[2], b[3]);
+      }
+    }
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int i = 0; i < kUnit / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float t = sc[i][e] * scale_log2;
+        if (edge && 8 * i + 2 * (lane & 3) + (e & 1) >= see[e >> 1]) t = -CUDART_INF_F;
+        sc[i][e] = t;
+        mx[e >> 1] = fmaxf(mx[e >> 1], t);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
+    }
+    if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = mx[h] > m[h] ? ex2(m[h] - mx[h]) : 1.f;
+        m[h] = mx[h];
+        l[h] *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i][2 * h] *= f, o[i][2 * h + 1] *= f;
+      }
+    }
+    const float ms[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
+#pragma unroll
+    for (int j = 0; j < kUnit / 16; ++j) {
+      uint32_t a[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* s4 = sc[2 * j + i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s4[e] = ex2(s4[e] - ms[e >> 1]);
+          l[e >> 1] += s4[e];
+        }
+        // bf16 weights: at most 2^-8 relative each, averaged over the sum,
+        // below the rounding of the bf16 output.
+        a[2 * i] = pack_bf16(s4[0], s4[1]);
+        a[2 * i + 1] = pack_bf16(s4[2], s4[3]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        const int tok = 16 * j + (lane & 15);
+        const int c = (t & 7) + (lane >> 4);
+        uint32_t b[4];
+        ldsm4t(vb + (t >> 3) * kHalf + tok * 128 + ((c ^ (tok & 7)) << 4), b);
+        if (edge) {
+          // Rows of V past the length may hold anything: 0 * NaN is NaN.
+          const int tk = 16 * j + 2 * (lane & 3);
+          b[0] = keep_tokens(b[0], tk, n);
+          b[1] = keep_tokens(b[1], tk + 8, n);
+          b[2] = keep_tokens(b[2], tk, n);
+          b[3] = keep_tokens(b[3], tk + 8, n);
+        }
+        mma_bf16(o[t], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_bf16(o[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+      }
+    }
+  }
+
+  // The four lanes of a row add up its sum.
+  __device__ __forceinline__ void close() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
+    }
+  }
+
+  // o to rows of D at `dst`, m and l to ml[row], ml[16 + row].
+  __device__ __forceinline__ void store(float* dst, float* ml, int rows) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(dst + r * D + 8 * n + 2 * (lane & 3)) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+      if ((lane & 3) == 0) {
+        ml[r] = m[h];
+        ml[kAttnWarpRows + r] = l[h];
+      }
+    }
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kWorkers * 32, 1)
@@ -153,34 +298,19 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
   };
   fill();
   // ------------------------------------------------------------------- sums --
-  constexpr int NT = D / 8;
   bool alive = true;
+  WarpRows<D> rows;
   while (alive && seg_out != seg_in) {
     const AttnSeg g = segs[seg_out & 7];
-    // This thread's two rows and their queries, as MMA fragments.
-    const int r0 = lane >> 2;
-    uint32_t qf[D / 16][4];
+    rows.load(p, g.tok0, g.kvh, g.row0, g.rows);
     int vis[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = r0 + 8 * h;
-      const bool in = r < g.rows;
-      const int i = in ? r / p.group : 0;  // a part of at most 16 rows is one tile: row0 = 0
-      vis[h] = in ? attn_visible(p, g, i) : 0;
-      const uint16_t* src = p.q + (int64_t)(g.tok0 + i) * p.q_stride +
-                            (int64_t)(g.kvh * p.group + (in ? r : 0) - i * p.group) * D + 2 * (lane & 3);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        qf[kk][h] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
-        qf[kk][h + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
-      }
+      const int r = (lane >> 2) + 8 * h;
+      vis[h] = r < g.rows ? attn_visible(p, g, (g.row0 + r) / p.group) : 0;
     }
     // Units that end above the first row's tokens need the mask.
-    const int vis_min = attn_visible(p, g, 0);
-    float o[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    const int vis_min = attn_visible(p, g, g.row0 / p.group);
     for (int kv = g.kv0; kv < g.kv1; kv += kUnit) {
       const int st = un % C::kStages;
       alive = __all_sync(0xFFFFFFFFu, mbar_wait_for(&full[st], (un / C::kStages) & 1, p.wait_limit));
@@ -188,107 +318,17 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
         set_status_word(p.status, MOE_ERR_TIMEOUT);
         break;
       }
-      const uint32_t kb = smem_u32(ring + st * C::kStage), vb = kb + C::kMat;
-      const bool edge = kv + kUnit > vis_min;
-      // Scores of 16 rows x 32 tokens.
-      float sc[kUnit / 8][4];
-#pragma unroll
-      for (int i = 0; i < kUnit / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-        for (int j = 0; j < kUnit / 16; ++j) {
-          const int tok = 16 * j + (lane & 7) + ((lane >> 4) << 3);
-          const int c = (kk & 3) * 2 + ((lane >> 3) & 1);
-          uint32_t b[4];
-          ldsm4(kb + (kk >> 2) * C::kHalf + tok * 128 + ((c ^ (tok & 7)) << 4), b);
-          mma_bf16(sc[2 * j], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b[0], b[1]);
-          mma_bf16(sc[2 * j + 1], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b[2], b[3]);
-        }
-      }
-      float mx[2] = {m[0], m[1]};
-#pragma unroll
-      for (int i = 0; i < kUnit / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float t = sc[i][e] * p.scale_log2;
-          if (edge && kv + 8 * i + 2 * (lane & 3) + (e & 1) >= vis[e >> 1]) t = -CUDART_INF_F;
-          sc[i][e] = t;
-          mx[e >> 1] = fmaxf(mx[e >> 1], t);
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-      }
-      if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = mx[h] > m[h] ? ex2(m[h] - mx[h]) : 1.f;
-          m[h] = mx[h];
-          l[h] *= f;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) o[i][2 * h] *= f, o[i][2 * h + 1] *= f;
-        }
-      }
-      const float ms[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
-#pragma unroll
-      for (int j = 0; j < kUnit / 16; ++j) {
-        uint32_t a[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float* s4 = sc[2 * j + i];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s4[e] = ex2(s4[e] - ms[e >> 1]);
-            l[e >> 1] += s4[e];
-          }
-          // bf16 weights: at most 2^-8 relative each, averaged over the sum,
-          // below the rounding of the bf16 output.
-          a[2 * i] = pack_bf16(s4[0], s4[1]);
-          a[2 * i + 1] = pack_bf16(s4[2], s4[3]);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          const int tok = 16 * j + (lane & 15);
-          const int c = (n & 7) + (lane >> 4);
-          uint32_t b[4];
-          ldsm4t(vb + (n >> 3) * C::kHalf + tok * 128 + ((c ^ (tok & 7)) << 4), b);
-          if (edge) {
-            // Rows of V past the length may hold anything: 0 * NaN is NaN.
-            const int tk = kv + 16 * j + 2 * (lane & 3);
-            b[0] = keep_tokens(b[0], tk, g.kv1);
-            b[1] = keep_tokens(b[1], tk + 8, g.kv1);
-            b[2] = keep_tokens(b[2], tk, g.kv1);
-            b[3] = keep_tokens(b[3], tk + 8, g.kv1);
-          }
-          mma_bf16(o[n], a[0], a[1], a[2], a[3], b[0], b[1]);
-          mma_bf16(o[n + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
-        }
-      }
+      const uint32_t kb = smem_u32(ring + st * C::kStage);
+      const int see[2] = {vis[0] - kv, vis[1] - kv};
+      rows.unit(kb, kb + C::kMat, p.scale_log2, kv + kUnit > vis_min, see, g.kv1 - kv);
       ++un;
       __syncwarp();  // every lane has read the stage
       fill();
     }
     if (!alive) break;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-    }
+    rows.close();
     float* slot = sd.slots + (int64_t)g.slot * kAttnWarpRows * (D + 2);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + 8 * h;
-      if (r >= g.rows) continue;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(slot + r * D + 8 * n + 2 * (lane & 3)) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-      if ((lane & 3) == 0) {
-        slot[kAttnWarpRows * D + r] = m[h];
-        slot[kAttnWarpRows * (D + 1) + r] = l[h];
-      }
-    }
+    rows.store(slot, slot + kAttnWarpRows * D, g.rows);
     ++seg_out;
     fill();
   }
@@ -303,6 +343,180 @@ cudaError_t launch_warp(const AttnParams& p, const CUtensorMap& km, const CUtens
   cudaError_t err = ensure_smem_attr((const void*)k_attn_warp<D>, WarpCfg<D>::kSmem);
   if (err != cudaSuccess) return err;
   return launch_pdl(k_attn_warp<D>, dim3(p.side[0].ctas), dim3(kWorkers * 32), WarpCfg<D>::kSmem, s, p, km, vm);
+}
+
+// ------------------------------------------------------------- tile kernel --
+// Small problems, where launches and latencies are the time: one launch, no
+// plan, no joining kernel.  A cluster takes 16 rows of one (sequence, key head)
+// over everything they see, the prefix and then the own part; its warps take
+// the units of 32 tokens in turn and join through (distributed) shared memory.
+// A prefix is read once per sequence here, from L2.
+struct TileShared {
+  uint64_t full[kWorkers][4];
+  float ml[kWorkers][2 * kAttnWarpRows];  // m, l of each warp's rows
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWorkers * 32, 1)
+    k_attn_tile(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = WarpCfg<D>;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ TileShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cl = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = dyn + warp * (C::kStages * C::kStage);
+  uint64_t* full = sh.full[warp];
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+  pdl_trigger();
+  pdl_wait();
+  const int tile = blockIdx.x / cl;
+  const int rt = tile % p.tile_rows, kvh = tile / p.tile_rows % p.kv_heads, b = tile / p.tile_rows / p.kv_heads;
+  const AttnRaw raw = attn_load(p, b);
+  const int ql = raw.q1 - raw.q0, row0 = rt * kAttnWarpRows;
+  if (!attn_valid(p, raw)) return;  // uniform over the cluster, like all of the above
+  const int rows = ql * p.group - row0 < kAttnWarpRows ? ql * p.group - row0 : kAttnWarpRows;
+  if (rows <= 0) return;
+  // Own tokens that row r sees: len - ql + 1 + its token, within [0, len].
+  auto visible = [&](int r) {
+    const int v = raw.len - ql + 1 + (row0 + r) / p.group;
+    return v < 0 ? 0 : (v > raw.len ? raw.len : v);
+  };
+  const int own_end = visible(rows - 1), own_all = visible(0);
+  const int units_p = (p.b.prefix_len + kUnit - 1) / kUnit, units = units_p + (own_end + kUnit - 1) / kUnit;
+  const int box = attn_box(p.page_size, kUnit);
+  const int my_box = lane >> 2, my_half = (lane >> 1) & 1, my_v = lane & 1;
+  const bool my_lane = my_half < D / 64 && my_box * box < kUnit;
+  const int step = cl * kWorkers;
+  auto unit_at = [&](int u, int& kv, int& end) {  // its first token and the end of its part
+    const bool pre = u < units_p;
+    kv = (pre ? u : u - units_p) * kUnit;
+    end = pre ? p.b.prefix_len : own_end;
+    return pre ? p.b.batch : b;
+  };
+  auto fetch = [&](int u) {  // this lane's page of unit u
+    if (u >= units) return 0;
+    int kv, end;
+    const int set = unit_at(u, kv, end);
+    const int tok = kv + my_box * box;
+    return my_lane && tok < end ? __ldg(&attn_table(p, set)[tok >> p.page_shift]) : 0;
+  };
+  auto load = [&](int u, int st, int page) {
+    int kv, end;
+    unit_at(u, kv, end);
+    const int left = end - kv < kUnit ? end - kv : kUnit;
+    const int nb = (left + box - 1) / box;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(nb * box * D * 4));
+    __syncwarp();
+    if (my_lane && my_box < nb) {
+      if (page < 0 || page >= p.num_pages) {
+        set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
+        page = p.num_pages;  // past the map: the box is filled with zeros
+      }
+      tma_load_4d(ring + st * C::kStage + my_v * C::kMat + my_half * C::kHalf + my_box * box * 128, my_v ? &vmap : &kmap,
+                  my_half * 64, (kv + my_box * box) & (p.page_size - 1), kvh, page, &full[st]);
+    }
+    __syncwarp();
+  };
+  const int u0 = warp * cl + rank;  // few units spread over the CTAs first
+  int page[C::kStages], n_in = 0;
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s) page[s] = fetch(u0 + s * step);
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s)
+    if (u0 + s * step < units) {
+      load(u0 + s * step, s, page[s]);
+      ++n_in;
+    }
+  int next = fetch(u0 + C::kStages * step);
+  WarpRows<D> acc;
+  acc.load(p, raw.q0, kvh, row0, rows);
+  int vis[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) vis[h] = (lane >> 2) + 8 * h < rows ? visible((lane >> 2) + 8 * h) : 0;
+  int n = 0;
+  bool alive = true;
+  for (int u = u0; u < units; u += step, ++n) {
+    const int st = n % C::kStages;
+    alive = __all_sync(0xFFFFFFFFu, mbar_wait_for(&full[st], (n / C::kStages) & 1, p.wait_limit));
+    if (!alive) {
+      set_status_word(p.status, MOE_ERR_TIMEOUT);
+      break;
+    }
+    int kv, end;
+    const bool pre = unit_at(u, kv, end) == p.b.batch;
+    const int see[2] = {(pre ? end : vis[0]) - kv, (pre ? end : vis[1]) - kv};
+    const uint32_t kb = smem_u32(ring + st * C::kStage);
+    acc.unit(kb, kb + C::kMat, p.scale_log2, kv + kUnit > (pre ? end : own_all), see, end - kv);
+    __syncwarp();  // every lane has read the stage
+    if (u + C::kStages * step < units) {
+      load(u + C::kStages * step, st, next);
+      ++n_in;
+      next = fetch(u + (C::kStages + 1) * step);
+    }
+  }
+  // Copies still in flight after a wait gave up must land before the ring is
+  // used again or left.
+  for (int i = n; i < n_in; ++i)
+    if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+  acc.close();
+  acc.store(reinterpret_cast<float*>(ring), sh.ml[warp], rows);
+  cluster.sync();
+  // CTA `rank` joins rows rank, rank + cl, ...: D / 4 threads a row, the warps
+  // in order.
+  constexpr int L = D / 4;
+  static_assert(C::kStages * C::kStage >= kAttnWarpRows * D * 4, "a warp's ring holds its sums");
+  for (int i = threadIdx.x; i < (rows - rank + cl - 1) / cl * L; i += kWorkers * 32) {
+    const int r = rank + i / L * cl, col = i % L * 4;
+    float mx = -CUDART_INF_F;
+    for (int w = 0; w < step; ++w) mx = fmaxf(mx, cluster.map_shared_rank(&sh, w % cl)->ml[w / cl][r]);
+    float acc4[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+    for (int w = 0; w < step; ++w) {
+      const TileShared* o = cluster.map_shared_rank(&sh, w % cl);
+      const float m = o->ml[w / cl][r];
+      const float f = m == -CUDART_INF_F ? 0.f : ex2(m - mx);
+      l += o->ml[w / cl][kAttnWarpRows + r] * f;  // a NaN sum stays one
+      const float4 v = *reinterpret_cast<const float4*>(
+          cluster.map_shared_rank(dyn, w % cl) + (w / cl) * (C::kStages * C::kStage) + (r * D + col) * 4);
+      if (f > 0.f) {
+        acc4[0] = fmaf(f, v.x, acc4[0]);
+        acc4[1] = fmaf(f, v.y, acc4[1]);
+        acc4[2] = fmaf(f, v.z, acc4[2]);
+        acc4[3] = fmaf(f, v.w, acc4[3]);
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int rr = row0 + r, tok = rr / p.group, head = kvh * p.group + rr - tok * p.group;
+    *reinterpret_cast<uint2*>(p.out + (int64_t)(raw.q0 + tok) * p.out_stride + head * D + col) =
+        make_uint2(pack_bf16(acc4[0] * inv, acc4[1] * inv), pack_bf16(acc4[2] * inv, acc4[3] * inv));
+    if (p.lse && col == 0)
+      p.lse[(int64_t)(raw.q0 + tok) * p.q_heads + head] = l == 0.f ? -CUDART_INF_F : (mx + log2f(l)) * 0.69314718055994531f;
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+template <int D>
+cudaError_t launch_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
+  cudaError_t err = ensure_smem_attr((const void*)k_attn_tile<D>, WarpCfg<D>::kSmem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.b.batch * p.kv_heads * p.tile_rows * cl));
+  cfg.blockDim = dim3(kWorkers * 32);
+  cfg.dynamicSmemBytes = WarpCfg<D>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_attn_tile<D>, p, km, vm);
 }
 
 // --------------------------------------------------------------- join kernel --
@@ -531,6 +745,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
 
 cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
   return p.head_dim == 128 ? launch_warp<128>(p, km, vm, s) : launch_warp<64>(p, km, vm, s);
+}
+
+cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
+  return p.head_dim == 128 ? launch_tile<128>(p, cl, km, vm, s) : launch_tile<64>(p, cl, km, vm, s);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s) {

@@ -11,6 +11,9 @@
 //   * one thread issues the MMAs: S_t = Q_t K^T and O_t += P_t V for the two
 //     128-row halves t of the tile, S and O in Tensor Memory (S_0, S_1, O_0,
 //     O_1: 128 columns each, all 512 at head_dim 128);
+//   * a warp walks the CTA's range and hands its segments on through shared
+//     memory, so that the others hold no walk state (with it the softmax
+//     spilled, and its spills went past the 28 KB that L1 has left);
 //   * warpgroup t turns S_t into P_t = 2^(S_t scale - m) in bf16, written over
 //     S_t, one row per thread, so that row sums and maxima need no exchange.
 // While one half's softmax runs, the other half's MMAs do.  The reference m of
@@ -25,8 +28,9 @@ namespace {
 
 constexpr int kUnit = kAttnTcUnit;       // tokens
 constexpr int kHalfRows = 128;           // rows of an MMA tile
-constexpr int kThreads = 12 * 32;        // 2 x 4 softmax warps, producer, MMA, two idle
+constexpr int kThreads = 12 * 32;        // 2 x 4 softmax warps, producer, MMA, walk, one idle
 constexpr int kBufs = 5;
+constexpr int kSegs = 4;                 // segments handed from the walking warp to the others
 constexpr uint32_t kTmemCols = 512;
 // Registers: 168 a thread at launch (384 * 168 = 64,512); the softmax
 // warpgroups take 224 each, which holds a row of 128 scores, and the third
@@ -43,6 +47,8 @@ struct TcCfg {
 
 struct TcShared {
   uint64_t full[kBufs], empty[kBufs];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  AttnSeg seg[kSegs];
   uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -156,6 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.o_done[t], 1);
     }
     mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], 10);
+    }
     sh.abort_flag = 0;
     mbar_init_fence();
   }
@@ -165,22 +175,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   // else (see k_attn_warp).
   pdl_wait();
   pdl_trigger();
-  AttnWalk w;
   long long total;
   const long long per = attn_plan<1>(p, sd, sh.plan, total);
-  const bool work = attn_begin<1>(p, sd, sh.plan, 0, per, total, w);
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  AttnSeg g;
   uint8_t* ring = dyn + 2 * C::kMat;
+  // The n-th segment of the range, null past the last one or when a wait gave
+  // up; release it when it is no longer read.
+  uint32_t nseg = 0;
+  auto take_seg = [&]() -> const AttnSeg* {
+    const bool got = tc_wait(sh, &sh.seg_full[nseg % kSegs], (nseg / kSegs) & 1, p);
+    const AttnSeg* g = &sh.seg[nseg % kSegs];
+    return __all_sync(0xFFFFFFFFu, got) && g->slot >= 0 ? g : nullptr;
+  };
+  auto drop_seg = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.seg_empty[nseg % kSegs]);
+    ++nseg;
+  };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (work && warp == 8) {
+    if (warp == 8) {
     // ------------------------------------------------------------ producer --
     const int box = attn_box(p.page_size, kUnit);
     int bi = 0, use = 0;
     bool ok = true;
-    while (ok && attn_next(p, sd, w, g)) {
+    while (ok) {
+      const AttnSeg* sg = take_seg();
+      if (!sg) break;
+      const AttnSeg g = *sg;
+      drop_seg();
       const int32_t* table = attn_table(p, g.set);
       for (int kv = g.kv0; kv < g.kv1 && ok; kv += kUnit) {
         const int left = g.kv1 - kv < kUnit ? g.kv1 - kv : kUnit;
@@ -222,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = use + (i < bi ? 1 : 0);
         if (n > 0 && !mbar_wait(&sh.full[i], (n - 1) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
       }
-    } else if (work && warp == 9) {
+    } else if (warp == 9) {
     // ----------------------------------------------------------------- MMA --
     const uint32_t id_s = idesc_bf16_f32(128, kUnit);
     const uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);  // B: N contiguous
@@ -263,10 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // The buffers of the next unit are waited for while MMAs are queued: the
     // time between the last scores of a unit and the next P V is tensor idle.
-    while (ok && attn_next(p, sd, w, g)) {
-      const int nt = (g.kv1 - g.kv0 + kUnit - 1) / kUnit;
+    while (ok) {
+      const AttnSeg* sg = take_seg();
+      if (!sg) break;
+      const int kv0 = sg->kv0, kv1 = sg->kv1;
+      const bool two = sg->rows > kHalfRows;
+      drop_seg();
+      const int nt = (kv1 - kv0 + kUnit - 1) / kUnit;
       if (nt == 0) continue;
-      const bool two = g.rows > kHalfRows;
       int kbuf, vbuf;
       take(kbuf);
       for (int t = 0; t < (two ? 2 : 1); ++t) {
@@ -280,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       take(vbuf);
       if (nt > 1) take(kbuf);
       for (int j = 0; j < nt && ok; ++j) {
-        const int left = g.kv1 - g.kv0 - j * kUnit;
+        const int left = kv1 - kv0 - j * kUnit;
         const bool more = j + 1 < nt;
         if (left < kUnit) {
           // Rows of V past the length may hold anything, and 0 * NaN is NaN.
@@ -317,6 +345,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No MMA may be in flight when Tensor Memory is released.
     commit_one(&sh.drain, one);
     if (!mbar_wait(&sh.drain, 0)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- walk --
+      AttnWalk w;
+      bool more = attn_begin<1>(p, sd, sh.plan, 0, per, total, w);
+      for (;; ++nseg) {
+        if (nseg >= (uint32_t)kSegs &&
+            !__all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.seg_empty[nseg % kSegs], (nseg / kSegs - 1) & 1, p)))
+          break;
+        AttnSeg g;
+        g.slot = -1;
+        more = more && attn_next(p, sd, w, g);
+        if (!more) g.slot = -1;
+        if (lane == 0) {
+          sh.seg[nseg % kSegs] = g;
+          mbar_arrive(&sh.seg_full[nseg % kSegs]);
+        }
+        __syncwarp();
+        if (!more) break;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -327,15 +374,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
     const float c = p.scale_log2;
     uint32_t ns = 0, no = 0;
-    bool ok = work;
-    while (ok && attn_next(p, sd, w, g)) {
-      if (t == 1 && g.rows <= kHalfRows) continue;
-      float* slot = sd.slots + (int64_t)g.slot * sd.rows * (D + 2);
-      uint8_t* qd = dyn + t * C::kMat;
-      const bool in = r < g.rows;
-      const int vis = in ? attn_visible(p, g, (g.row0 + r) / p.group) : 0;
-      const int vis_min = attn_visible(p, g, (g.row0 + t * kHalfRows) / p.group);
-      if (g.kv0 < g.kv1) {
+    bool ok = true;
+    uint8_t* qd = dyn + t * C::kMat;
+    for (;;) {
+      const AttnSeg* sg = take_seg();
+      if (!sg) break;
+      if (t == 1 && sg->rows <= kHalfRows) {
+        drop_seg();
+        continue;
+      }
+      const int kv0 = sg->kv0, kv1 = sg->kv1;
+      const int vis = r < sg->rows ? attn_visible(p, *sg, (sg->row0 + r) / p.group) : 0;
+      const int vis_min = attn_visible(p, *sg, (sg->row0 + t * kHalfRows) / p.group);
+      if (kv0 < kv1) {
+        const int row0 = sg->row0, row_end = row0 + sg->rows, tok0 = sg->tok0, head0 = sg->kvh * p.group;
         // The warp's 32 query rows into the swizzled A tile, whole rows at a
         // time (one row per thread would take 32 lines per load).  The MMAs
         // that read the previous ones are complete: their scores came back.
@@ -346,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int rr = g.row0 + t * kHalfRows + rl + (b + k) * R;
+            const int rr = row0 + t * kHalfRows + rl + (b + k) * R;
             const int ii = rr / p.group;
-            v[k] = rr < g.row0 + g.rows
-                       ? __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(g.tok0 + ii) * p.q_stride +
-                                                              (int64_t)(g.kvh * p.group + rr - ii * p.group) * D + 8 * ch))
+            v[k] = rr < row_end
+                       ? __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)(tok0 + ii) * p.q_stride +
+                                                              (int64_t)(head0 + rr - ii * p.group) * D + 8 * ch))
                        : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
@@ -362,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sh.q_ready[t]);
       }
       float m = -CUDART_INF_F, l = 0.f;
-      for (int kv = g.kv0; kv < g.kv1; kv += kUnit) {
+      for (int kv = kv0; kv < kv1; kv += kUnit) {
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.s_full[t], ns++ & 1, p));
         if (!ok) break;
         tc_fence_after();
@@ -415,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           weights(s, v, m == -CUDART_INF_F ? 0.f : m);
           if (!__any_sync(0xFFFFFFFFu, top > m + kGrow)) break;
           const float mn = top > m + kGrow ? top : m;
-          if (kv != g.kv0) {
+          if (kv != kv0) {
             // O_t is complete up to the previous unit: its MMAs were issued
             // before the scores that just arrived.
             const float f = m == mn ? 1.f : ex2(m - mn);
@@ -439,7 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += sa + sb;
       }
       if (!ok) break;
-      if (g.kv0 < g.kv1) {
+      float* slot = sd.slots + (int64_t)sg->slot * kAttnTcRows * (D + 2);
+      const int rows = sg->rows;
+      if (kv0 < kv1) {
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.o_done[t], no++ & 1, p));
         if (!ok) break;
         tc_fence_after();
@@ -460,16 +514,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 8; ++e) {
             const int rr = 4 * e + (lane >> 3), ro = t * kHalfRows + q * 32 + rr;
             const uint4 x = *reinterpret_cast<const uint4*>(st + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-            if (ro < g.rows) *reinterpret_cast<uint4*>(slot + (int64_t)ro * D + 32 * k + 4 * (lane & 7)) = x;
+            if (ro < rows) *reinterpret_cast<uint4*>(slot + (int64_t)ro * D + 32 * k + 4 * (lane & 7)) = x;
           }
           __syncwarp();
         }
         tc_fence_before();
       }
-      if (in) {
-        slot[sd.rows * D + r] = m;
-        slot[sd.rows * (D + 1) + r] = l;
+      if (r < rows) {
+        slot[kAttnTcRows * D + r] = m;
+        slot[kAttnTcRows * (D + 1) + r] = l;
       }
+      drop_seg();
     }
   }
   tc_fence_before();

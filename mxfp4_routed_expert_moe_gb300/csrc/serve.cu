@@ -75,6 +75,30 @@ void plan_sides(const moe_kv_batch& b, int group, AttnSide (&side)[2]) {
   }
 }
 
+// Whether the tile kernel takes the call, and on clusters of how many CTAs
+// (0: no).  It goes by the most tokens a sequence may have (its table's
+// width): as many CTAs a tile as keep all tiles on the chip at once.  A wave of
+// it costs about 6 us and each unit that a warp takes in turn 1.2 us; the
+// split kernels cost 10 us and more before their first byte, or 30 us where the
+// prefix and the own parts go to two kernels.  Measured at 56 / 8 heads of 128,
+// tile against split: 1 sequence of 200 tokens 6.6 / 12.3 us, of 16,000 (11
+// units in turn) 26.4 / 34.7; 16 of 1,000 14.3 / 16.4, of 4,000 (21 units) 37.7
+// / 36.0; 32 of 100 behind 1,000 (two waves, 6 units each) 28.3 / 33.0; 64 of
+// 200 (four waves) 26.6 / 14.9.
+int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
+  const int64_t row_tiles = ((int64_t)b.max_q * group + kAttnWarpRows - 1) / kAttnWarpRows;
+  const int64_t tiles = b.batch * c.kv_heads * row_tiles;
+  const int64_t units = ((int64_t)b.prefix_len + kAttnWarpUnit - 1) / kAttnWarpUnit +
+                        ((int64_t)b.table_pages * c.page_size + kAttnWarpUnit - 1) / kAttnWarpUnit;
+  int cl = 1;
+  while (cl < 8 && tiles * cl * 2 <= kNumSMs && (int64_t)cl * kAttnWarpWorkers < units) cl *= 2;
+  const int64_t each = (units + cl * kAttnWarpWorkers - 1) / (cl * kAttnWarpWorkers);
+  if (tiles * cl <= kNumSMs) return each <= 16 ? cl : 0;
+  const bool two_kernels = b.prefix_len > 0 && (int64_t)b.tokens * group > kAttnWarpRows &&
+                           (int64_t)b.max_q * group <= kAttnWarpRows;
+  return tiles <= 2 * kNumSMs && two_kernels && each <= 6 ? cl : 0;
+}
+
 size_t side_layout(const moe_kv_batch& b, int group, int kv_heads, int head_dim, AttnSide (&side)[2], void* base) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -197,6 +221,14 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   p.status = status;
   p.wait_limit = wait_limit();
   cudaStream_t s = (cudaStream_t)stream;
+  if (const int cl = tile_cluster(*batch, *cache, p.group)) {
+    CUtensorMap km, vm;
+    const int box = attn_box(cache->page_size, kAttnWarpUnit);
+    if ((st = cache_map(&km, cache, cache->k, box)) != MOE_OK || (st = cache_map(&vm, cache, cache->v, box)) != MOE_OK)
+      return st;
+    p.tile_rows = (int)(((int64_t)batch->max_q * p.group + kAttnWarpRows - 1) / kAttnWarpRows);
+    return cuda_status(launch_attn_tile(p, cl, km, vm, s));
+  }
   for (int i = 1; i >= 0; --i) {
     if (!p.side[i].own && !p.side[i].prefix) continue;
     CUtensorMap km, vm;

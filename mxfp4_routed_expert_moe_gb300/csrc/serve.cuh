@@ -104,6 +104,7 @@ struct AttnParams {
   int kv_heads, head_dim, page_size, page_shift, num_pages;
   moe_kv_batch b;
   AttnSide side[2];    // 0: warp kernel, 1: Tensor Memory kernel
+  int tile_rows;       // tile kernel: row tiles of a sequence and key head
   int32_t* status;
   long long wait_limit;
 };
@@ -136,17 +137,22 @@ struct AttnSet {
   int units;     // units per row tile, with the tile's own cost
 };
 
+// Whether a sequence's entries fit the batch and its table (reported if not).
+__device__ __forceinline__ bool attn_valid(const AttnParams& p, const AttnRaw& r) {
+  if (r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.b.tokens && r.q1 - r.q0 <= p.b.max_q && r.len >= 0 &&
+      r.len <= (long long)p.b.table_pages * p.page_size)
+    return true;
+  set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
+  return false;
+}
+
 __device__ __forceinline__ AttnSet attn_set(const AttnParams& p, const AttnSide& sd, int s, const AttnRaw& r) {
   AttnSet a;
   a.rows = a.tok0 = a.len = a.first_vis = a.tiles = a.units = 0;
   const bool prefix = s == p.b.batch;
   if (!(prefix ? sd.prefix : sd.own)) return a;
   const int ql = r.q1 - r.q0;
-  if (!prefix && (r.q0 < 0 || ql < 0 || r.q1 > p.b.tokens || ql > p.b.max_q || r.len < 0 ||
-                  r.len > (long long)p.b.table_pages * p.page_size)) {
-    set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
-    return a;
-  }
+  if (!prefix && !attn_valid(p, r)) return a;
   if (ql == 0 || r.len == 0) return a;
   a.tok0 = r.q0;
   a.len = r.len;
@@ -363,6 +369,7 @@ __host__ __device__ __forceinline__ int attn_box(int page_size, int unit) { retu
 cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 // The warp kernel: one CTA per SM, six workers in each, tiles of 16 rows,
 // units of 32 tokens.
 constexpr int kAttnWarpCtas = kNumSMs;

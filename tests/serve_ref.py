@@ -21,7 +21,7 @@ def bf16(x):
 class Paged:
     """A cache with pages handed out in a random order, NaN in every row that no token owns."""
 
-    def __init__(self, rng, lens, prefix, page, heads, dim, head_major=False, spare=2):
+    def __init__(self, rng, lens, prefix, page, heads, dim, head_major=False, spare=2, capacity=0):
         t = torch()
         self.page, self.heads, self.dim, self.prefix, self.lens = page, heads, dim, prefix, list(lens)
         npre = -(-prefix // page)
@@ -29,7 +29,7 @@ class Paged:
         self.pages = npre + sum(own) + spare
         order = rng.permutation(self.pages).astype(np.int32)
         self.prefix_table = order[:npre].copy()
-        width = max(1, max(own))
+        width = max(1, max(own), -(-capacity // page))  # a table may have room for more
         self.table = np.full((len(lens), width), -7, dtype=np.int32)  # entries past a length are never read
         at = npre
         for b, n in enumerate(own):
