@@ -23,19 +23,19 @@ namespace cg = cooperative_groups;
 // head_dim bytes per token and key head against 4 * head_dim * rows
 // operations, so warp MMAs (m16n8k16) keep up, and 16 rows waste less than a
 // Tensor Memory tile of 128.  Every warp is a worker of its own: it copies the
-// K and V of its next units (32 tokens) into its own ring of shared memory
+// K and V of its next units (16 KB: 32 tokens of 128, 64 of 64) into its own ring of shared memory
 // with tensor-map boxes and takes them in turn, so that no warp waits for
 // another and short sequences cost no CTA-wide joins (four warps that shared
 // each unit spent 1.0 us of a 3.2 us one-unit segment on joining).
-constexpr int kUnit = kAttnWarpUnit;
 constexpr int kWorkers = kAttnWarpWorkers;
 
 template <int D>
 struct WarpCfg {
-  static constexpr int kHalf = kUnit * 128;            // bytes of 32 tokens x 64 dims
+  static constexpr int kUnit = attn_warp_unit(D);
+  static constexpr int kHalf = kUnit * 128;            // bytes of a unit's tokens x 64 dims
   static constexpr int kMat = kHalf * (D / 64);        // K or V of a stage
-  static constexpr int kStage = 2 * kMat;
-  static constexpr int kStages = D == 128 ? 2 : 4;     // 32 KB a worker
+  static constexpr int kStage = 2 * kMat;              // 16 KB
+  static constexpr int kStages = 2;
   static constexpr int kSmem = kWorkers * kStages * kStage;
 };
 
@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t keep_tokens(uint32_t v, int t, int n) {
 // l / 4 + 8 in MMA fragments.
 template <int D>
 struct WarpRows {
-  static constexpr int NT = D / 8;
+  static constexpr int NT = D / 8, kUnit = WarpCfg<D>::kUnit;
   uint32_t qf[D / 16][4];
   float o[NT][4];
   float m[2], l[2];
@@ -103,7 +103,7 @@ struct WarpRows {
     l[0] = l[1] = 0.f;
   }
 
-  // One unit: 32 tokens of K at kb and V at vb.  With `edge`, row h sees its
+  // One unit: its tokens of K at kb and V at vb.  With `edge`, row h sees its
   // first see[h] tokens and the V rows from n on are not to be used.
   __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, float scale_log2, bool edge, const int (&see)[2], int n) {
     constexpr int kHalf = WarpCfg<D>::kHalf;
@@ -216,6 +216,7 @@ template <int D>
 __global__ void __launch_bounds__(kWorkers * 32, 1)
     k_attn_warp(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = WarpCfg<D>;
+  constexpr int kUnit = C::kUnit;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ WarpShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
   uint64_t* full = sh.full[warp];
   AttnSeg* segs = sh.seg[warp];
   // ------------------------------------------------------------------ loads --
-  // A stage holds min(page, 32)-token boxes of K and V: lane i issues box i / 4
+  // A stage holds min(page, unit)-token boxes of K and V: lane i issues box i / 4
   // of matrix i % 2, half (i / 2) % 2 of the dims.  Page ids are read one unit
   // ahead.
   const int box = attn_box(p.page_size, kUnit);
@@ -349,7 +350,7 @@ cudaError_t launch_warp(const AttnParams& p, const CUtensorMap& km, const CUtens
 // Small problems, where launches and latencies are the time: one launch, no
 // plan, no joining kernel.  A cluster takes 16 rows of one (sequence, key head)
 // over everything they see, the prefix and then the own part; its warps take
-// the units of 32 tokens in turn and join through (distributed) shared memory.
+// the units in turn and join through (distributed) shared memory.
 // A prefix is read once per sequence here, from L2.
 struct TileShared {
   uint64_t full[kWorkers][4];
@@ -360,6 +361,7 @@ template <int D>
 __global__ void __launch_bounds__(kWorkers * 32, 1)
     k_attn_tile(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = WarpCfg<D>;
+  constexpr int kUnit = C::kUnit;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ TileShared sh;
   cg::cluster_group cluster = cg::this_cluster();

@@ -49,7 +49,7 @@ int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
 
 // Which kernel takes which part: the warp kernel takes parts of at most 16
 // rows per key head (one tile), the Tensor Memory kernel the others.
-void plan_sides(const moe_kv_batch& b, int group, AttnSide (&side)[2]) {
+void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)[2]) {
   memset(side, 0, sizeof side);
   const bool own_tc = (int64_t)b.max_q * group > kAttnWarpRows, prefix = b.prefix_len > 0;
   const bool prefix_tc = (int64_t)b.tokens * group > kAttnWarpRows;
@@ -57,7 +57,7 @@ void plan_sides(const moe_kv_batch& b, int group, AttnSide (&side)[2]) {
   w.own = !own_tc;
   w.prefix = prefix && !prefix_tc;
   w.rows = kAttnWarpRows;
-  w.unit = kAttnWarpUnit;
+  w.unit = attn_warp_unit(head_dim);
   w.ctas = kAttnWarpCtas;
   w.workers = kAttnWarpCtas * kAttnWarpWorkers;
   w.min_units = 1;
@@ -88,8 +88,8 @@ void plan_sides(const moe_kv_batch& b, int group, AttnSide (&side)[2]) {
 int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
   const int64_t row_tiles = ((int64_t)b.max_q * group + kAttnWarpRows - 1) / kAttnWarpRows;
   const int64_t tiles = b.batch * c.kv_heads * row_tiles;
-  const int64_t units = ((int64_t)b.prefix_len + kAttnWarpUnit - 1) / kAttnWarpUnit +
-                        ((int64_t)b.table_pages * c.page_size + kAttnWarpUnit - 1) / kAttnWarpUnit;
+  const int unit = attn_warp_unit(c.head_dim);
+  const int64_t units = ((int64_t)b.prefix_len + unit - 1) / unit + ((int64_t)b.table_pages * c.page_size + unit - 1) / unit;
   int cl = 1;
   while (cl < 8 && tiles * cl * 2 <= kNumSMs && (int64_t)cl * kAttnWarpWorkers < units) cl *= 2;
   const int64_t each = (units + cl * kAttnWarpWorkers - 1) / (cl * kAttnWarpWorkers);
@@ -185,7 +185,7 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_bat
   if (check_cache(cache) != MOE_OK || check_batch(batch) != MOE_OK || check_heads(cache, q_heads) != MOE_OK) return 0;
   AttnSide side[2];
   const int group = q_heads / cache->kv_heads;
-  plan_sides(*batch, group, side);
+  plan_sides(*batch, group, cache->head_dim, side);
   return side_layout(*batch, group, cache->kv_heads, cache->head_dim, side, nullptr);
 }
 
@@ -202,7 +202,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   AttnParams p;
   memset(&p, 0, sizeof p);
   p.group = q_heads / cache->kv_heads;
-  plan_sides(*batch, p.group, p.side);
+  plan_sides(*batch, p.group, cache->head_dim, p.side);
   if (ws_bytes < side_layout(*batch, p.group, cache->kv_heads, cache->head_dim, p.side, ws)) return MOE_ERR_WORKSPACE;
   p.q = (const uint16_t*)q;
   p.out = (uint16_t*)out;
@@ -223,7 +223,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   cudaStream_t s = (cudaStream_t)stream;
   if (const int cl = tile_cluster(*batch, *cache, p.group)) {
     CUtensorMap km, vm;
-    const int box = attn_box(cache->page_size, kAttnWarpUnit);
+    const int box = attn_box(cache->page_size, attn_warp_unit(cache->head_dim));
     if ((st = cache_map(&km, cache, cache->k, box)) != MOE_OK || (st = cache_map(&vm, cache, cache->v, box)) != MOE_OK)
       return st;
     p.tile_rows = (int)(((int64_t)batch->max_q * p.group + kAttnWarpRows - 1) / kAttnWarpRows);

@@ -370,12 +370,13 @@ cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUt
 cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
-// The warp kernel: one CTA per SM, six workers in each, tiles of 16 rows,
-// units of 32 tokens.
+// The warp kernel: one CTA per SM, seven workers in each (32 KB of ring and up to 255
+// registers a thread), tiles of 16 rows,
+// units of 16 KB of keys and values.
 constexpr int kAttnWarpCtas = kNumSMs;
-constexpr int kAttnWarpWorkers = 6;
+constexpr int kAttnWarpWorkers = 7;
 constexpr int kAttnWarpRows = 16;
-constexpr int kAttnWarpUnit = 32;
+__host__ __device__ constexpr int attn_warp_unit(int head_dim) { return head_dim == 128 ? 32 : 64; }
 // The Tensor Memory kernel: one CTA per SM, tiles of 256 rows, units of 128 tokens.
 constexpr int kAttnTcCtas = kNumSMs;
 constexpr int kAttnTcRows = 256;
