@@ -1,4 +1,4 @@
-// attention_tc.cu — attention over the paged cache on tcgen05 tensor cores,
+// attention_tc.cuh — the Tensor Memory side of attention (attention_split.cu),
 // for parts that many query rows share: the prefix of a batch, and long new
 // parts (prompts).
 //
@@ -20,15 +20,15 @@
 // a row moves only when its maximum grew by more than 2^8 (then the warpgroup
 // rescales O_t in Tensor Memory): any reference gives the same quotient, and
 // 2^8 keeps every partial sum far inside fp32.
+#pragma once
+
 #include "serve.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
-namespace {
 
-constexpr int kUnit = kAttnTcUnit;       // tokens
 constexpr int kHalfRows = 128;           // rows of an MMA tile
-constexpr int kThreads = 12 * 32;        // 2 x 4 softmax warps, producer, MMA, walk, one idle
+constexpr int kAttnThreads = 12 * 32;    // 2 x 4 softmax warps, producer, MMA, walk, one idle
 constexpr int kBufs = 5;
 constexpr int kSegs = 4;                 // segments handed from the walking warp to the others
 constexpr uint32_t kTmemCols = 512;
@@ -40,7 +40,7 @@ constexpr float kGrow = 8.f;             // log2 of the growth a stale reference
 
 template <int D>
 struct TcCfg {
-  static constexpr int kSub = kUnit * 128;           // 128 rows x 64 values
+  static constexpr int kSub = kAttnTcUnit * 128;           // 128 rows x 64 values
   static constexpr int kMat = kSub * (D / 64);       // one operand tile
   static constexpr int kSmem = (2 + kBufs) * kMat;   // Q_0, Q_1, ring
 };
@@ -52,7 +52,6 @@ struct TcShared {
   uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem_base;
   int abort_flag;
-  AttnPlanShared<1> plan;
 };
 
 __device__ __forceinline__ bool tc_wait(TcShared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
@@ -137,12 +136,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The Tensor Memory side of the split kernel, for all kAttnThreads threads.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                             const AttnPlan& plan, TcShared& sh, uint8_t* dyn) {
   using C = TcCfg<D>;
-  extern __shared__ __align__(1024) uint8_t dyn[];
-  __shared__ TcShared sh;
+  constexpr int kUnit = kAttnTcUnit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnSide& sd = p.side[1];
   if (warp == 9) {
@@ -170,13 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_fence();
   }
   tc_fence_before();
-  // The kernels after this one may start once it has seen the work before it
-  // complete: the warp kernel, which takes the other parts, waits for nothing
-  // else (see k_attn_warp).
-  pdl_wait();
-  pdl_trigger();
-  long long total;
-  const long long per = attn_plan<1>(p, sd, sh.plan, total);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   uint8_t* ring = dyn + 2 * C::kMat;
@@ -348,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 10) {
       // -------------------------------------------------------------- walk --
       AttnWalk w;
-      bool more = attn_begin<1>(p, sd, sh.plan, 0, per, total, w);
+      bool more = attn_begin(p, plan, 1, 0, w);
       for (;; ++nseg) {
         if (nseg >= (uint32_t)kSegs &&
             !__all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.seg_empty[nseg % kSegs], (nseg / kSegs - 1) & 1, p)))
@@ -534,19 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-template <int D>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
-  cudaError_t err = ensure_smem_attr((const void*)k_attn_tc<D>, TcCfg<D>::kSmem);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(k_attn_tc<D>, dim3(p.side[1].ctas), dim3(kThreads), TcCfg<D>::kSmem, s, p, km, vm);
-}
-
-}  // namespace
-
-cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
-  return p.head_dim == 128 ? launch<128>(p, km, vm, s) : launch<64>(p, km, vm, s);
 }
 
 }  // namespace moe

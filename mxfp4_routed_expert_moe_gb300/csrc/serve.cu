@@ -47,8 +47,8 @@ int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
   return t;
 }
 
-// Which kernel takes which part: the warp kernel takes parts of at most 16
-// rows per key head (one tile), the Tensor Memory kernel the others.
+// Which side of the split kernel takes which part: the warps take parts of at
+// most 16 rows per key head (one tile), the Tensor Memory side the others.
 void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)[2]) {
   memset(side, 0, sizeof side);
   const bool own_tc = (int64_t)b.max_q * group > kAttnWarpRows, prefix = b.prefix_len > 0;
@@ -58,16 +58,13 @@ void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)
   w.prefix = prefix && !prefix_tc;
   w.rows = kAttnWarpRows;
   w.unit = attn_warp_unit(head_dim);
-  w.ctas = kAttnWarpCtas;
-  w.workers = kAttnWarpCtas * kAttnWarpWorkers;
-  w.min_units = 1;
+  w.workers = kAttnCtas * kAttnWarpWorkers;
   w.tile_cost = 1;
   t.own = own_tc;
   t.prefix = prefix && prefix_tc;
   t.rows = kAttnTcRows;
   t.unit = kAttnTcUnit;
-  t.ctas = t.workers = kAttnTcCtas;
-  t.min_units = 1;
+  t.workers = kAttnCtas;
   t.tile_cost = 4;
   for (AttnSide& s : side) {
     while ((1 << s.rows_shift) < s.rows) ++s.rows_shift;
@@ -229,14 +226,14 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
     p.tile_rows = (int)(((int64_t)batch->max_q * p.group + kAttnWarpRows - 1) / kAttnWarpRows);
     return cuda_status(launch_attn_tile(p, cl, km, vm, s));
   }
-  for (int i = 1; i >= 0; --i) {
-    if (!p.side[i].own && !p.side[i].prefix) continue;
-    CUtensorMap km, vm;
+  CUtensorMap maps[4];  // K and V in the boxes of either side
+  for (int i = 0; i < 2; ++i) {
     const int box = attn_box(cache->page_size, p.side[i].unit);
-    if ((st = cache_map(&km, cache, cache->k, box)) != MOE_OK || (st = cache_map(&vm, cache, cache->v, box)) != MOE_OK)
+    if ((st = cache_map(&maps[2 * i], cache, cache->k, box)) != MOE_OK ||
+        (st = cache_map(&maps[2 * i + 1], cache, cache->v, box)) != MOE_OK)
       return st;
-    if ((st = cuda_status(i ? launch_attn_tc(p, km, vm, s) : launch_attn_warp(p, km, vm, s))) != MOE_OK) return st;
   }
+  if ((st = cuda_status(launch_attn_split(p, maps, s))) != MOE_OK) return st;
   return cuda_status(launch_attn_join(p, s));
 }
 

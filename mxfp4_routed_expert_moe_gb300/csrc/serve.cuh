@@ -86,8 +86,7 @@ struct AttnSide {
   int own, prefix;       // which sets this kernel takes
   int rows, unit;        // query rows of a tile, tokens of a unit (powers of two)
   int rows_shift, unit_shift;
-  int ctas, workers;     // CTAs launched, workers of all
-  int min_units;         // least units of a worker's range
+  int workers;           // most workers
   int tile_cost;         // units that a tile counts beside its tokens'
   float* slots;          // [workers + tiles][rows * (head_dim + 2)]
   long long* unit_start; // [batch + 1] first unit of each set; [batch + 1]: units per worker
@@ -103,11 +102,23 @@ struct AttnParams {
   float scale_log2;    // scale * log2(e)
   int kv_heads, head_dim, page_size, page_shift, num_pages;
   moe_kv_batch b;
-  AttnSide side[2];    // 0: warp kernel, 1: Tensor Memory kernel
+  AttnSide side[2];    // 0: warps, 1: Tensor Memory
   int tile_rows;       // tile kernel: row tiles of a sequence and key head
   int32_t* status;
   long long wait_limit;
 };
+
+// The warp side: seven workers a CTA (32 KB of ring each), tiles of 16 rows,
+// units of 16 KB of keys and values.
+constexpr int kAttnWarpRows = 16;
+__host__ __device__ constexpr int attn_warp_unit(int head_dim) { return head_dim == 128 ? 32 : 64; }
+// The Tensor Memory side: one worker a CTA, tiles of 256 rows, units of 128
+// tokens.
+constexpr int kAttnTcRows = 256;
+constexpr int kAttnTcUnit = 128;
+// Measured time of a unit in us: of a worker among seven, and of a tile of more
+// than 128 rows (with its 64-value heads about half).
+constexpr float kAttnWarpUnitCost = 1.65f, kAttnTcUnitCost = 1.7f;
 
 // What a set's entries say, as loaded.
 struct AttnRaw {
@@ -193,22 +204,29 @@ struct AttnWalk {
   long long u, u1;   // next unit, end of the range
 };
 
-template <int W>
-struct AttnPlanShared {
+// The plan as the CTAs of one launch share it.  Blocks [0, ctas[1]) work on
+// side 1 (Tensor Memory), the others on side 0 (warps).
+constexpr int kAttnWarpWorkers = 7;
+struct AttnPlan {
   long long part_u[32];
   int part_t[32];
-  long long unit0[W];
-  int set[W], tile0[W];
+  long long unit0[kAttnWarpWorkers];
+  int set[kAttnWarpWorkers], tile0[kAttnWarpWorkers];
+  // Everything below is the same in every CTA.
+  long long total[2], per[2];
+  int ctas[2];
 };
 
-// All threads of the CTA: add up the sets' units, cut them into ranges for
-// W * gridDim.x workers (worker w of CTA c is number w * gridDim.x + c, so
-// that few units spread over the SMs) and find where the ranges of this CTA's
-// workers begin.  CTA 0 writes the plan for the joining kernel.  Returns the
-// units per worker.
-template <int W>
-__device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSide& sd, AttnPlanShared<W>& sh,
-                                               long long& total) {
+// All threads of the CTA: add up the sets' units, share the CTAs out between
+// the two sides by what their units cost, cut each side's units into ranges for
+// its workers (worker w of a side's CTA c is number w * ctas + c, so that few
+// units spread over the SMs) and find where the ranges of this CTA's workers
+// begin.  Only the side of the own parts needs a scan; a prefix alone on its
+// side is one set.  CTA 0 writes the plan for the joining kernel.
+__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
+  const int own = p.side[1].own ? 1 : 0;  // the side that is scanned
+  const AttnSide& sd = p.side[own];
+  const bool two = p.side[own ^ 1].prefix != 0;
   const int nsets = p.b.batch + 1, nt = blockDim.x, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5, nwarps = nt >> 5;
   const int per_thread = (nsets + nt - 1) / nt;
@@ -238,7 +256,7 @@ __device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSi
     sh.part_t[warp] = et;
   }
   __syncthreads();
-  total = 0;
+  long long total = 0;
   eu -= u;  // exclusive
   et -= t;
   for (int i = 0; i < nwarps; ++i) {
@@ -249,17 +267,54 @@ __device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSi
     }
     total += x;
   }
-  const long long workers = (long long)W * gridDim.x;
-  long long per;
-  if (total < 0x7FFFFFFFll)
-    per = ((uint32_t)total + (uint32_t)workers - 1) / (uint32_t)workers;
-  else
-    per = (total + workers - 1) / workers;
-  if (per < sd.min_units) per = sd.min_units;
-  bool mine = blockIdx.x == 0;
+  if (tid == 0) {
+    long long other = 0;
+    if (two) {
+      const AttnSet a = attn_set(p, p.side[own ^ 1], p.b.batch, attn_load(p, p.b.batch));
+      other = (long long)a.tiles * p.kv_heads * a.units;
+    }
+    sh.total[own] = total;
+    sh.total[own ^ 1] = other;
+    // CTAs of side 1: its share of the time, a unit of side 0 costing a
+    // worker-th of kAttnWarpUnitCost and one of side 1 kAttnTcUnitCost; both
+    // sides that have units get one at least.
+    const int n = gridDim.x;
+    const float c1 = (float)sh.total[1] * kAttnTcUnitCost, c0 = (float)sh.total[0] * (kAttnWarpUnitCost / kAttnWarpWorkers);
+    int n1 = sh.total[1] == 0 ? 0 : sh.total[0] == 0 ? n : (int)((float)n * c1 / (c0 + c1) + 0.5f);
+    if (sh.total[1] > 0 && n1 < 1) n1 = 1;
+    if (sh.total[0] > 0 && n1 > n - 1) n1 = n - 1;
+    sh.ctas[1] = n1;
+    sh.ctas[0] = n - n1;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const long long u0 = ((long long)w * gridDim.x + blockIdx.x) * per;
+    for (int i = 0; i < 2; ++i) {
+      const long long workers = (long long)sh.ctas[i] * (i == 0 ? kAttnWarpWorkers : 1);
+      const long long x = workers > 0 ? (sh.total[i] + workers - 1) / workers : 0;
+      sh.per[i] = x < 1 ? 1 : x;
+    }
+    if (two) {
+      sh.set[0] = p.b.batch;
+      sh.unit0[0] = 0;
+      sh.tile0[0] = 0;
+    }
+    if (blockIdx.x == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (p.side[i].unit_start) p.side[i].unit_start[nsets] = sh.per[i];
+      if (two) {
+        p.side[own ^ 1].unit_start[p.b.batch] = 0;
+        p.side[own ^ 1].tile_start[p.b.batch] = 0;
+      }
+    }
+  }
+  __syncthreads();
+  // Where this CTA's workers of the scanned side begin.
+  const int side = (int)blockIdx.x < sh.ctas[1] ? 1 : 0;
+  const int workers = side != own ? 0 : own == 0 ? kAttnWarpWorkers : 1;
+  const int cta = side == 1 ? (int)blockIdx.x : (int)blockIdx.x - sh.ctas[1], ctas = sh.ctas[side];
+  const long long per = sh.per[own];
+  bool mine = blockIdx.x == 0;
+  for (int w = 0; w < workers; ++w) {
+    const long long u0 = ((long long)w * ctas + cta) * per;
     mine |= u0 >= eu && u0 < eu + u;
   }
   if (mine) {
@@ -269,16 +324,15 @@ __device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSi
       const AttnSet a = attn_set(p, sd, s, attn_load(p, s));
       const int tiles = a.tiles * p.kv_heads;
       const long long n = (long long)tiles * a.units;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const long long u0 = ((long long)w * gridDim.x + blockIdx.x) * per;
+      for (int w = 0; w < workers; ++w) {
+        const long long u0 = ((long long)w * ctas + cta) * per;
         if (u0 >= su && u0 < su + n) {
           sh.set[w] = s;
           sh.unit0[w] = su;
           sh.tile0[w] = st;
         }
       }
-      if (blockIdx.x == 0) {
+      if (blockIdx.x == 0 && (s < p.b.batch || !two)) {
         sd.unit_start[s] = su;
         sd.tile_start[s] = st;
       }
@@ -286,23 +340,20 @@ __device__ __forceinline__ long long attn_plan(const AttnParams& p, const AttnSi
       st += tiles;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) sd.unit_start[nsets] = per;
   __syncthreads();
-  return per;
 }
 
-// The walk of this CTA's worker w; false: nothing to do.
-template <int W>
-__device__ __forceinline__ bool attn_begin(const AttnParams& p, const AttnSide& sd, const AttnPlanShared<W>& sh, int w,
-                                           long long per, long long total, AttnWalk& k) {
-  k.worker = w * gridDim.x + blockIdx.x;
-  k.u = k.worker * per;
-  if (k.u >= total) return false;
-  k.u1 = k.u + per < total ? k.u + per : total;
+// The walk of this CTA's worker w on its side; false: nothing to do.
+__device__ __forceinline__ bool attn_begin(const AttnParams& p, const AttnPlan& sh, int side, int w, AttnWalk& k) {
+  const int cta = side == 1 ? (int)blockIdx.x : (int)blockIdx.x - sh.ctas[1];
+  k.worker = w * sh.ctas[side] + cta;
+  k.u = k.worker * sh.per[side];
+  if (k.u >= sh.total[side]) return false;
+  k.u1 = k.u + sh.per[side] < sh.total[side] ? k.u + sh.per[side] : sh.total[side];
   k.set = sh.set[w];
   k.unit0 = sh.unit0[w];
   k.tile0 = sh.tile0[w];
-  k.a = attn_set(p, sd, k.set, attn_load(p, k.set));
+  k.a = attn_set(p, p.side[side], k.set, attn_load(p, k.set));
   k.next = attn_load(p, k.set < p.b.batch ? k.set + 1 : k.set);
   return true;
 }
@@ -366,20 +417,10 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnSide& s
 // Token rows of one tensor-map box: pages shorter than a unit give several.
 __host__ __device__ __forceinline__ int attn_box(int page_size, int unit) { return page_size < unit ? page_size : unit; }
 
-cudaError_t launch_attn_tc(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
-cudaError_t launch_attn_warp(const AttnParams& p, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
+cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap (&maps)[4], cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
-// The warp kernel: one CTA per SM, seven workers in each (32 KB of ring and up to 255
-// registers a thread), tiles of 16 rows,
-// units of 16 KB of keys and values.
-constexpr int kAttnWarpCtas = kNumSMs;
-constexpr int kAttnWarpWorkers = 7;
-constexpr int kAttnWarpRows = 16;
-__host__ __device__ constexpr int attn_warp_unit(int head_dim) { return head_dim == 128 ? 32 : 64; }
-// The Tensor Memory kernel: one CTA per SM, tiles of 256 rows, units of 128 tokens.
-constexpr int kAttnTcCtas = kNumSMs;
-constexpr int kAttnTcRows = 256;
-constexpr int kAttnTcUnit = 128;
+// One CTA per SM.
+constexpr int kAttnCtas = kNumSMs;
 
 }  // namespace moe
