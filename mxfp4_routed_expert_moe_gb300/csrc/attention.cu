@@ -122,8 +122,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
     int kv, end;
     const bool pre = unit_at(u, kv, end) == p.b.batch;
     const int see[2] = {(pre ? end : vis[0]) - kv, (pre ? end : vis[1]) - kv};
-    const uint32_t kb = smem_u32(ring + st * C::kStage);
-    acc.unit(kb, kb + C::kMat, p.scale_log2, kv + kUnit > (pre ? end : own_all), see, end - kv);
+    acc.unit(ring + st * C::kStage, p.scale_log2, kv + kUnit > (pre ? end : own_all), see, end - kv);
     __syncwarp();  // every lane has read the stage
     if (u + C::kStages * step < units) {
       load(u + C::kStages * step, st, next);

@@ -55,11 +55,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Keep the 16-bit halves of v whose token (t, t + 1) is below n.
-__device__ __forceinline__ uint32_t keep_tokens(uint32_t v, int t, int n) {
-  return t + 1 < n ? v : (t < n ? v & 0xFFFFu : 0u);
-}
-
 // The rows of a 16-row tile as one warp holds them: lane l has rows l / 4 and
 // l / 4 + 8 in MMA fragments.
 template <int D>
@@ -91,11 +86,22 @@ struct WarpRows {
     l[0] = l[1] = 0.f;
   }
 
-  // One unit: its tokens of K at kb and V at vb.  With `edge`, row h sees its
-  // first see[h] tokens and the V rows from n on are not to be used.
-  __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, float scale_log2, bool edge, const int (&see)[2], int n) {
-    constexpr int kHalf = WarpCfg<D>::kHalf;
+  // One unit: its tokens of K and V in a stage of the warp's ring.  With
+  // `edge`, row h sees its first see[h] tokens and the V rows from n on are not
+  // to be used.
+  __device__ __forceinline__ void unit(uint8_t* stage, float scale_log2, bool edge, const int (&see)[2], int n) {
+    using C = WarpCfg<D>;
+    constexpr int kHalf = C::kHalf;
     const int lane = threadIdx.x & 31;
+    const uint32_t kb = smem_u32(stage), vb = kb + C::kMat;
+    if (edge) {
+      // Rows of V past the length may hold anything, and 0 * NaN is NaN.
+      for (int i = n * 8 + lane; i < kUnit * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<uint4*>(stage + C::kMat + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
     float sc[kUnit / 8][4];
 #pragma unroll
     for (int i = 0; i < kUnit / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
@@ -159,14 +165,6 @@ struct WarpRows {
         const int c = (t & 7) + (lane >> 4);
         uint32_t b[4];
         ldsm4t(vb + (t >> 3) * kHalf + tok * 128 + ((c ^ (tok & 7)) << 4), b);
-        if (edge) {
-          // Rows of V past the length may hold anything: 0 * NaN is NaN.
-          const int tk = 16 * j + 2 * (lane & 3);
-          b[0] = keep_tokens(b[0], tk, n);
-          b[1] = keep_tokens(b[1], tk + 8, n);
-          b[2] = keep_tokens(b[2], tk, n);
-          b[3] = keep_tokens(b[3], tk + 8, n);
-        }
         mma_bf16(o[t], a[0], a[1], a[2], a[3], b[0], b[1]);
         mma_bf16(o[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
       }
@@ -306,9 +304,8 @@ __device__ __forceinline__ void attn_warp_role(const AttnParams& p, const CUtens
         set_status_word(p.status, MOE_ERR_TIMEOUT);
         break;
       }
-      const uint32_t kb = smem_u32(ring + st * C::kStage);
       const int see[2] = {vis[0] - kv, vis[1] - kv};
-      rows.unit(kb, kb + C::kMat, scale, kv + kUnit > vis_min, see, g.kv1 - kv);
+      rows.unit(ring + st * C::kStage, scale, kv + kUnit > vis_min, see, g.kv1 - kv);
       ++un;
       kv += kUnit;
       __syncwarp();  // every lane has read the stage
