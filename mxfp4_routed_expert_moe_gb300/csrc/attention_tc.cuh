@@ -246,8 +246,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
     const uint32_t qb = smem_u32(dyn), rb = smem_u32(ring);
     const uint32_t one = elect_one();  // commits track the electing lane's MMAs
     int bi = 0, use = 0;         // next ring buffer
-    uint32_t nq[2] = {0, 0};     // segments that used half t
-    uint32_t np[2] = {0, 0};     // P tiles of half t taken
+    uint32_t nq = 0, np = 0;     // parities by half: of the segments, of the P tiles taken
     bool ok = true;
     auto all = [](bool x) { return __all_sync(0xFFFFFFFFu, x) != 0; };
     auto take = [&](int& b) {    // the next ring buffer, filled
@@ -269,14 +268,14 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       const uint32_t va = desc_v<D>(rb + b * C::kMat);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        ok = ok && all(tc_wait(sh, &sh.p_ready[t][k], np[t] & 1, p));
+        ok = ok && all(tc_wait(sh, &sh.p_ready[t][k], np >> t & 1, p));
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int kb = 4 * k; kb < 4 * k + 4; ++kb)
           mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kb, va + kb * (2048 >> 4), id_o, !first || kb > 0, one);
       }
-      ++np[t];
+      np ^= 1u << t;
     };
     // The buffers of the next unit are waited for while MMAs are queued: the
     // time between the last scores of a unit and the next P V is tensor idle.
@@ -290,8 +289,11 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       if (nt == 0) continue;
       int kbuf, vbuf;
       take(kbuf);
-      for (int t = 0; t < (two ? 2 : 1); ++t) {
-        ok = ok && all(tc_wait(sh, &sh.q_ready[t], nq[t]++ & 1, p));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t == 1 && !two) break;
+        ok = ok && all(tc_wait(sh, &sh.q_ready[t], nq >> t & 1, p));
+        nq ^= 1u << t;
         if (!ok) break;
         tc_fence_after();
         scores(t, kbuf);
@@ -386,7 +388,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         // that read the previous ones are complete: their scores came back.
         constexpr int L = D / 8, R = 32 / L;  // lanes of a row, rows of a pass
         const int rl = q * 32 + lane / L, ch = lane % L;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 32 / R; b += 8) {
           uint4 v[8];
 #pragma unroll
@@ -411,15 +413,24 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.s_full[t], ns++ & 1, p));
         if (!ok) break;
         tc_fence_after();
+        if (kv + kUnit > vis_min) {
+          // The few units with an edge: mask the scores where they are.
+#pragma unroll 1
+          for (int k = 0; k < kUnit; k += 32) {
+            uint32_t x[32];
+            tmem_ld32(ts + k, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (kv + k + e >= vis) x[e] = 0xFF800000u;
+            tmem_st32(ts + k, x);
+          }
+          tmem_st_wait();
+        }
         uint32_t s[kUnit];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
         tmem_ld_wait();
-        if (kv + kUnit > vis_min) {
-#pragma unroll
-          for (int e = 0; e < kUnit; ++e)
-            if (kv + e >= vis) s[e] = 0xFF800000u;
-        }
         float mx[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
