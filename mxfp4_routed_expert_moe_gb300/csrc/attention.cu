@@ -193,9 +193,11 @@ cudaError_t launch_tile(const AttnParams& p, int cl, const CUtensorMap& km, cons
 // --------------------------------------------------------------- join kernel --
 // A row's segments are the workers whose ranges meet its tile's units, in
 // order, first the prefix's and then the own part's.  A CTA takes some heads
-// of one token: two warps look up the token's sets, then each warp joins a
-// head at a time.
+// of one token: two warps look up the token's sets, one thread per head and
+// part finds the segments, then each warp joins four heads at a time.  Bound by
+// instructions: about 100 per row and segment.
 constexpr int kJoinWarps = 4;
+constexpr int kJoinHeads = 64;  // heads of a CTA at a time
 
 struct JoinPart {
   const float* slots;
@@ -255,8 +257,8 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int n, int head, 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams p) {
   __shared__ JoinPart sh_part[2];
+  __shared__ JoinRow sh_row[2][kJoinHeads];
   pdl_trigger();
-  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = blockIdx.x;
   if (warp < 2) {  // 0: the prefix, 1: the own part
@@ -275,9 +277,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
     }
     const AttnSide& sd = p.side[warp ? (p.side[1].own ? 1 : 0) : (p.side[1].prefix ? 1 : 0)];
     if (any) {
-      t.unit0 = sd.unit_start[b];
-      t.per = sd.unit_start[p.b.batch + 1];
-      t.tile0 = sd.tile_start[b];
+      // The batch's own entries are as the split kernel saw them: it lets this
+      // kernel start only after everything before it is complete.
       const AttnSet a = attn_set(p, sd, b, attn_load(p, b));
       t.units = a.units;
       t.tiles = a.tiles;
@@ -285,130 +286,149 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
       t.slots = sd.slots;
       t.rows_shift = sd.rows_shift;
     }
+    pdl_wait();
+    if (t.units) {
+      t.unit0 = sd.unit_start[b];
+      t.per = sd.unit_start[p.b.batch + 1];
+      t.tile0 = sd.tile_start[b];
+    }
     if (lane == 0) sh_part[warp] = t;
+  } else {
+    pdl_wait();
   }
   __syncthreads();
   constexpr int E = D / 32;
-  const int step = gridDim.y * kJoinWarps;
-  const int head0 = blockIdx.y * kJoinWarps + warp;
-  // Four heads at a time while each has at most 8 segments: lane 8 h + s looks
-  // after segment s of head h, and the loads of the four overlap.
-  int done = head0;  // first head of this warp that is still to do
-  for (; done < p.q_heads; done += 4 * step) {
-    const int head = done + (lane >> 3) * step, s = lane & 7;
-    JoinRow a, b;
-    a.n = b.n = 0;
-    int64_t fa = 0, fb = 0;
-    int rows = 0;
-    const float *src = nullptr, *ms = nullptr;
-    if (head < p.q_heads) {
-      fa = (int64_t)(D + 2) << sh_part[0].rows_shift;
-      fb = (int64_t)(D + 2) << sh_part[1].rows_shift;
-      a = join_row(p, sh_part[0], head, fa);
-      b = join_row(p, sh_part[1], head, fb);
-      if (s < a.n) {
-        src = a.first + s * fa;
-        ms = a.m + s * fa;
-        rows = 1 << sh_part[0].rows_shift;
-      } else if (s < a.n + b.n) {
-        src = b.first + (s - a.n) * fb;
-        ms = b.m + (s - a.n) * fb;
-        rows = 1 << sh_part[1].rows_shift;
-      }
-    }
-    if (__any_sync(0xFFFFFFFFu, a.n + b.n > 8)) break;
-    float m = -CUDART_INF_F, l = 0.f;
-    if (ms) {
-      m = *ms;
-      l = ms[rows];
-    }
-    float mx = m;
+  int64_t sf[2];
+  int rows[2];
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    const float f = m == -CUDART_INF_F ? 0.f : ex2(m - mx);
-    l *= f;  // a NaN sum stays one
-    // In segment order: the same order whichever way a row is joined.
-    float lt = 0.f;
-    float acc[4][E] = {};
-    const int most = __reduce_max_sync(0xFFFFFFFFu, a.n + b.n);
-    for (int k = 0; k < most; ++k) {
-      lt += __shfl_sync(0xFFFFFFFFu, l, (lane & 24) + k);
-      float v[4][E], fs[4];
+  for (int k = 0; k < 2; ++k) {
+    rows[k] = 1 << sh_part[k].rows_shift;
+    sf[k] = (int64_t)(D + 2) << sh_part[k].rows_shift;
+  }
+  // This CTA's heads, kJoinHeads at a time.
+  const int per_cta = (p.q_heads + gridDim.y - 1) / gridDim.y;
+  const int h_end = (int)(blockIdx.y + 1) * per_cta < p.q_heads ? (int)(blockIdx.y + 1) * per_cta : p.q_heads;
+  for (int h0 = blockIdx.y * per_cta; h0 < h_end; h0 += kJoinHeads) {
+    const int heads = h_end - h0 < kJoinHeads ? h_end - h0 : kJoinHeads;
+    __syncthreads();
+    static_assert(2 * kJoinHeads == kJoinWarps * 32, "a thread per head and part");
+    {
+      const int k = threadIdx.x / kJoinHeads, h = threadIdx.x % kJoinHeads;
+      if (h < heads) sh_row[k][h] = join_row(p, sh_part[k], h0 + h, sf[k]);
+    }
+    __syncthreads();
+    const bool many = __syncthreads_or((int)threadIdx.x < heads && sh_row[0][threadIdx.x].n + sh_row[1][threadIdx.x].n > 8);
+    // Four heads at a time where each has at most 8 segments: lane 8 h + s looks
+    // after segment s of head h, and the loads of the four overlap.
+    for (int done = warp * 4; done < heads && !many; done += 4 * kJoinWarps) {
+      const int hl = done + (lane >> 3), s = lane & 7;
+      JoinRow a, b;
+      a.n = b.n = 0;
+      int rw = 0;
+      const float *src = nullptr, *ms = nullptr;
+      if (hl < heads) {
+        a = sh_row[0][hl];
+        b = sh_row[1][hl];
+        if (s < a.n) {
+          src = a.first + s * sf[0];
+          ms = a.m + s * sf[0];
+          rw = rows[0];
+        } else if (s < a.n + b.n) {
+          src = b.first + (s - a.n) * sf[1];
+          ms = b.m + (s - a.n) * sf[1];
+          rw = rows[1];
+        }
+      }
+      float m = -CUDART_INF_F, l = 0.f;
+      if (ms) {
+        m = *ms;
+        l = ms[rw];
+      }
+      float mx = m;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+      const float f = m == -CUDART_INF_F ? 0.f : ex2(m - mx);
+      l *= f;  // a NaN sum stays one
+      // In segment order: the same order whichever way a row is joined.
+      float lt = 0.f;
+      float acc[4][E] = {};
+      const int most = __reduce_max_sync(0xFFFFFFFFu, a.n + b.n);
+#pragma unroll 2
+      for (int k = 0; k < most; ++k) {
+        lt += __shfl_sync(0xFFFFFFFFu, l, (lane & 24) + k);
+        float v[4][E], fs[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          fs[h] = __shfl_sync(0xFFFFFFFFu, f, 8 * h + k);
+          const float* row = (const float*)__shfl_sync(0xFFFFFFFFu, (unsigned long long)src, 8 * h + k);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[h][e] = 0.f;
+          if (fs[h] > 0.f) {  // a segment without weight may hold an unwritten sum
+            if (E == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(row + lane * E);
+              v[h][0] = x.x, v[h][1] = x.y, v[h][E - 2] = x.z, v[h][E - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(row + lane * E);
+              v[h][0] = x.x, v[h][1] = x.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(fs[h], v[h][e], acc[h][e]);
+      }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        fs[h] = __shfl_sync(0xFFFFFFFFu, f, 8 * h + k);
-        const float* row = (const float*)__shfl_sync(0xFFFFFFFFu, (unsigned long long)src, 8 * h + k);
-        if (fs[h] > 0.f) {
-          if (E == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(row + lane * E);
-            v[h][0] = x.x, v[h][1] = x.y, v[h][E - 2] = x.z, v[h][E - 1] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(row + lane * E);
-            v[h][0] = x.x, v[h][1] = x.y;
-          }
-        }
+        if (done + h >= heads) break;
+        store_row<D>(p, n, h0 + done + h, lane, acc[h], __shfl_sync(0xFFFFFFFFu, lt, 8 * h), __shfl_sync(0xFFFFFFFFu, mx, 8 * h));
       }
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[h][e] = fs[h] > 0.f ? fmaf(fs[h], v[h][e], acc[h][e]) : acc[h][e];
     }
+    // Else a head at a time.
+    for (int hl = warp; hl < heads && many; hl += kJoinWarps) {
+      const int head = h0 + hl;
+      JoinRow part[2];
+      part[0] = sh_row[0][hl];
+      part[1] = sh_row[1][hl];
+      float mx = -CUDART_INF_F;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int hd = done + h * step;
-      if (hd >= p.q_heads) break;
-      store_row<D>(p, n, hd, lane, acc[h], __shfl_sync(0xFFFFFFFFu, lt, 8 * h), __shfl_sync(0xFFFFFFFFu, mx, 8 * h));
-    }
-  }
-  for (int head = done; head < p.q_heads; head += step) {
-    JoinRow part[2];
-    int64_t sf[2];
-    int rows[2];
+      for (int k = 0; k < 2; ++k)
+        for (int s = lane; s < part[k].n; s += 32) mx = fmaxf(mx, part[k].m[s * sf[k]]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const JoinPart& t = sh_part[k];
-      rows[k] = 1 << t.rows_shift;
-      sf[k] = (int64_t)(D + 2) << t.rows_shift;
-      part[k] = join_row(p, t, head, sf[k]);
-    }
-    float mx = -CUDART_INF_F;
+      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+      float acc[E] = {}, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int s = lane; s < part[k].n; s += 32) mx = fmaxf(mx, part[k].m[s * sf[k]]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    float acc[E] = {}, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      for (int s0 = 0; s0 < part[k].n; s0 += 32) {
-        // Lane s holds segment s0 + s's weight and sum.
-        float f = 0.f, ls = 0.f;
-        if (s0 + lane < part[k].n) {
-          const float* b = part[k].m + (s0 + lane) * sf[k];
-          const float ms = *b;
-          f = ms == -CUDART_INF_F ? 0.f : ex2(ms - mx);
-          ls = b[rows[k]] * f;  // a NaN sum stays one
-        }
-        const int cnt = part[k].n - s0 < 32 ? part[k].n - s0 : 32;
+      for (int k = 0; k < 2; ++k) {
+        for (int s0 = 0; s0 < part[k].n; s0 += 32) {
+          // Lane s holds segment s0 + s's weight and sum.
+          float f = 0.f, ls = 0.f;
+          if (s0 + lane < part[k].n) {
+            const float* b = part[k].m + (s0 + lane) * sf[k];
+            const float ms = *b;
+            f = ms == -CUDART_INF_F ? 0.f : ex2(ms - mx);
+            ls = b[rows[k]] * f;  // a NaN sum stays one
+          }
+          const int cnt = part[k].n - s0 < 32 ? part[k].n - s0 : 32;
 #pragma unroll 8
-        for (int s = 0; s < cnt; ++s) {
-          const float fs = __shfl_sync(0xFFFFFFFFu, f, s);
-          l += __shfl_sync(0xFFFFFFFFu, ls, s);
-          const float* src = part[k].first + (s0 + s) * sf[k] + lane * E;
-          float v[E];
-          if (E == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src);
-            v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            v[0] = x.x, v[1] = x.y;
-          }
+          for (int s = 0; s < cnt; ++s) {
+            const float fs = __shfl_sync(0xFFFFFFFFu, f, s);
+            l += __shfl_sync(0xFFFFFFFFu, ls, s);
+            const float* src = part[k].first + (s0 + s) * sf[k] + lane * E;
+            float v[E];
+            if (E == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[0] = x.x, v[1] = x.y;
+            }
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fs > 0.f ? fmaf(fs, v[e], acc[e]) : acc[e];  // weightless: unwritten
+            for (int e = 0; e < E; ++e) acc[e] = fs > 0.f ? fmaf(fs, v[e], acc[e]) : acc[e];
+          }
         }
       }
+      store_row<D>(p, n, head, lane, acc, l, mx);
     }
-    store_row<D>(p, n, head, lane, acc, l, mx);
   }
 }
 
@@ -419,7 +439,8 @@ cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km,
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s) {
-  // A warp a head while the CTAs are few; fewer CTAs a token for long batches.
+  // All heads of a token in one CTA for long batches, down to a head a warp
+  // while the CTAs are few.
   const int most = (p.q_heads + kJoinWarps - 1) / kJoinWarps;
   int ny = (8 * kNumSMs + p.b.tokens - 1) / p.b.tokens;
   ny = ny < 1 ? 1 : (ny > most ? most : ny);

@@ -117,8 +117,8 @@ __host__ __device__ constexpr int attn_warp_unit(int head_dim) { return head_dim
 constexpr int kAttnTcRows = 256;
 constexpr int kAttnTcUnit = 128;
 // Measured time of a unit in us: of a worker among seven, and of a tile of more
-// than 128 rows (with its 64-value heads about half).
-constexpr float kAttnWarpUnitCost = 1.65f, kAttnTcUnitCost = 1.7f;
+// than 128 rows; and how much longer the Tensor Memory side takes to get going.
+constexpr float kAttnWarpUnitCost = 1.65f, kAttnTcUnitCost = 1.65f, kAttnTcStart = 5.f;
 
 // What a set's entries say, as loaded.
 struct AttnRaw {
@@ -275,12 +275,22 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
     }
     sh.total[own] = total;
     sh.total[own ^ 1] = other;
-    // CTAs of side 1: its share of the time, a unit of side 0 costing a
-    // worker-th of kAttnWarpUnitCost and one of side 1 kAttnTcUnitCost; both
-    // sides that have units get one at least.
+    // CTAs of side 1, x of n: both sides should end together,
+    //   kAttnTcStart + c1 / x = c0 / (n - x),
+    // with c the time that their units cost one CTA.  Sides with units get one
+    // CTA at least.
     const int n = gridDim.x;
     const float c1 = (float)sh.total[1] * kAttnTcUnitCost, c0 = (float)sh.total[0] * (kAttnWarpUnitCost / kAttnWarpWorkers);
-    int n1 = sh.total[1] == 0 ? 0 : sh.total[0] == 0 ? n : (int)((float)n * c1 / (c0 + c1) + 0.5f);
+    int n1 = sh.total[1] == 0 ? 0 : n;
+    if (n1 > 0 && sh.total[0] > 0) {
+      int lo = 1, hi = n - 1;
+      while (lo < hi) {
+        const int x = (lo + hi) / 2;
+        if (kAttnTcStart + __fdividef(c1, (float)x) > __fdividef(c0, (float)(n - x))) lo = x + 1;
+        else hi = x;
+      }
+      n1 = lo;
+    }
     if (sh.total[1] > 0 && n1 < 1) n1 = 1;
     if (sh.total[0] > 0 && n1 > n - 1) n1 = n - 1;
     sh.ctas[1] = n1;
