@@ -317,9 +317,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
       if (h < heads) sh_row[k][h] = join_row(p, sh_part[k], h0 + h, sf[k]);
     }
     __syncthreads();
-    const bool many = __syncthreads_or((int)threadIdx.x < heads && sh_row[0][threadIdx.x].n + sh_row[1][threadIdx.x].n > 8);
-    // Four heads at a time where each has at most 8 segments: lane 8 h + s looks
-    // after segment s of head h, and the loads of the four overlap.
+    // A head a warp where there are no more heads than warps, or segments for
+    // more than 8 lanes: eight of a row's loads in flight, one latency for most.
+    // Else four heads at a time: lane 8 h + s looks after segment s of head h,
+    // and the loads of the four overlap.
+    const bool wide = (int)threadIdx.x < heads && sh_row[0][threadIdx.x].n + sh_row[1][threadIdx.x].n > 8;
+    const bool many = __syncthreads_or(heads <= kJoinWarps || wide);
     for (int done = warp * 4; done < heads && !many; done += 4 * kJoinWarps) {
       const int hl = done + (lane >> 3), s = lane & 7;
       JoinRow a, b;
