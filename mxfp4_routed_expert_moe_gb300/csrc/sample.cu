@@ -26,6 +26,8 @@
 // (512 rows of 128,000: 391 against 377 us; 64 rows: 74 against 64 us).
 #include <cooperative_groups.h>
 
+#include <cuda/std/type_traits>
+
 #include "serve.cuh"
 
 namespace moe {
@@ -45,8 +47,7 @@ constexpr int kMostScores = 65536;       // of a CTA
 constexpr int kMostBytes = 84 << 10;
 constexpr float kFix = 2147483648.f;     // 2^31
 constexpr float kBinScale = 45.9f;       // times kCut: below kBins - 1
-constexpr float kCut = 22.25f;           // below m - kCut every W is 0, ...
-constexpr float kSure = 22.f;            // ... down to m - kSure none is (exp(-22) 2^31 = 0.599)
+constexpr float kCut = 22.25f;           // below m - kCut every W is 0
 constexpr unsigned long long kKeyAll = ~0ull;
 
 struct SampleShared {
@@ -99,7 +100,9 @@ struct Row {
   float m;       // largest scaled score
   float least;   // scores below have W = 0 or rank past K*
   float min_p;   // 0: off
-  unsigned long long key_max;  // K*
+  bool bounded;  // K* is set: score z_max, index i_max
+  float z_max;
+  uint32_t i_max;
 
   // exp(z - m).  expf, not an approximation: the weights are part of the
   // definition, and the same function gives the same integers everywhere.
@@ -112,11 +115,13 @@ struct Row {
   }
   // Not dropped by the bound found so far (for z >= least).
   __device__ __forceinline__ bool within(float z, uint32_t idx) const {
-    return key_max == kKeyAll || rank_key(z, idx) <= key_max;
+    return !bounded || z > z_max || (z == z_max && idx <= i_max);
   }
   __device__ __forceinline__ void set_max(unsigned long long key) {
-    key_max = key;
-    least = fmaxf(least, order_float(~(uint32_t)(key >> kIdxBits)));
+    bounded = true;
+    z_max = order_float(~(uint32_t)(key >> kIdxBits));
+    i_max = (uint32_t)key & ((1u << kIdxBits) - 1);
+    least = fmaxf(least, z_max);
   }
   // Weight of a kept token, 0 for the others.
   __device__ __forceinline__ uint32_t kept(float z, uint32_t idx) const {
@@ -139,14 +144,14 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // What a search looks for: the token of a given rank, or the last one whose
 // better ranks weigh less than a bound.
 struct Target {
-  bool by_count;
-  uint32_t count;   // >= 1: rank count - 1
-  double bound;
+  uint32_t count;   // by count: >= 1, rank count - 1
+  double bound;     // by sum
+  template <bool SUMS>
   __device__ __forceinline__ bool holds(uint32_t before_cnt, uint32_t cnt, unsigned long long before,
                                         unsigned long long sum) const {
     if (cnt == 0) return false;
-    return by_count ? before_cnt < count && before_cnt + cnt >= count
-                    : (double)before < bound && (double)(before + sum) >= bound;
+    return SUMS ? (double)before < bound && (double)(before + sum) >= bound
+                : before_cnt < count && before_cnt + cnt >= count;
   }
 };
 
@@ -220,10 +225,10 @@ class Sampler {
     return cluster.map_shared_rank(p, r);
   }
 
-  // f(score, index) for the CTA's scores that can have a weight, eight per
-  // thread and step.
+  // f(score, index) for the CTA's scores from `cut` on, eight per thread and
+  // step.
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each(float cut, F f) const {
     const float kNone = -CUDART_INF_F;
     for (int v = threadIdx.x; v < n4; v += 2 * kThreads) {
       const float4 a = sc.get(v);
@@ -231,8 +236,12 @@ class Sampler {
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (x[e] >= row.least) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
+        if (x[e] >= cut) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
     }
+  }
+  // No score of a bin up to b0 is below this.
+  __device__ __forceinline__ float bin_cut(int b0) const {
+    return fmaxf(row.least, row.m - ((float)b0 + 1.f) / kBinScale);
   }
 
   __device__ __forceinline__ bool matches(const Match& mt, float zi, uint32_t idx) const {
@@ -246,22 +255,32 @@ class Sampler {
   }
 
   // Histogram of the matching tokens over the cluster into tcnt / tsum, by
-  // the next level's bins; of counts alone where no sums are needed.
-  __device__ void histogram(const Match& mt, bool sums, const Pieces& pc) {
+  // the next level's bins; of counts alone where no sums are needed.  Tokens
+  // whose weight rounds to 0 count too: they rank last.
+  template <bool SUMS>
+  __device__ void histogram(const Match& mt, const Pieces& pc) {
     const int tid = threadIdx.x;
-    for (int b = tid; b < kBins; b += kThreads) sh.cnt[b] = sh.lo[b] = sh.hi[b] = 0u;
+    for (int b = tid; b < kBins; b += kThreads) {
+      sh.cnt[b] = 0u;
+      if (SUMS) sh.lo[b] = sh.hi[b] = 0u;
+    }
     __syncthreads();
-    each([&](float zi, uint32_t idx) {
-      uint32_t w = 1u;
-      if (sums || zi < row.m - kSure) w = Row::fixed(row.w(zi));
-      if (w == 0u || !matches(mt, zi, idx)) return;
-      const int b = mt.level == 0 ? row.bin(zi) : pc.piece(rank_key(zi, idx));
+    auto add = [&](int b, float zi) {
       atomicAdd(&sh.cnt[b], 1u);
-      if (sums) {
+      if (SUMS) {
+        const uint32_t w = Row::fixed(row.w(zi));
         atomicAdd(&sh.lo[b], w & 0xFFFFu);
         atomicAdd(&sh.hi[b], w >> 16);
       }
-    });
+    };
+    if (mt.level == 0)
+      each(row.least, [&](float zi, uint32_t idx) {
+        if (row.within(zi, idx)) add(row.bin(zi), zi);
+      });
+    else
+      each(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
+        if (matches(mt, zi, idx)) add(pc.piece(rank_key(zi, idx)), zi);
+      });
     cluster.sync();
     // Each CTA adds up its share of the bins and gives every CTA the totals.
     const int share = kBins / cl;
@@ -273,7 +292,7 @@ class Sampler {
         if (r < cl) {
           const SampleShared* o = remote(&sh, r);
           c += o->cnt[b];
-          if (sums) s += o->lo[b] + ((unsigned long long)o->hi[b] << 16);
+          if (SUMS) s += o->lo[b] + ((unsigned long long)o->hi[b] << 16);
         }
       }
 #pragma unroll
@@ -281,7 +300,7 @@ class Sampler {
         if (r < cl) {
           SampleShared* o = remote(&sh, r);
           o->tcnt[b] = c;
-          o->tsum[b] = s;
+          if (SUMS) o->tsum[b] = s;
         }
       }
     }
@@ -311,53 +330,58 @@ class Sampler {
   }
 
   // The bin that holds the target, given what ranks before this histogram;
-  // false (uniform): there is none.  A target by sum with `of_all` set has its
-  // bound set to bound * the histogram's total first.
+  // false (uniform): there is none.  A target by sum (SUMS) with `of_all` set
+  // has its bound set to bound * the histogram's total first.
+  template <bool SUMS>
   __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, bool of_all) {
     constexpr int P = kBins / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t c = 0;
-    unsigned long long s = 0;
+    uint32_t xc[P], c = 0;
+    unsigned long long xs[P], s = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      c += sh.tcnt[tid * P + i];
-      s += sh.tsum[tid * P + i];
+      xc[i] = sh.tcnt[tid * P + i];
+      xs[i] = SUMS ? sh.tsum[tid * P + i] : 0ull;
+      c += xc[i];
+      s += xs[i];
     }
     uint32_t ic = c;
     unsigned long long is = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t oc = __shfl_up_sync(0xFFFFFFFFu, ic, o);
-      const unsigned long long os = __shfl_up_sync(0xFFFFFFFFu, is, o);
-      if (lane >= o) ic += oc, is += os;
+      if (lane >= o) ic += oc;
+      if (SUMS) {
+        const unsigned long long os = __shfl_up_sync(0xFFFFFFFFu, is, o);
+        if (lane >= o) is += os;
+      }
     }
     if (lane == 31) sh.warp_cnt[warp] = ic, sh.warp_sum[warp] = is;
     if (tid == 0) sh.f_bin = kBins;
     __syncthreads();
     unsigned long long all_sum = 0;
-    uint32_t bc = before_cnt;
-    unsigned long long bs = before_sum;
+    uint32_t bc = before_cnt + ic - c;
+    unsigned long long bs = before_sum + is - s;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      const unsigned long long x = sh.warp_sum[i];
-      if (i < warp) bc += sh.warp_cnt[i], bs += x;
-      all_sum += x;
+      if (i < warp) bc += sh.warp_cnt[i];
+      if (SUMS) {
+        const unsigned long long x = sh.warp_sum[i];
+        if (i < warp) bs += x;
+        all_sum += x;
+      }
     }
-    if (of_all) tg.bound *= (double)all_sum;
-    bc += ic - c;
-    bs += is - s;
+    if (SUMS && of_all) tg.bound *= (double)all_sum;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const uint32_t xc = sh.tcnt[tid * P + i];
-      const unsigned long long xs = sh.tsum[tid * P + i];
-      if (tg.holds(bc, xc, bs, xs)) {
+      if (tg.template holds<SUMS>(bc, xc[i], bs, xs[i])) {
         sh.f_bin = tid * P + i;
-        sh.f_cnt = xc;
+        sh.f_cnt = xc[i];
         sh.f_before_cnt = bc;
         sh.f_before_sum = bs;
       }
-      bc += xc;
-      bs += xs;
+      bc += xc[i];
+      bs += xs[i];
     }
     __syncthreads();
     return sh.f_bin < kBins;
@@ -368,10 +392,9 @@ class Sampler {
   // histogram lie between.
   __device__ void gather(const Match& mt) {
     uint32_t* cursor = remote(&sh.list_n, 0);
-    each([&](float zi, uint32_t idx) {
+    each(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
       if (!matches(mt, zi, idx)) return;
       const uint32_t w = Row::fixed(row.w(zi));
-      if (w == 0u) return;
       const uint32_t at = atomicAdd(cursor, 1u);
       const unsigned long long k = rank_key(zi, idx);
       if (at < kList)
@@ -385,7 +408,8 @@ class Sampler {
   }
 
   // After find_bin on the first histogram: the key of the target.
-  __device__ unsigned long long resolve(Target& tg, bool sums) {
+  template <bool SUMS>
+  __device__ unsigned long long resolve(Target& tg) {
     Match mt;
     mt.level = 1;
     mt.b0 = (int)sh.f_bin;
@@ -395,7 +419,9 @@ class Sampler {
     unsigned long long before_sum = sh.f_before_sum;
     while (cnt > kList) {  // uniform: every CTA of the cluster has the same totals
       unsigned long long low, high;
-      key_range([&](auto f) { each([&](float zi, uint32_t idx) { if (matches(mt, zi, idx)) f(rank_key(zi, idx)); }); }, low, high);
+      key_range([&](auto f) {
+        each(bin_cut(mt.b0), [&](float zi, uint32_t idx) { if (matches(mt, zi, idx)) f(rank_key(zi, idx)); });
+      }, low, high);
       if ((int)threadIdx.x < cl) {
         SampleShared* o = remote(&sh, threadIdx.x);
         o->cl_low[rank] = low;
@@ -407,8 +433,8 @@ class Sampler {
         high = sh.cl_best[r] > high ? sh.cl_best[r] : high;
       }
       const Pieces pc(low, high);
-      histogram(mt, sums, pc);
-      find_bin(tg, before_cnt, before_sum, false);
+      histogram<SUMS>(mt, pc);
+      find_bin<SUMS>(tg, before_cnt, before_sum, false);
       pc.narrow((int)sh.f_bin, mt.lo, mt.hi);
       mt.level = 2;
       before_cnt = sh.f_before_cnt;
@@ -441,7 +467,7 @@ class Sampler {
         atomicAdd(&sh.tsum[b], (unsigned long long)w);
       });
       __syncthreads();
-      find_bin(tg, before_cnt, before_sum, false);
+      find_bin<SUMS>(tg, before_cnt, before_sum, false);
       pc.narrow((int)sh.f_bin, lo, hi);
       before_cnt = sh.f_before_cnt;
       before_sum = sh.f_before_sum;
@@ -465,79 +491,87 @@ class Sampler {
         c += better;
         s += better ? sh.few.w[j] : 0u;
       }
-      if (tg.holds(c, 1u, s, sh.few.w[threadIdx.x])) sh.f_key = k;
+      if (tg.template holds<SUMS>(c, 1u, s, sh.few.w[threadIdx.x])) sh.f_key = k;
     }
     __syncthreads();
     return sh.f_key;
   }
 
-  // All candidates are the cnt <= kShort tokens of the list: apply the filters
-  // and draw, in every CTA alike (no cluster barrier).  Returns the
+  // All candidates are the cnt <= kShort tokens of the list: rank them, apply
+  // the filters and draw, in every CTA alike (no cluster barrier).  The filters
+  // are top-k (k > 0), then top-p as a bound on the sum of better ranks:
+  // `bound`, or, where that is negative, tp times what top-k keeps.  Returns the
   // total and the number kept; `mine` tells the thread whose token was drawn.
-  // The filters are top-k (k > 0), then top-p as a bound on the sum of better
-  // ranks: `bound`, or, where that is negative, tp times what top-k keeps.
-  __device__ void finish(int cnt, int k, float tp, double bound, float u, unsigned long long& total,
-                         uint32_t& kept, bool& mine, uint32_t& idx, uint32_t& weight) {
-    const int tid = threadIdx.x;
+  __device__ void finish(int cnt, int k, float tp, double bound, float u, unsigned long long& total, uint32_t& kept,
+                         bool& mine, uint32_t& idx, uint32_t& weight) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto& list = sh.list;
-    static_assert(kShort <= kThreads, "one candidate per thread");
-    unsigned long long key = kKeyAll, before = 0;
-    uint32_t w = 0, c = 0;
-    if (tid < cnt) {
-      key = list.key[tid];
-      w = list.w[tid];
-#pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        const bool better = list.key[j] < key;
-        c += better;
-        before += better ? list.w[j] : 0u;
+    constexpr int kSortWarps = kShort / 32;
+    static_assert(kShort <= kThreads && kShort <= kList, "one candidate per thread");
+    unsigned long long key = tid < cnt ? list.key[tid] : kKeyAll;
+    uint32_t w = tid < cnt ? list.w[tid] : 0u;
+    // Bitonic sort by key over the first kShort threads (as many as needed).
+    int size = 32;
+    while (size < cnt) size *= 2;
+    for (int b = 2; b <= size; b *= 2) {
+      for (int j = b / 2; j > 0; j /= 2) {
+        unsigned long long ok = key;
+        uint32_t ow = w;
+        if (j >= 32) {
+          __syncthreads();
+          if (tid < kShort) list.key[tid] = key, list.w[tid] = w;
+          __syncthreads();
+          if (tid < kShort) ok = list.key[tid ^ j], ow = list.w[tid ^ j];
+        } else if (warp < kSortWarps) {
+          ok = __shfl_xor_sync(0xFFFFFFFFu, key, j);
+          ow = __shfl_xor_sync(0xFFFFFFFFu, w, j);
+        }
+        const bool keep_less = ((tid & j) == 0) == ((tid & b) == 0);
+        if (keep_less ? ok < key : ok > key) key = ok, w = ow;
       }
     }
-    bool in = tid < cnt && (k <= 0 || c < (uint32_t)k);
-    uint32_t n;
-    unsigned long long s = block_sum(in ? w : 0u, in, n);
-    if (tp < 1.f) in = in && ((double)before < (bound >= 0.0 ? bound : (double)tp * (double)s) || c == 0u);
-    if (row.min_p > 0.f && in) {
-      in = row.w(order_float(~(uint32_t)(key >> kIdxBits))) >= row.min_p;
+    // Running sum by rank.
+    unsigned long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += x;
     }
-    total = block_sum(in ? w : 0u, in, kept);
-    const unsigned long long target = draw(u, total);
-    // Running sum in index order: the weights of the others that are kept.
-    if (tid < cnt && !in) list.w[tid] = 0u;
-    // K*: the worst kept key (min-p also keeps a prefix).
-    if (tid == 0) sh.f_key = 0;
     __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = inc;
+    if (tid < kShort) list.key[tid] = key, list.w[tid] = w;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortWarps; ++i)
+      if (i < warp) inc += sh.warp_sum[i];
+    if (bound < 0.0) {
+      // What top-k keeps.
+      const int last = (k > 0 && k < cnt ? k : cnt) - 1;
+      if (tid == last) sh.f_before_sum = inc;
+      __syncthreads();
+      bound = (double)tp * (double)sh.f_before_sum;
+    }
+    bool in = tid < cnt && (k <= 0 || tid < k) && w > 0u;
+    if (tp < 1.f) in = in && ((double)(inc - w) < bound || tid == 0);
+    if (row.min_p > 0.f) in = in && row.w(order_float(~(uint32_t)(key >> kIdxBits))) >= row.min_p;
+    kept = (uint32_t)__syncthreads_count(in);  // each filter keeps a prefix of the ranking
+    if (tid == (int)kept - 1) sh.f_before_sum = inc, sh.f_key = key;
+    __syncthreads();
+    total = sh.f_before_sum;
+    row.set_max(sh.f_key);
+    const unsigned long long target = draw(u, total);
+    // Running sum in index order.
     idx = (uint32_t)key & ((1u << kIdxBits) - 1);
     unsigned long long run = 0;
     if (in) {
-      atomicMax(&sh.f_key, key);
 #pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
+      for (uint32_t j = 0; j < kept; ++j) {
         const uint32_t oi = (uint32_t)list.key[j] & ((1u << kIdxBits) - 1);
         run += oi < idx ? list.w[j] : 0u;
       }
     }
     mine = in && target >= run && target < run + w;
     weight = w;
-    __syncthreads();
-    row.set_max(sh.f_key);
-  }
-
-  // Sum of v and count of `one` over the CTA.
-  __device__ unsigned long long block_sum(uint32_t v, bool one, uint32_t& n) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long s = v;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const uint32_t c = __popc(__ballot_sync(0xFFFFFFFFu, one));
-    __syncthreads();
-    if (lane == 0) sh.warp_sum[warp] = s, sh.warp_cnt[warp] = c;
-    __syncthreads();
-    s = 0;
-    n = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += sh.warp_sum[i], n += sh.warp_cnt[i];
-    return s;
   }
 
   // floor(u * total), in [0, total).
@@ -597,6 +631,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   const int start = rank * p.chunk;
   const int n = start < p.vocab ? (p.vocab - start < p.chunk ? p.vocab - start : p.chunk) : 0;
   const float temp = p.temperature ? __ldg(&p.temperature[r]) : 1.f;
+  const int k = p.top_k ? __ldg(&p.top_k[r]) : 0;
+  const float tp = p.top_p ? __ldg(&p.top_p[r]) : 1.f;
+  const float mp = p.min_p ? __ldg(&p.min_p[r]) : 0.f;
+  const float u = __ldg(&p.u[r]);
   const bool greedy = temp == 0.f;
   const bool valid = temp >= 0.f;
   const float inv = greedy ? 1.f : 1.f / temp;
@@ -658,8 +696,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   for (int i = 0; i < cl; ++i) ob = sh.cl_best[i] > ob ? sh.cl_best[i] : ob;
   float m = order_float((uint32_t)ob);
   const bool empty = !valid || m == -CUDART_INF_F;
-  const int k = p.top_k ? __ldg(&p.top_k[r]) : 0;
-  const float tp = p.top_p ? __ldg(&p.top_p[r]) : 1.f;
   float* probs = p.probs ? p.probs + (int64_t)r * p.vocab + start : nullptr;
   if (empty) {  // uniform over the cluster; no remote access follows
     if (rank == 0 && tid == 0) {
@@ -683,53 +719,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   Sampler<T> s(sh, sc, mis + n, (uint32_t)(start - mis));
   s.row.m = m;
   s.row.least = m - kCut;
-  const float mp = p.min_p ? __ldg(&p.min_p[r]) : 0.f;
   s.row.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;  // the best token passes
-  s.row.key_max = kKeyAll;
+  s.row.bounded = false;
   if (greedy || tp <= 0.f) {
     // Only the best token, the lowest index among equals: the least key.
     s.row.least = m;
     unsigned long long low, high;
-    s.key_range([&](auto f) { s.each([&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
+    s.key_range([&](auto f) { s.each(m, [&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
     if (tid < cl) cluster.map_shared_rank(&sh, tid)->cl_low[rank] = low;
     cluster.sync();
     for (int i = 0; i < cl; ++i) low = sh.cl_low[i] < low ? sh.cl_low[i] : low;
     s.row.set_max(low);
   }
-  const float u = __ldg(&p.u[r]);
   Match all;
   all.level = all.b0 = 0;
   all.lo = all.hi = 0;
   bool short_list = false;
   unsigned long long total = 0;
   uint32_t kept = 0;
-  const bool one = s.row.key_max != kKeyAll;
+  const bool one = s.row.bounded;
   const bool use_k = k > 0 && k < p.vocab && !one, use_p = tp < 1.f && !one;
-  for (int search = 0; search < 2 && !short_list; ++search) {  // 0: top-k, 1: top-p of what it left
-    if (search == 0 ? !use_k : !use_p) continue;
-    Target tg;
-    tg.by_count = search == 0;
-    tg.count = search == 0 ? (uint32_t)k : 0u;
-    tg.bound = (double)tp;
-    s.histogram(all, search == 1, Pieces(0, 0));
-    if (!s.find_bin(tg, 0u, 0ull, search == 1)) continue;
-    short_list = sh.f_before_cnt + sh.f_cnt <= kShort;
-    if (short_list) {
-      Match to;
-      to.level = -1;
-      to.b0 = (int)sh.f_bin;
-      s.gather(to);  // no remote access follows
-      const int cnt = (int)(sh.f_before_cnt + sh.f_cnt);
-      bool mine;
-      uint32_t idx, w;
-      s.finish(cnt, search == 0 && use_k ? k : 0, tp, search == 1 ? tg.bound : -1.0, u, total, kept, mine, idx, w);
-      if (rank == 0 && mine) {
-        p.token[r] = (int)idx;
-        if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
-      }
-    } else {
-      s.row.set_max(s.resolve(tg, search == 1));
+  // Top-k, then top-p of what it left.  A short list of candidates ends the row.
+  auto search = [&](auto by_sum, Target tg) {
+    constexpr bool SUMS = decltype(by_sum)::value;
+    s.template histogram<SUMS>(all, Pieces(0, 0));
+    if (!s.template find_bin<SUMS>(tg, 0u, 0ull, true)) return;
+    const uint32_t upto = sh.f_before_cnt + sh.f_cnt;
+    if (upto > kShort) {
+      s.row.set_max(s.template resolve<SUMS>(tg));
+      return;
     }
+    short_list = true;
+    Match to;
+    to.level = -1;
+    to.b0 = (int)sh.f_bin;
+    s.gather(to);  // no remote access follows
+    bool mine;
+    uint32_t idx, w;
+    s.finish((int)upto, SUMS ? 0 : k, tp, SUMS ? tg.bound : -1.0, u, total, kept, mine, idx, w);
+    if (rank == 0 && mine) {
+      p.token[r] = (int)idx;
+      if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+    }
+  };
+  if (use_k) {
+    Target tg;
+    tg.count = (uint32_t)k;
+    tg.bound = 0.0;
+    search(cuda::std::false_type{}, tg);
+  }
+  if (use_p && !short_list) {
+    Target tg;
+    tg.count = 0u;
+    tg.bound = (double)tp;
+    search(cuda::std::true_type{}, tg);
   }
   // Kept weight by warp: warp w owns a contiguous piece of the CTA's groups
   // of four.
@@ -747,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   if (!short_list) {
     unsigned long long sum = 0;
     uint32_t cnt = 0;
-    if (row.key_max == kKeyAll && row.min_p == 0.f) {  // no filter: exp and add
+    if (!row.bounded && row.min_p == 0.f) {  // no filter: exp and add
 #pragma unroll 2
       for (int v = p0 + lane; v < p1; v += 32) {
         const float4 x = sc.get(v);
