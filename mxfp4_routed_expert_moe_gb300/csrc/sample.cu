@@ -82,6 +82,7 @@ struct SampleShared {
   // Where a search ended.
   uint32_t f_bin, f_cnt, f_before_cnt;
   unsigned long long f_before_sum, f_key;
+  unsigned long long limit, target;
 };
 static_assert(MOE_SAMPLE_MAX_VOCAB <= kMostScores * kMaxCl, "a cluster takes the longest row");
 static_assert(MOE_SAMPLE_MAX_VOCAB == 1 << kIdxBits, "index bits of the key");
@@ -141,19 +142,23 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   return v;
 }
 
-// What a search looks for: the token of a given rank, or the last one whose
-// better ranks weigh less than a bound.
+// What a search looks for: the token of a given rank (its limit is the rank + 1),
+// or the last one whose better ranks weigh less than the limit.  A bound p * S
+// in double becomes a limit by rounding up: sums of integers are below the one
+// exactly when they are below the other, and the double arithmetic, which is
+// slow on this chip, is done once.
 struct Target {
-  uint32_t count;   // by count: >= 1, rank count - 1
-  double bound;     // by sum
+  unsigned long long limit;
   template <bool SUMS>
   __device__ __forceinline__ bool holds(uint32_t before_cnt, uint32_t cnt, unsigned long long before,
                                         unsigned long long sum) const {
     if (cnt == 0) return false;
-    return SUMS ? (double)before < bound && (double)(before + sum) >= bound
-                : before_cnt < count && before_cnt + cnt >= count;
+    return SUMS ? before < limit && before + sum >= limit : before_cnt < limit && before_cnt + cnt >= limit;
   }
 };
+__device__ __forceinline__ unsigned long long share_limit(float p, unsigned long long sum) {
+  return __double2ull_ru((double)p * (double)sum);
+}
 
 // Tokens that match the search so far: level -1 those down to bin b0, 0 all, 1
 // those of bin b0, 2 those of them with a key in [lo, hi].
@@ -330,10 +335,10 @@ class Sampler {
   }
 
   // The bin that holds the target, given what ranks before this histogram;
-  // false (uniform): there is none.  A target by sum (SUMS) with `of_all` set
-  // has its bound set to bound * the histogram's total first.
+  // false (uniform): there is none.  By sums, with p >= 0 the limit is first set
+  // to that share of the histogram's total.
   template <bool SUMS>
-  __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, bool of_all) {
+  __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, float p) {
     constexpr int P = kBins / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t xc[P], c = 0;
@@ -359,19 +364,23 @@ class Sampler {
     if (lane == 31) sh.warp_cnt[warp] = ic, sh.warp_sum[warp] = is;
     if (tid == 0) sh.f_bin = kBins;
     __syncthreads();
-    unsigned long long all_sum = 0;
+    if (SUMS && p >= 0.f) {
+      if (warp == 0) {
+        unsigned long long all = lane < kWarps ? sh.warp_sum[lane] : 0ull;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        if (lane == 0) sh.limit = share_limit(p, all);
+      }
+      __syncthreads();
+      tg.limit = sh.limit;
+    }
     uint32_t bc = before_cnt + ic - c;
     unsigned long long bs = before_sum + is - s;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) bc += sh.warp_cnt[i];
-      if (SUMS) {
-        const unsigned long long x = sh.warp_sum[i];
-        if (i < warp) bs += x;
-        all_sum += x;
-      }
+      if (SUMS && i < warp) bs += sh.warp_sum[i];
     }
-    if (SUMS && of_all) tg.bound *= (double)all_sum;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (tg.template holds<SUMS>(bc, xc[i], bs, xs[i])) {
@@ -434,7 +443,7 @@ class Sampler {
       }
       const Pieces pc(low, high);
       histogram<SUMS>(mt, pc);
-      find_bin<SUMS>(tg, before_cnt, before_sum, false);
+      find_bin<SUMS>(tg, before_cnt, before_sum, -1.f);
       pc.narrow((int)sh.f_bin, mt.lo, mt.hi);
       mt.level = 2;
       before_cnt = sh.f_before_cnt;
@@ -467,7 +476,7 @@ class Sampler {
         atomicAdd(&sh.tsum[b], (unsigned long long)w);
       });
       __syncthreads();
-      find_bin<SUMS>(tg, before_cnt, before_sum, false);
+      find_bin<SUMS>(tg, before_cnt, before_sum, -1.f);
       pc.narrow((int)sh.f_bin, lo, hi);
       before_cnt = sh.f_before_cnt;
       before_sum = sh.f_before_sum;
@@ -499,10 +508,11 @@ class Sampler {
 
   // All candidates are the cnt <= kShort tokens of the list: rank them, apply
   // the filters and draw, in every CTA alike (no cluster barrier).  The filters
-  // are top-k (k > 0), then top-p as a bound on the sum of better ranks:
-  // `bound`, or, where that is negative, tp times what top-k keeps.  Returns the
-  // total and the number kept; `mine` tells the thread whose token was drawn.
-  __device__ void finish(int cnt, int k, float tp, double bound, float u, unsigned long long& total, uint32_t& kept,
+  // are top-k (k > 0), then top-p as a limit on the sum of better ranks: that of
+  // the search by sums, or (`own_limit`) the share tp of what top-k keeps.
+  // Returns the total and the number kept; `mine` tells the thread whose token
+  // was drawn.
+  __device__ void finish(int cnt, int k, float tp, bool own_limit, float u, unsigned long long& total, uint32_t& kept,
                          bool& mine, uint32_t& idx, uint32_t& weight) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto& list = sh.list;
@@ -544,22 +554,23 @@ class Sampler {
 #pragma unroll
     for (int i = 0; i < kSortWarps; ++i)
       if (i < warp) inc += sh.warp_sum[i];
-    if (bound < 0.0) {
-      // What top-k keeps.
-      const int last = (k > 0 && k < cnt ? k : cnt) - 1;
-      if (tid == last) sh.f_before_sum = inc;
+    if (own_limit && tp < 1.f) {
+      if (tid == (k > 0 && k < cnt ? k : cnt) - 1) sh.limit = share_limit(tp, inc);
       __syncthreads();
-      bound = (double)tp * (double)sh.f_before_sum;
     }
     bool in = tid < cnt && (k <= 0 || tid < k) && w > 0u;
-    if (tp < 1.f) in = in && ((double)(inc - w) < bound || tid == 0);
+    if (tp < 1.f) in = in && (inc - w < sh.limit || tid == 0);
     if (row.min_p > 0.f) in = in && row.w(order_float(~(uint32_t)(key >> kIdxBits))) >= row.min_p;
     kept = (uint32_t)__syncthreads_count(in);  // each filter keeps a prefix of the ranking
-    if (tid == (int)kept - 1) sh.f_before_sum = inc, sh.f_key = key;
+    if (tid == (int)kept - 1) {
+      sh.f_before_sum = inc;
+      sh.f_key = key;
+      sh.target = draw(u, inc);
+    }
     __syncthreads();
     total = sh.f_before_sum;
     row.set_max(sh.f_key);
-    const unsigned long long target = draw(u, total);
+    const unsigned long long target = sh.target;
     // Running sum in index order.
     idx = (uint32_t)key & ((1u << kIdxBits) - 1);
     unsigned long long run = 0;
@@ -740,10 +751,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   const bool one = s.row.bounded;
   const bool use_k = k > 0 && k < p.vocab && !one, use_p = tp < 1.f && !one;
   // Top-k, then top-p of what it left.  A short list of candidates ends the row.
-  auto search = [&](auto by_sum, Target tg) {
+  auto search = [&](auto by_sum, Target tg, float share) {
     constexpr bool SUMS = decltype(by_sum)::value;
     s.template histogram<SUMS>(all, Pieces(0, 0));
-    if (!s.template find_bin<SUMS>(tg, 0u, 0ull, true)) return;
+    if (!s.template find_bin<SUMS>(tg, 0u, 0ull, share)) return;
     const uint32_t upto = sh.f_before_cnt + sh.f_cnt;
     if (upto > kShort) {
       s.row.set_max(s.template resolve<SUMS>(tg));
@@ -756,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     s.gather(to);  // no remote access follows
     bool mine;
     uint32_t idx, w;
-    s.finish((int)upto, SUMS ? 0 : k, tp, SUMS ? tg.bound : -1.0, u, total, kept, mine, idx, w);
+    s.finish((int)upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept, mine, idx, w);
     if (rank == 0 && mine) {
       p.token[r] = (int)idx;
       if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
@@ -764,15 +775,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   };
   if (use_k) {
     Target tg;
-    tg.count = (uint32_t)k;
-    tg.bound = 0.0;
-    search(cuda::std::false_type{}, tg);
+    tg.limit = (unsigned long long)k;
+    search(cuda::std::false_type{}, tg, -1.f);
   }
   if (use_p && !short_list) {
     Target tg;
-    tg.count = 0u;
-    tg.bound = (double)tp;
-    search(cuda::std::true_type{}, tg);
+    tg.limit = 0;
+    search(cuda::std::true_type{}, tg, tp);
   }
   // Kept weight by warp: warp w owns a contiguous piece of the CTA's groups
   // of four.
@@ -834,7 +843,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
       total += sh.cl_sum[i];
       kept += sh.cl_cnt[i];
     }
-    const unsigned long long target = Sampler<T>::draw(u, total);
+    if (tid == 0) sh.target = Sampler<T>::draw(u, total);
+    __syncthreads();
+    const unsigned long long target = sh.target;
     for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
     if (target >= before && target < before + sum) {  // one warp of the cluster
       unsigned long long run = before;
