@@ -18,7 +18,7 @@
 // a list, which each searches alone, in the same way.  Top-k is searched
 // first, by counts alone (no exponentials); what it drops, later passes skip.
 // When all tokens down to the end of the first bin found number at most kShort
-// (small top-k, peaked rows), every CTA gets them all and finishes alone.
+// (small top-k, peaked rows), the first CTA gets them all and finishes alone.
 // Bound by latency (cluster barriers of 0.8 us) for few rows, by the
 // instructions of the passes and the barriers for many: shared memory holds
 // some 38 rows of 128,000 scores on the chip at a time.  Reading the scores
@@ -67,11 +67,12 @@ struct SampleShared {
   unsigned long long tsum[kBins];  // the cluster's totals
   uint32_t tcnt[kBins];
   uint32_t list_n;  // rank 0's is the cluster's
+  unsigned long long end_total, end_key;  // of a row that rank 0 finished
   struct {  // the tokens of the list that are left
     unsigned long long key[kDirect];
     uint32_t w[kDirect];
   } few;
-  uint32_t few_n;
+  uint32_t few_n, list_at;
   unsigned long long warp_low[kWarps], cl_low[kMaxCl];
   unsigned long long warp_best[kWarps];
   unsigned long long warp_sum[kWarps];
@@ -231,14 +232,20 @@ class Sampler {
   }
 
   // f(score, index) for the CTA's scores from `cut` on, eight per thread and
-  // step.
-  template <typename F>
+  // step; FEW: most steps are expected to have none.
+  template <bool FEW = false, typename F>
   __device__ __forceinline__ void each(float cut, F f) const {
     const float kNone = -CUDART_INF_F;
     for (int v = threadIdx.x; v < n4; v += 2 * kThreads) {
       const float4 a = sc.get(v);
       const float4 b = v + kThreads < n4 ? sc.get(v + kThreads) : make_float4(kNone, kNone, kNone, kNone);
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      if (FEW) {
+        float most = x[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) most = fmaxf(most, x[e]);
+        if (!(most >= cut)) continue;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (x[e] >= cut) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
@@ -396,23 +403,33 @@ class Sampler {
     return sh.f_bin < kBins;
   }
 
-  // Hand every CTA the list of the matching tokens (in any order).  No CTA
-  // still reads the list of an earlier search: two cluster barriers of a
-  // histogram lie between.
-  __device__ void gather(const Match& mt) {
-    uint32_t* cursor = remote(&sh.list_n, 0);
-    each(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
+  // Hand the first `to` CTAs the list of the matching tokens (in any order).  A
+  // CTA collects its own first, where the totals of the histogram were, and then
+  // takes its place in the lists with one remote atomic: one per token cost a
+  // round trip each, in turn for the tokens of a warp.  No CTA still reads the
+  // list of an earlier search: two cluster barriers of a histogram lie between.
+  __device__ void gather(const Match& mt, int to) {
+    if (threadIdx.x == 0) sh.few_n = 0;
+    __syncthreads();
+    each<true>(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
       if (!matches(mt, zi, idx)) return;
-      const uint32_t w = Row::fixed(row.w(zi));
-      const uint32_t at = atomicAdd(cursor, 1u);
-      const unsigned long long k = rank_key(zi, idx);
-      if (at < kList)
-        for (int r = 0; r < cl; ++r) {
-          SampleShared* o = remote(&sh, r);
-          o->list.key[at] = k;
-          o->list.w[at] = w;
-        }
+      const uint32_t at = atomicAdd(&sh.few_n, 1u);
+      if (at < kList) sh.tsum[at] = rank_key(zi, idx);
     });
+    __syncthreads();
+    const uint32_t n = sh.few_n;
+    if (threadIdx.x == 0) sh.list_at = n ? atomicAdd(remote(&sh.list_n, 0), n) : 0u;
+    __syncthreads();
+    const uint32_t at = sh.list_at;
+    for (uint32_t i = threadIdx.x; i < n && at + i < kList; i += kThreads) {
+      const unsigned long long k = sh.tsum[i];
+      const uint32_t w = Row::fixed(row.w(order_float(~(uint32_t)(k >> kIdxBits))));
+      for (int r = 0; r < to; ++r) {
+        SampleShared* o = remote(&sh, r);
+        o->list.key[at + i] = k;
+        o->list.w[at + i] = w;
+      }
+    }
     cluster.sync();
   }
 
@@ -450,7 +467,7 @@ class Sampler {
       before_sum = sh.f_before_sum;
       cnt = sh.f_cnt;
     }
-    gather(mt);
+    gather(mt, cl);
     // Each CTA narrows the list down by itself.
     const auto& list = sh.list;
     const int n = (int)cnt;
@@ -507,7 +524,7 @@ class Sampler {
   }
 
   // All candidates are the cnt <= kShort tokens of the list: rank them, apply
-  // the filters and draw, in every CTA alike (no cluster barrier).  The filters
+  // the filters and draw (one CTA, no cluster barrier).  The filters
   // are top-k (k > 0), then top-p as a limit on the sum of better ranks: that of
   // the search by sums, or (`own_limit`) the share tp of what top-k keeps.
   // Returns the total and the number kept; `mine` tells the thread whose token
@@ -764,13 +781,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     Match to;
     to.level = -1;
     to.b0 = (int)sh.f_bin;
-    s.gather(to);  // no remote access follows
-    bool mine;
-    uint32_t idx, w;
-    s.finish((int)upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept, mine, idx, w);
-    if (rank == 0 && mine) {
-      p.token[r] = (int)idx;
-      if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+    s.gather(to, 1);
+    if (rank == 0) {
+      bool mine;
+      uint32_t idx, w;
+      s.finish((int)upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept, mine, idx, w);
+      if (mine) {
+        p.token[r] = (int)idx;
+        if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+      }
+      if (p.probs && tid < cl) {
+        SampleShared* o = cluster.map_shared_rank(&sh, tid);
+        o->end_total = total;
+        o->end_key = sh.f_key;
+      }
+    }
+    if (p.probs) {  // the others need the bound; no remote access follows
+      cluster.sync();
+      total = sh.end_total;
+      s.row.set_max(sh.end_key);
     }
   };
   if (use_k) {
