@@ -14,8 +14,8 @@
 // that the CTAs of the cluster add up over distributed shared memory: the
 // first by m - z in some 1,000 equal bins (a monotone function of z); if the
 // bin that holds the bound has more than kList tokens (ties), the next by equal
-// pieces of the range of its keys.  A bin of at most kList tokens goes to every CTA as
-// a list, which each searches alone, in the same way.  Top-k is searched
+// pieces of the range of its keys.  A bin of at most kList tokens goes to the
+// first CTA as a list, which it searches alone, in the same way.  Top-k is searched
 // first, by counts alone (no exponentials); what it drops, later passes skip.
 // When all tokens down to the end of the first bin found number at most kShort
 // (small top-k, peaked rows), the first CTA gets them all and finishes alone.
@@ -38,8 +38,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 1024;             // tokens of one bin that go to every CTA
-constexpr int kShort = 256;             // candidates that every CTA finishes alone
+constexpr int kList = 1024;             // tokens of one bin that go to one CTA
+constexpr int kShort = 256;             // candidates that one CTA finishes alone
 constexpr int kDirect = 128;            // tokens that are ranked pair by pair
 constexpr int kIdxBits = 18;             // MOE_SAMPLE_MAX_VOCAB = 2^18
 constexpr int kMaxCl = 8;
@@ -79,7 +79,7 @@ struct SampleShared {
   uint32_t warp_cnt[kWarps];
   unsigned long long cl_best[kMaxCl];
   unsigned long long cl_sum[kMaxCl];
-  uint32_t cl_cnt[kMaxCl];
+  uint32_t cl_cnt[kMaxCl], cl_kept[kMaxCl];
   // Where a search ended.
   uint32_t f_bin, f_cnt, f_before_cnt;
   unsigned long long f_before_sum, f_key;
@@ -134,13 +134,15 @@ struct Row {
   }
 };
 
+// Over a warp, on the 32-bit reduction instruction.
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const unsigned long long x = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = x > v ? x : v;
-  }
-  return v;
+  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(v >> 32));
+  return (unsigned long long)hi << 32 | __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+// For v whose sum over the warp is below 2^57 (weights: below 2^50).
+__device__ __forceinline__ unsigned long long warp_add(unsigned long long v) {
+  const uint32_t lo = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)v & 0x3FFFFFFu);
+  return ((unsigned long long)__reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 26)) << 26) + lo;
 }
 
 // What a search looks for: the token of a given rank (its limit is the rank + 1),
@@ -277,22 +279,32 @@ class Sampler {
       if (SUMS) sh.lo[b] = sh.hi[b] = 0u;
     }
     __syncthreads();
-    auto add = [&](int b, float zi) {
+    auto add = [&](int b, uint32_t w) {
       atomicAdd(&sh.cnt[b], 1u);
       if (SUMS) {
-        const uint32_t w = Row::fixed(row.w(zi));
         atomicAdd(&sh.lo[b], w & 0xFFFFu);
         atomicAdd(&sh.hi[b], w >> 16);
       }
     };
-    if (mt.level == 0)
-      each(row.least, [&](float zi, uint32_t idx) {
-        if (row.within(zi, idx)) add(row.bin(zi), zi);
-      });
-    else
+    if (mt.level == 0) {
+      // Weights of a whole group at once: in one branch per score, the latency
+      // of the exponential would not overlap.
+      for (int v = threadIdx.x; v < n4; v += kThreads) {
+        const float4 a = sc.get(v);
+        const float x[4] = {a.x, a.y, a.z, a.w};
+        if (!(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)) >= row.least)) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = SUMS ? Row::fixed(row.w(x[e])) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x[e] >= row.least && row.within(x[e], first + 4 * v + e)) add(row.bin(x[e]), w[e]);
+      }
+    } else {
       each(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
-        if (matches(mt, zi, idx)) add(pc.piece(rank_key(zi, idx)), zi);
+        if (matches(mt, zi, idx)) add(pc.piece(rank_key(zi, idx)), SUMS ? Row::fixed(row.w(zi)) : 0u);
       });
+    }
     cluster.sync();
     // Each CTA adds up its share of the bins and gives every CTA the totals.
     const int share = kBins / cl;
@@ -334,11 +346,8 @@ class Sampler {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.warp_low[threadIdx.x >> 5] = low, sh.warp_best[threadIdx.x >> 5] = high;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      low = sh.warp_low[i] < low ? sh.warp_low[i] : low;
-      high = sh.warp_best[i] > high ? sh.warp_best[i] : high;
-    }
+    low = ~warp_max(~sh.warp_low[threadIdx.x & (kWarps - 1)]);
+    high = warp_max(sh.warp_best[threadIdx.x & (kWarps - 1)]);
   }
 
   // The bin that holds the target, given what ranks before this histogram;
@@ -357,58 +366,60 @@ class Sampler {
       c += xc[i];
       s += xs[i];
     }
-    uint32_t ic = c;
-    unsigned long long is = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t oc = __shfl_up_sync(0xFFFFFFFFu, ic, o);
-      if (lane >= o) ic += oc;
-      if (SUMS) {
-        const unsigned long long os = __shfl_up_sync(0xFFFFFFFFu, is, o);
-        if (lane >= o) is += os;
-      }
+    const uint32_t wc = __reduce_add_sync(0xFFFFFFFFu, c);
+    const unsigned long long ws = SUMS ? warp_add(s) : 0ull;
+    if (lane == 0) {
+      sh.warp_cnt[warp] = wc;
+      if (SUMS) sh.warp_sum[warp] = ws;
     }
-    if (lane == 31) sh.warp_cnt[warp] = ic, sh.warp_sum[warp] = is;
     if (tid == 0) sh.f_bin = kBins;
     __syncthreads();
     if (SUMS && p >= 0.f) {
       if (warp == 0) {
-        unsigned long long all = lane < kWarps ? sh.warp_sum[lane] : 0ull;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+        const unsigned long long all = warp_add(lane < kWarps ? sh.warp_sum[lane] : 0ull);
         if (lane == 0) sh.limit = share_limit(p, all);
       }
       __syncthreads();
       tg.limit = sh.limit;
     }
-    uint32_t bc = before_cnt + ic - c;
-    unsigned long long bs = before_sum + is - s;
+    uint32_t bc = before_cnt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.warp_cnt[lane] : 0u);
+    unsigned long long bs = before_sum + (SUMS ? warp_add(lane < warp ? sh.warp_sum[lane] : 0ull) : 0ull);
+    if (tg.template holds<SUMS>(bc, wc, bs, ws)) {  // one warp at most
+      uint32_t ic = c;
+      unsigned long long is = s;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) bc += sh.warp_cnt[i];
-      if (SUMS && i < warp) bs += sh.warp_sum[i];
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (tg.template holds<SUMS>(bc, xc[i], bs, xs[i])) {
-        sh.f_bin = tid * P + i;
-        sh.f_cnt = xc[i];
-        sh.f_before_cnt = bc;
-        sh.f_before_sum = bs;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t oc = __shfl_up_sync(0xFFFFFFFFu, ic, o);
+        if (lane >= o) ic += oc;
+        if (SUMS) {
+          const unsigned long long os = __shfl_up_sync(0xFFFFFFFFu, is, o);
+          if (lane >= o) is += os;
+        }
       }
-      bc += xc[i];
-      bs += xs[i];
+      bc += ic - c;
+      bs += is - s;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (tg.template holds<SUMS>(bc, xc[i], bs, xs[i])) {
+          sh.f_bin = tid * P + i;
+          sh.f_cnt = xc[i];
+          sh.f_before_cnt = bc;
+          sh.f_before_sum = bs;
+        }
+        bc += xc[i];
+        bs += xs[i];
+      }
     }
     __syncthreads();
     return sh.f_bin < kBins;
   }
 
-  // Hand the first `to` CTAs the list of the matching tokens (in any order).  A
+  // Hand the first CTA the list of the matching tokens (in any order).  A
   // CTA collects its own first, where the totals of the histogram were, and then
   // takes its place in the lists with one remote atomic: one per token cost a
   // round trip each, in turn for the tokens of a warp.  No CTA still reads the
   // list of an earlier search: two cluster barriers of a histogram lie between.
-  __device__ void gather(const Match& mt, int to) {
+  __device__ void gather(const Match& mt) {
     if (threadIdx.x == 0) sh.few_n = 0;
     __syncthreads();
     each<true>(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
@@ -421,14 +432,12 @@ class Sampler {
     if (threadIdx.x == 0) sh.list_at = n ? atomicAdd(remote(&sh.list_n, 0), n) : 0u;
     __syncthreads();
     const uint32_t at = sh.list_at;
+    SampleShared* o = remote(&sh, 0);
     for (uint32_t i = threadIdx.x; i < n && at + i < kList; i += kThreads) {
       const unsigned long long k = sh.tsum[i];
       const uint32_t w = Row::fixed(row.w(order_float(~(uint32_t)(k >> kIdxBits))));
-      for (int r = 0; r < to; ++r) {
-        SampleShared* o = remote(&sh, r);
-        o->list.key[at + i] = k;
-        o->list.w[at + i] = w;
-      }
+      o->list.key[at + i] = k;
+      o->list.w[at + i] = w;
     }
     cluster.sync();
   }
@@ -467,8 +476,18 @@ class Sampler {
       before_sum = sh.f_before_sum;
       cnt = sh.f_cnt;
     }
-    gather(mt, cl);
-    // Each CTA narrows the list down by itself.
+    gather(mt);
+    if (rank == 0) {
+      const unsigned long long key = in_list<SUMS>(tg, cnt, before_cnt, before_sum);
+      if ((int)threadIdx.x < cl) remote(&sh, threadIdx.x)->end_key = key;
+    }
+    cluster.sync();
+    return sh.end_key;
+  }
+
+  // The key of the target among the cnt tokens of the list (one CTA).
+  template <bool SUMS>
+  __device__ unsigned long long in_list(Target& tg, uint32_t cnt, uint32_t before_cnt, unsigned long long before_sum) {
     const auto& list = sh.list;
     const int n = (int)cnt;
     unsigned long long lo = 0, hi = kKeyAll;
@@ -507,18 +526,24 @@ class Sampler {
       sh.few.w[at] = w;
     });
     __syncthreads();
-    if (threadIdx.x < cnt) {
-      const unsigned long long k = sh.few.key[threadIdx.x];
-      uint32_t c = before_cnt;
-      unsigned long long s = before_sum;
+    constexpr uint32_t kEach = kThreads / kDirect;  // threads of a token
+    static_assert(kEach * kDirect == kThreads && kEach <= 32, "neighbouring lanes share a token");
+    const uint32_t mine = threadIdx.x / kEach;
+    const unsigned long long k = mine < cnt ? sh.few.key[mine] : 0ull;
+    uint32_t c = 0;
+    unsigned long long s = 0;
 #pragma unroll 4
-      for (uint32_t j = 0; j < cnt; ++j) {
-        const bool better = sh.few.key[j] < k;
-        c += better;
-        s += better ? sh.few.w[j] : 0u;
-      }
-      if (tg.template holds<SUMS>(c, 1u, s, sh.few.w[threadIdx.x])) sh.f_key = k;
+    for (uint32_t j = threadIdx.x % kEach; j < cnt; j += kEach) {
+      const bool better = sh.few.key[j] < k;
+      c += better;
+      s += better ? sh.few.w[j] : 0u;
     }
+#pragma unroll
+    for (uint32_t o = 1; o < kEach; o *= 2) {
+      c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    }
+    if (mine < cnt && tg.template holds<SUMS>(before_cnt + c, 1u, before_sum + s, sh.few.w[mine])) sh.f_key = k;
     __syncthreads();
     return sh.f_key;
   }
@@ -711,18 +736,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     if (tid < 4) z[n + tid] = L::none();
   }
   // Largest score of the row.
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-  if (lane == 0) sh.warp_best[warp] = order_bits(best);
+  const uint32_t warp_most = __reduce_max_sync(0xFFFFFFFFu, order_bits(best));
+  if (lane == 0) sh.warp_cnt[warp] = warp_most;
   __syncthreads();
   if (warp == 0) {
-    const unsigned long long b = warp_max(lane < kWarps ? sh.warp_best[lane] : 0ull);
-    if (lane < cl) cluster.map_shared_rank(&sh, lane)->cl_best[rank] = b;
+    const uint32_t b = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_cnt[lane] : 0u);
+    if (lane < cl) cluster.map_shared_rank(&sh, lane)->cl_cnt[rank] = b;
   }
   cluster.sync();
-  unsigned long long ob = 0;
-  for (int i = 0; i < cl; ++i) ob = sh.cl_best[i] > ob ? sh.cl_best[i] : ob;
-  float m = order_float((uint32_t)ob);
+  float m = order_float(__reduce_max_sync(0xFFFFFFFFu, lane < cl ? sh.cl_cnt[lane] : 0u));
   const bool empty = !valid || m == -CUDART_INF_F;
   float* probs = p.probs ? p.probs + (int64_t)r * p.vocab + start : nullptr;
   if (empty) {  // uniform over the cluster; no remote access follows
@@ -781,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     Match to;
     to.level = -1;
     to.b0 = (int)sh.f_bin;
-    s.gather(to, 1);
+    s.gather(to);
     if (rank == 0) {
       bool mine;
       uint32_t idx, w;
@@ -849,33 +871,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
         for (int e = 0; e < 4; ++e) sum += w[e], cnt += w[e] != 0u;
       }
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      cnt += __shfl_xor_sync(0xFFFFFFFFu, cnt, o);
-    }
+    sum = warp_add(sum);
+    cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
     __syncthreads();  // warp_sum, warp_cnt are also find_bin's
     if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_cnt[warp] = cnt;
     __syncthreads();
-    if (tid < cl) {
-      unsigned long long a = 0;
-      uint32_t c = 0;
-      for (int i = 0; i < kWarps; ++i) a += sh.warp_sum[i], c += sh.warp_cnt[i];
-      SampleShared* o = cluster.map_shared_rank(&sh, tid);
-      o->cl_sum[rank] = a;
-      o->cl_cnt[rank] = c;
+    if (warp == 0) {
+      const unsigned long long a = warp_add(lane < kWarps ? sh.warp_sum[lane] : 0ull);
+      const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_cnt[lane] : 0u);
+      if (lane < cl) {
+        SampleShared* o = cluster.map_shared_rank(&sh, lane);
+        o->cl_sum[rank] = a;
+        o->cl_kept[rank] = c;
+      }
     }
     cluster.sync();  // no remote access follows
-    unsigned long long before = 0;
-    for (int i = 0; i < cl; ++i) {
-      if (i < rank) before += sh.cl_sum[i];
-      total += sh.cl_sum[i];
-      kept += sh.cl_cnt[i];
-    }
+    const unsigned long long of_cta = lane < cl ? sh.cl_sum[lane] : 0ull;
+    total = warp_add(of_cta);
+    kept = __reduce_add_sync(0xFFFFFFFFu, lane < cl ? sh.cl_kept[lane] : 0u);
+    unsigned long long before = warp_add((lane < rank ? of_cta : 0ull) + (lane < warp ? sh.warp_sum[lane] : 0ull));
     if (tid == 0) sh.target = Sampler<T>::draw(u, total);
     __syncthreads();
     const unsigned long long target = sh.target;
-    for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
     if (target >= before && target < before + sum) {  // one warp of the cluster
       unsigned long long run = before;
       for (int v0 = p0; v0 < p1; v0 += 32) {
