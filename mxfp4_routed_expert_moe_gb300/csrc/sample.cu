@@ -17,7 +17,7 @@
 // pieces of the range of its keys.  A bin of at most kList tokens goes to the
 // first CTA as a list, which it searches alone, in the same way.  Top-k is searched
 // first, by counts alone (no exponentials); what it drops, later passes skip.
-// When all tokens down to the end of the first bin found number at most kShort
+// When all tokens down to the end of the first bin found number at most kList
 // (small top-k, peaked rows), the first CTA gets them all and finishes alone.
 // Bound by latency (cluster barriers of 0.8 us) for few rows, by the
 // instructions of the passes and the barriers for many: shared memory holds
@@ -38,10 +38,10 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kList = 1024;             // tokens of one bin that go to one CTA
-constexpr int kShort = 256;             // candidates that one CTA finishes alone
+constexpr int kList = 1024;             // tokens that one CTA searches or finishes alone
 constexpr int kDirect = 128;            // tokens that are ranked pair by pair
 constexpr int kIdxBits = 18;             // MOE_SAMPLE_MAX_VOCAB = 2^18
+constexpr int kPiece = (1 << kIdxBits) / kBins;  // indices of one of kBins pieces of the longest row
 constexpr int kMaxCl = 8;
 constexpr int kMostScores = 65536;       // of a CTA
 constexpr int kMostBytes = 84 << 10;
@@ -58,20 +58,24 @@ struct SampleShared {
     struct {
       uint32_t cnt[kBins], lo[kBins], hi[kBins];
     };
-    // After the cluster has added them up: the tokens of one bin.
+    // After the cluster has added them up: the keys of some tokens, and
+    // cursors of the bins.
     struct {
-      unsigned long long key[kList];
-      uint32_t w[kList];
-    } list;
+      unsigned long long list[kList];
+      uint32_t cursor[kBins];
+    };
   };
   unsigned long long tsum[kBins];  // the cluster's totals
   uint32_t tcnt[kBins];
   uint32_t list_n;  // rank 0's is the cluster's
   unsigned long long end_total, end_key;  // of a row that rank 0 finished
-  struct {  // the tokens of the list that are left
-    unsigned long long key[kDirect];
-    uint32_t w[kDirect];
-  } few;
+  union {
+    struct {  // the tokens of the list that are left
+      unsigned long long key[kDirect];
+      uint32_t w[kDirect];
+    } few;
+    uint32_t piece_w[kPiece];  // weights of the kept tokens of a piece, by index
+  };
   uint32_t few_n, list_at;
   unsigned long long warp_low[kWarps], cl_low[kMaxCl];
   unsigned long long warp_best[kWarps];
@@ -82,6 +86,7 @@ struct SampleShared {
   uint32_t cl_cnt[kMaxCl], cl_kept[kMaxCl];
   // Where a search ended.
   uint32_t f_bin, f_cnt, f_before_cnt;
+  uint32_t f_w;
   unsigned long long f_before_sum, f_key;
   unsigned long long limit, target;
 };
@@ -110,6 +115,9 @@ struct Row {
   // definition, and the same function gives the same integers everywhere.
   __device__ __forceinline__ float w(float z) const { return expf(z - m); }
   __device__ __forceinline__ static uint32_t fixed(float w) { return __float2uint_rn(w * kFix); }
+  __device__ __forceinline__ uint32_t weight(unsigned long long key) const {
+    return fixed(w(order_float(~(uint32_t)(key >> kIdxBits))));
+  }
   // Bin of a score that is not below m - kCut: adding 2^23 leaves the rounded
   // product in the low bits (monotone in z; cheaper than a conversion).
   __device__ __forceinline__ int bin(float z) const {
@@ -155,7 +163,6 @@ struct Target {
   template <bool SUMS>
   __device__ __forceinline__ bool holds(uint32_t before_cnt, uint32_t cnt, unsigned long long before,
                                         unsigned long long sum) const {
-    if (cnt == 0) return false;
     return SUMS ? before < limit && before + sum >= limit : before_cnt < limit && before_cnt + cnt >= limit;
   }
 };
@@ -352,9 +359,11 @@ class Sampler {
 
   // The bin that holds the target, given what ranks before this histogram;
   // false (uniform): there is none.  By sums, with p >= 0 the limit is first set
-  // to that share of the histogram's total.
+  // to that share of the histogram's total.  `offsets`: tcnt becomes the number
+  // of tokens in better bins.
   template <bool SUMS>
-  __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, float p) {
+  __device__ bool find_bin(Target& tg, uint32_t before_cnt, unsigned long long before_sum, float p,
+                           bool offsets = false) {
     constexpr int P = kBins / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t xc[P], c = 0;
@@ -384,30 +393,44 @@ class Sampler {
     }
     uint32_t bc = before_cnt + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.warp_cnt[lane] : 0u);
     unsigned long long bs = before_sum + (SUMS ? warp_add(lane < warp ? sh.warp_sum[lane] : 0ull) : 0ull);
-    if (tg.template holds<SUMS>(bc, wc, bs, ws)) {  // one warp at most
+    const bool here = tg.template holds<SUMS>(bc, wc, bs, ws);  // one warp at most
+    if (here || offsets) {
       uint32_t ic = c;
-      unsigned long long is = s;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t oc = __shfl_up_sync(0xFFFFFFFFu, ic, o);
         if (lane >= o) ic += oc;
-        if (SUMS) {
+      }
+      bc += ic - c;
+    }
+    if (here) {
+      uint32_t at = bc;
+      if (SUMS) {
+        unsigned long long is = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
           const unsigned long long os = __shfl_up_sync(0xFFFFFFFFu, is, o);
           if (lane >= o) is += os;
         }
+        bs += is - s;
       }
-      bc += ic - c;
-      bs += is - s;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        if (tg.template holds<SUMS>(bc, xc[i], bs, xs[i])) {
+        if (tg.template holds<SUMS>(at, xc[i], bs, xs[i])) {
           sh.f_bin = tid * P + i;
           sh.f_cnt = xc[i];
-          sh.f_before_cnt = bc;
+          sh.f_before_cnt = at;
           sh.f_before_sum = bs;
         }
-        bc += xc[i];
+        at += xc[i];
         bs += xs[i];
+      }
+    }
+    if (offsets) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        sh.tcnt[tid * P + i] = bc;
+        bc += xc[i];
       }
     }
     __syncthreads();
@@ -421,6 +444,7 @@ class Sampler {
   // list of an earlier search: two cluster barriers of a histogram lie between.
   __device__ void gather(const Match& mt) {
     if (threadIdx.x == 0) sh.few_n = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) sh.cursor[b] = 0u;
     __syncthreads();
     each<true>(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
       if (!matches(mt, zi, idx)) return;
@@ -433,12 +457,7 @@ class Sampler {
     __syncthreads();
     const uint32_t at = sh.list_at;
     SampleShared* o = remote(&sh, 0);
-    for (uint32_t i = threadIdx.x; i < n && at + i < kList; i += kThreads) {
-      const unsigned long long k = sh.tsum[i];
-      const uint32_t w = Row::fixed(row.w(order_float(~(uint32_t)(k >> kIdxBits))));
-      o->list.key[at + i] = k;
-      o->list.w[at + i] = w;
-    }
+    for (uint32_t i = threadIdx.x; i < n && at + i < kList; i += kThreads) o->list[at + i] = sh.tsum[i];
     cluster.sync();
   }
 
@@ -488,28 +507,27 @@ class Sampler {
   // The key of the target among the cnt tokens of the list (one CTA).
   template <bool SUMS>
   __device__ unsigned long long in_list(Target& tg, uint32_t cnt, uint32_t before_cnt, unsigned long long before_sum) {
-    const auto& list = sh.list;
     const int n = (int)cnt;
     unsigned long long lo = 0, hi = kKeyAll;
     auto left = [&](auto f) {
       for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long k = list.key[i];
-        if (k >= lo && k <= hi) f(k, list.w[i]);
+        const unsigned long long k = sh.list[i];
+        if (k >= lo && k <= hi) f(k);
       }
     };
     while (cnt > kDirect) {
       unsigned long long low, high;
-      key_range([&](auto f) { left([&](unsigned long long k, uint32_t) { f(k); }); }, low, high);
+      key_range([&](auto f) { left(f); }, low, high);
       const Pieces pc(low, high);
       for (int b = threadIdx.x; b < kBins; b += kThreads) {
         sh.tcnt[b] = 0u;
         sh.tsum[b] = 0ull;
       }
       __syncthreads();
-      left([&](unsigned long long k, uint32_t w) {
+      left([&](unsigned long long k) {
         const int b = pc.piece(k);
         atomicAdd(&sh.tcnt[b], 1u);
-        atomicAdd(&sh.tsum[b], (unsigned long long)w);
+        if (SUMS) atomicAdd(&sh.tsum[b], (unsigned long long)row.weight(k));
       });
       __syncthreads();
       find_bin<SUMS>(tg, before_cnt, before_sum, -1.f);
@@ -520,12 +538,19 @@ class Sampler {
     }
     if (threadIdx.x == 0) sh.few_n = 0;
     __syncthreads();
-    left([&](unsigned long long k, uint32_t w) {
+    left([&](unsigned long long k) {
       const uint32_t at = atomicAdd(&sh.few_n, 1u);
       sh.few.key[at] = k;
-      sh.few.w[at] = w;
+      sh.few.w[at] = row.weight(k);
     });
     __syncthreads();
+    pick<SUMS>(tg, cnt, before_cnt, before_sum);
+    return sh.f_key;
+  }
+
+  // The target among sh.few, by comparing all pairs: f_key, f_w.
+  template <bool SUMS>
+  __device__ void pick(const Target& tg, uint32_t cnt, uint32_t before_cnt, unsigned long long before_sum) {
     constexpr uint32_t kEach = kThreads / kDirect;  // threads of a token
     static_assert(kEach * kDirect == kThreads && kEach <= 32, "neighbouring lanes share a token");
     const uint32_t mine = threadIdx.x / kEach;
@@ -543,88 +568,143 @@ class Sampler {
       c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
       s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     }
-    if (mine < cnt && tg.template holds<SUMS>(before_cnt + c, 1u, before_sum + s, sh.few.w[mine])) sh.f_key = k;
+    if (mine < cnt && tg.template holds<SUMS>(before_cnt + c, 1u, before_sum + s, sh.few.w[mine])) {
+      sh.f_key = k;
+      sh.f_w = sh.few.w[mine];
+    }
     __syncthreads();
-    return sh.f_key;
   }
 
-  // All candidates are the cnt <= kShort tokens of the list: rank them, apply
-  // the filters and draw (one CTA, no cluster barrier).  The filters
-  // are top-k (k > 0), then top-p as a limit on the sum of better ranks: that of
-  // the search by sums, or (`own_limit`) the share tp of what top-k keeps.
-  // Returns the total and the number kept; `mine` tells the thread whose token
-  // was drawn.
-  __device__ void finish(int cnt, int k, float tp, bool own_limit, float u, unsigned long long& total, uint32_t& kept,
-                         bool& mine, uint32_t& idx, uint32_t& weight) {
+  // All candidates are the cnt <= kList tokens of the list, those of the first
+  // bins of the histogram (tcnt: tokens in better bins): rank them, apply the
+  // filters and draw (one CTA, no cluster barrier).  The filters are top-k (k >
+  // 0), then top-p as a limit on the sum of better ranks: that of the search by
+  // sums, or (`own_limit`) the share tp of what top-k keeps.  f_key and f_w are
+  // the drawn token's index and weight.
+  __device__ void finish(uint32_t cnt, int k, float tp, bool own_limit, float u, unsigned long long& total,
+                         uint32_t& kept) {
+    constexpr int E = kList / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto& list = sh.list;
-    constexpr int kSortWarps = kShort / 32;
-    static_assert(kShort <= kThreads && kShort <= kList, "one candidate per thread");
-    unsigned long long key = tid < cnt ? list.key[tid] : kKeyAll;
-    uint32_t w = tid < cnt ? list.w[tid] : 0u;
-    // Bitonic sort by key over the first kShort threads (as many as needed).
-    int size = 32;
-    while (size < cnt) size *= 2;
-    for (int b = 2; b <= size; b *= 2) {
-      for (int j = b / 2; j > 0; j /= 2) {
-        unsigned long long ok = key;
-        uint32_t ow = w;
-        if (j >= 32) {
-          __syncthreads();
-          if (tid < kShort) list.key[tid] = key, list.w[tid] = w;
-          __syncthreads();
-          if (tid < kShort) ok = list.key[tid ^ j], ow = list.w[tid ^ j];
-        } else if (warp < kSortWarps) {
-          ok = __shfl_xor_sync(0xFFFFFFFFu, key, j);
-          ow = __shfl_xor_sync(0xFFFFFFFFu, w, j);
-        }
-        const bool keep_less = ((tid & j) == 0) == ((tid & b) == 0);
-        if (keep_less ? ok < key : ok > key) key = ok, w = ow;
-      }
+    constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1;
+    // Grouped by bin, then placed by comparing within the bin.
+    auto bin_of = [&](unsigned long long key) { return row.bin(order_float(~(uint32_t)(key >> kIdxBits))); };
+    for (uint32_t i = tid; i < cnt; i += kThreads) {
+      const unsigned long long x = sh.list[i];
+      const int b = bin_of(x);
+      sh.tsum[sh.tcnt[b] + atomicAdd(&sh.cursor[b], 1u)] = x;
     }
-    // Running sum by rank.
-    unsigned long long inc = w;
+    __syncthreads();
+    for (uint32_t i = tid; i < cnt; i += kThreads) {
+      const unsigned long long x = sh.tsum[i];
+      const int b = bin_of(x);
+      const uint32_t from = sh.tcnt[b], to = from + sh.cursor[b];
+      uint32_t at = from;
+#pragma unroll 4
+      for (uint32_t j = from; j < to; ++j) at += sh.tsum[j] < x;
+      sh.list[at] = x;
+    }
+    __syncthreads();
+    // Running sum by rank; a thread has ranks E * tid, ...
+    unsigned long long key[E], inc[E], sum = 0;
+    uint32_t w[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const bool is = E * tid + i < (int)cnt;
+      key[i] = is ? sh.list[E * tid + i] : kKeyAll;
+      w[i] = is ? row.weight(key[i]) : 0u;
+      sum += w[i];
+    }
+    unsigned long long run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += x;
+      const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, run, o);
+      if (lane >= o) run += x;
     }
+    if (lane == 31) sh.warp_sum[warp] = run;
     __syncthreads();
-    if (lane == 31) sh.warp_sum[warp] = inc;
-    if (tid < kShort) list.key[tid] = key, list.w[tid] = w;
-    __syncthreads();
+    run += warp_add(lane < warp ? sh.warp_sum[lane] : 0ull) - sum;
 #pragma unroll
-    for (int i = 0; i < kSortWarps; ++i)
-      if (i < warp) inc += sh.warp_sum[i];
+    for (int i = 0; i < E; ++i) inc[i] = run += w[i];
     if (own_limit && tp < 1.f) {
-      if (tid == (k > 0 && k < cnt ? k : cnt) - 1) sh.limit = share_limit(tp, inc);
+      const int last = (k > 0 && k < (int)cnt ? k : (int)cnt) - 1;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (E * tid + i == last) sh.limit = share_limit(tp, inc[i]);
       __syncthreads();
     }
-    bool in = tid < cnt && (k <= 0 || tid < k) && w > 0u;
-    if (tp < 1.f) in = in && (inc - w < sh.limit || tid == 0);
-    if (row.min_p > 0.f) in = in && row.w(order_float(~(uint32_t)(key >> kIdxBits))) >= row.min_p;
-    kept = (uint32_t)__syncthreads_count(in);  // each filter keeps a prefix of the ranking
-    if (tid == (int)kept - 1) {
-      sh.f_before_sum = inc;
-      sh.f_key = key;
-      sh.target = draw(u, inc);
+    bool in[E];
+    kept = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int e = E * tid + i;
+      in[i] = e < (int)cnt && (k <= 0 || e < k) && w[i] > 0u;
+      if (tp < 1.f) in[i] = in[i] && (inc[i] - w[i] < sh.limit || e == 0);
+      if (row.min_p > 0.f) in[i] = in[i] && row.w(order_float(~(uint32_t)(key[i] >> kIdxBits))) >= row.min_p;
+      kept += (uint32_t)__syncthreads_count(in[i]);  // each filter keeps a prefix of the ranking
     }
-    __syncthreads();
-    total = sh.f_before_sum;
-    row.set_max(sh.f_key);
-    const unsigned long long target = sh.target;
-    // Running sum in index order.
-    idx = (uint32_t)key & ((1u << kIdxBits) - 1);
-    unsigned long long run = 0;
-    if (in) {
-#pragma unroll 4
-      for (uint32_t j = 0; j < kept; ++j) {
-        const uint32_t oi = (uint32_t)list.key[j] & ((1u << kIdxBits) - 1);
-        run += oi < idx ? list.w[j] : 0u;
+    const bool direct = kept <= kDirect;
+    if (!direct) {
+      for (int b = tid; b < kBins; b += kThreads) sh.tsum[b] = 0ull;
+      if (tid < kPiece) sh.piece_w[tid] = 0u;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int e = E * tid + i;
+      if (e == (int)kept - 1) {
+        sh.end_total = inc[i];
+        sh.end_key = key[i];
+        sh.target = draw(u, inc[i]);
+      }
+      if (!in[i]) continue;
+      const uint32_t idx = (uint32_t)key[i] & kIdxMask;
+      if (direct) {
+        sh.few.key[e] = idx;
+        sh.few.w[e] = w[i];
+      } else {
+        atomicAdd(&sh.tsum[idx / kPiece], (unsigned long long)w[i]);
       }
     }
-    mine = in && target >= run && target < run + w;
-    weight = w;
+    __syncthreads();
+    total = sh.end_total;
+    // The first token in index order at which the running sum exceeds the target.
+    Target tg;
+    tg.limit = sh.target + 1;
+    if (direct) {
+      pick<true>(tg, kept, 0u, 0ull);
+      return;
+    }
+    // Of many: first the piece of the index range, then the token in it.
+    find_bin<true>(tg, 0u, 0ull, -1.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t idx = (uint32_t)key[i] & kIdxMask;
+      if (in[i] && idx / kPiece == sh.f_bin) sh.piece_w[idx % kPiece] = w[i];
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int kEach = kPiece / 32;
+      uint32_t x[kEach];
+      sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) x[i] = sh.piece_w[lane * kEach + i], sum += x[i];
+      run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += y;
+      }
+      run += sh.f_before_sum - sum;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (run < tg.limit && run + x[i] >= tg.limit) {
+          sh.f_key = sh.f_bin * kPiece + lane * kEach + i;
+          sh.f_w = x[i];
+        }
+        run += x[i];
+      }
+    }
+    __syncthreads();
   }
 
   // floor(u * total), in [0, total).
@@ -793,9 +873,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   auto search = [&](auto by_sum, Target tg, float share) {
     constexpr bool SUMS = decltype(by_sum)::value;
     s.template histogram<SUMS>(all, Pieces(0, 0));
-    if (!s.template find_bin<SUMS>(tg, 0u, 0ull, share)) return;
+    if (!s.template find_bin<SUMS>(tg, 0u, 0ull, share, rank == 0)) return;
     const uint32_t upto = sh.f_before_cnt + sh.f_cnt;
-    if (upto > kShort) {
+    if (upto > kList) {
       s.row.set_max(s.template resolve<SUMS>(tg));
       return;
     }
@@ -805,17 +885,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     to.b0 = (int)sh.f_bin;
     s.gather(to);
     if (rank == 0) {
-      bool mine;
-      uint32_t idx, w;
-      s.finish((int)upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept, mine, idx, w);
-      if (mine) {
-        p.token[r] = (int)idx;
-        if (p.logprob) p.logprob[r] = logf(__uint2float_rn(w) / __ull2float_rn(total));
+      s.finish(upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept);
+      if (tid == 0) {
+        p.token[r] = (int)sh.f_key;
+        if (p.logprob) p.logprob[r] = logf(__uint2float_rn(sh.f_w) / __ull2float_rn(total));
       }
-      if (p.probs && tid < cl) {
+      if (p.probs && tid > 0 && tid < cl) {
         SampleShared* o = cluster.map_shared_rank(&sh, tid);
-        o->end_total = total;
-        o->end_key = sh.f_key;
+        o->end_total = sh.end_total;
+        o->end_key = sh.end_key;
       }
     }
     if (p.probs) {  // the others need the bound; no remote access follows
