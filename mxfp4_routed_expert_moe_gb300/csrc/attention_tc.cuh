@@ -20,6 +20,13 @@
 // a row moves only when its maximum grew by more than 2^8 (then the warpgroup
 // rescales O_t in Tensor Memory): any reference gives the same quotient, and
 // 2^8 keeps every partial sum far inside fp32.
+//
+// A unit takes about 2.0 us with all SMs at work, 1.34 at the chip's measured
+// tensor rate: each half's chain of scores, softmax and P V is longer than the
+// other half's MMAs.  256 sequences of 56 query and 8 key heads over 32,768 shared
+// tokens take 212 us, start-up and join included: 1.1 PFLOP/s.  Scores in
+// buffers of 64 tokens, so that the next are computed during a softmax, took
+// 245 us: MMAs of 64 columns cost nearly as much as those of 128.
 #pragma once
 
 #include "serve.cuh"
@@ -199,7 +206,9 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       const AttnSeg g = *sg;
       drop_seg();
       const int32_t* table = attn_table(p, g.set);
-      for (int kv = g.kv0; kv < g.kv1 && ok; kv += kUnit) {
+      int kv = attn_first(p, g) - kUnit;
+      for (int n = (g.kv1 - g.kv0 + kUnit - 1) / kUnit; n > 0 && ok; --n) {
+        kv = kv + kUnit < g.kv1 ? kv + kUnit : g.kv0;
         const int left = g.kv1 - kv < kUnit ? g.kv1 - kv : kUnit;
         const int nb = (left + box - 1) / box;
         int page = 0, y = 0;
@@ -283,6 +292,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       const AttnSeg* sg = take_seg();
       if (!sg) break;
       const int kv0 = sg->kv0, kv1 = sg->kv1;
+      int left = kv1 - attn_first(p, *sg);  // tokens from the current unit on
       const bool two = sg->rows > kHalfRows;
       drop_seg();
       const int nt = (kv1 - kv0 + kUnit - 1) / kUnit;
@@ -303,7 +313,6 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       take(vbuf);
       if (nt > 1) take(kbuf);
       for (int j = 0; j < nt && ok; ++j) {
-        const int left = kv1 - kv0 - j * kUnit;
         const bool more = j + 1 < nt;
         if (left < kUnit) {
           // Rows of V past the length may hold anything, and 0 * NaN is NaN.
@@ -335,6 +344,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         }
         vbuf = vnext;
         kbuf = knext;
+        left = left > kUnit ? left - kUnit : kv1 - kv0;
       }
     }
     // No MMA may be in flight when Tensor Memory is released.
@@ -350,7 +360,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
           break;
         AttnSeg g;
         g.slot = -1;
-        more = more && attn_next(p, sd, w, g);
+        more = more && attn_next<true>(p, plan, sd, w, g);
         if (!more) g.slot = -1;
         if (lane == 0) {
           sh.seg[nseg % kSegs] = g;
@@ -409,7 +419,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         if (lane == 0) mbar_arrive(&sh.q_ready[t]);
       }
       float m = -CUDART_INF_F, l = 0.f;
-      for (int kv = kv0; kv < kv1; kv += kUnit) {
+      int kv = attn_first(p, *sg);
+      for (int n = (kv1 - kv0 + kUnit - 1) / kUnit; n > 0; --n) {
         ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.s_full[t], ns++ & 1, p));
         if (!ok) break;
         tc_fence_after();
@@ -471,9 +482,10 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
           weights(s, v, m == -CUDART_INF_F ? 0.f : m);
           if (!__any_sync(0xFFFFFFFFu, top > m + kGrow)) break;
           const float mn = top > m + kGrow ? top : m;
-          if (kv != kv0) {
+          if (__any_sync(0xFFFFFFFFu, m != -CUDART_INF_F)) {
             // O_t is complete up to the previous unit: its MMAs were issued
-            // before the scores that just arrived.
+            // before the scores that just arrived.  Without a maximum in any
+            // row it holds nothing yet, or zeros.
             const float f = m == mn ? 1.f : ex2(m - mn);
             l *= f;
 #pragma unroll 1
@@ -493,6 +505,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         float sa, sb;
         unpack2(add2(sum[0], sum[1]), sa, sb);
         l += sa + sb;
+        kv += kUnit;
+        if (kv >= sg->kv1) kv = sg->kv0;
       }
       if (!ok) break;
       float* slot = sd.slots + (int64_t)sg->slot * kAttnTcRows * (D + 2);

@@ -370,12 +370,19 @@ __device__ __forceinline__ bool attn_begin(const AttnParams& p, const AttnPlan& 
 
 // The next segment of the walk.
 struct AttnSeg {
-  int set, tok0, first_vis, len;  // the set
+  int set, tok0, len;  // the set
+  int first_vis;       // of an own part: tokens its first query token sees; of the prefix: where in [kv0, kv1) to begin
   int slot, kvh;
   int row0;      // first row of the tile in its set
   int rows;      // rows of the tile
   int kv0, kv1;  // token range [kv0, kv1) of the set, cut to what the tile's last row sees (may be empty)
 };
+
+// Where in [kv0, kv1) a segment begins; the rest follows in order, then what is
+// before it, from kv0 on.
+__device__ __forceinline__ int attn_first(const AttnParams& p, const AttnSeg& g) {
+  return g.set == p.b.batch ? g.first_vis : g.kv0;
+}
 
 __device__ __forceinline__ int attn_visible(const AttnParams& p, const AttnSeg& g, int i) {
   if (g.set == p.b.batch) return g.len;
@@ -383,7 +390,19 @@ __device__ __forceinline__ int attn_visible(const AttnParams& p, const AttnSeg& 
   return v < 0 ? 0 : (v > g.len ? g.len : v);
 }
 
-__device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnSide& sd, AttnWalk& w, AttnSeg& g) {
+// TURN: the segments of a long prefix begin where the ranges of other tiles are
+// at the same time, unit x as near as can be to x modulo the ranges' length
+// after the start.  The row tiles of a key head read the same cache; with every
+// range in plain order each unit came from HBM for most of them, once the
+// prefix was longer than L2 holds (256 sequences of up to 509 tokens behind
+// 32,768, 134 MB of prefix, 7 tiles a key head: 247 us in plain order, 229
+// turned).  What L2 holds is left in plain order, in which the CTAs ask for
+// different lines (9 prompts of up to 301 tokens behind 4,001: 117 us, 122
+// turned).
+constexpr long long kAttnTurnBytes = 96ll << 20;
+template <bool TURN>
+__device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& sh, const AttnSide& sd, AttnWalk& w,
+                                          AttnSeg& g) {
   if (w.u >= w.u1) return false;
   int tiles = w.a.tiles * p.kv_heads;
   while (w.u >= w.unit0 + (long long)tiles * w.a.units) {
@@ -421,6 +440,14 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnSide& s
   const long long e = r1 << sd.unit_shift;
   g.kv1 = e < vis ? (int)e : vis;
   if (g.kv1 < g.kv0) g.kv1 = g.kv0;
+  if (g.set == p.b.batch) g.first_vis = g.kv0;
+  if (TURN && g.set == p.b.batch && 4ll * p.head_dim * p.kv_heads * g.len > kAttnTurnBytes &&
+      sh.per[1] <= 0x7FFFFFFF) {
+    const int per = (int)sh.per[1], at = r0 % per;
+    const int past = (int)(w.u - n - (long long)w.worker * per);
+    const int turn = past >= at ? past - at : past - at + per;
+    if (turn < ((g.kv1 - g.kv0 + sd.unit - 1) >> sd.unit_shift)) g.first_vis += turn << sd.unit_shift;
+  }
   return true;
 }
 

@@ -221,3 +221,13 @@ def test_waits_give_up_and_next_call_is_correct(moe):
         else:
             assert t.equal(out, good)
         c.check()
+
+
+@pytest.mark.parametrize("dim,hk,prefix", [(128, 64, 3205), (64, 128, 3207)])
+def test_prefix_longer_than_the_cache_on_the_chip(moe, dim, hk, prefix):
+    """A prefix of more than 100 MB, two row tiles a key head: segments that begin inside their range."""
+    c = Case(moe, 21, q_lens=[140, 3], lens=[150, 20], prefix=prefix, page=64, hq=2 * hk, hk=hk, dim=dim, capacity=LONG)
+    c.check()
+    a, la = c.run()
+    b, lb = c.run()
+    assert torch().equal(a, b) and torch().equal(la, lb)
