@@ -92,8 +92,8 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, int x_dt
                   int32_t* status, void* stream);
 
 /* Bytes of device workspace moe_prefix_attention needs (0: bad arguments).  A
- * function of batch, tokens, max_q, q_heads, kv_heads, head_dim, prefix_len
- * (zero or not, and the number of rows that share it) and the device. */
+ * function of batch, tokens, max_q, q_heads, kv_heads, head_dim and of whether
+ * prefix_len is zero; nothing in it is kept from one call to the next. */
 size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_batch* batch, int q_heads);
 
 /* Attention.  Row (n, h): query n's head h, key head h / (q_heads / kv_heads).

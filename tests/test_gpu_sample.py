@@ -182,3 +182,21 @@ def test_graph_follows_the_parameters(moe):
     assert kept.tolist() == [17] * 4
     z, w = scaled(x, t.ones(4, device="cuda"))
     assert token.tolist() == [sample_row(z[i], w[i], 0.9, 17)[0] for i in range(4)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_candidate_lists_of_all_lengths(moe, dtype):
+    """Few to many candidates in one CTA's list, kept alone and cut further, at both ends of u."""
+    t = torch()
+    ks = [1, 2, 31, 32, 33, 127, 128, 129, 255, 256, 257, 511, 512, 513, 900, 1023, 1024, 1025, 2000]
+    rng = np.random.default_rng(77)
+    x = t.from_numpy((rng.standard_normal((len(ks), 50021)) * 2).astype(np.float32)).cuda()
+    if dtype == "bf16":
+        x = x.bfloat16()
+    temp = [1.7] * len(ks)  # flat: many tokens weigh alike
+    for u in (0.0, 0.37, 0.99999994):
+        check(moe, x, [u] * len(ks), temp, top_k=ks)
+        check(moe, x, [u] * len(ks), temp, top_k=ks, top_p=[0.9] * len(ks))
+        check(moe, x, [u] * len(ks), temp, top_k=ks, min_p=[0.2] * len(ks))
+    peaked = [0.25] * len(ks)
+    check(moe, x, rng.random(len(ks)).astype(np.float32).tolist(), peaked, top_p=np.linspace(0.05, 0.999, len(ks)).astype(np.float32).tolist())
