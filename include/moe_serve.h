@@ -67,6 +67,7 @@ typedef struct {
 } moe_kv_batch;
 
 #define MOE_SERVE_MAX_BATCH 4096
+#define MOE_SERVE_MAX_LEN (1 << 30) /* tokens of the prefix, and of an own part that attention reads */
 #define MOE_SAMPLE_MAX_VOCAB 262144
 
 /* Append: for every new token, k (rotated) and v go to the token's place in

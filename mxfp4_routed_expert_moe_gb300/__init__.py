@@ -279,5 +279,5 @@ class ExpertTable:
 
 
 # The operators around the layer in a serving step.
-from .serve import (KVBatch, KVCache, SAMPLE_MAX_VOCAB, SERVE_EXPORTS, SERVE_MAX_BATCH,  # noqa: E402
+from .serve import (KVBatch, KVCache, SAMPLE_MAX_VOCAB, SERVE_EXPORTS, SERVE_MAX_BATCH, SERVE_MAX_LEN,  # noqa: E402
                     attention_workspace_bytes, kv_append, prefix_attention, rope_table, sample)

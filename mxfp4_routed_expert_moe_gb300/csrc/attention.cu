@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
   const int rt = tile % p.tile_rows, kvh = tile / p.tile_rows % p.kv_heads, b = tile / p.tile_rows / p.kv_heads;
   const AttnRaw raw = attn_load(p, b);
   const int ql = raw.q1 - raw.q0, row0 = rt * kAttnWarpRows;
+  if ((b == 0 && raw.q0 != 0) || (b == p.b.batch - 1 && raw.q1 != p.b.tokens)) set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
   if (!attn_valid(p, raw)) return;  // uniform over the cluster, like all of the above
   const int rows = ql * p.group - row0 < kAttnWarpRows ? ql * p.group - row0 : kAttnWarpRows;
   if (rows <= 0) return;
@@ -275,11 +276,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
       }
       any = i >= 0 && i < p.b.max_q;  // attn_set refuses what else does not fit
     }
+    const AttnRaw raw = attn_load(p, b);
+    if (i < 0 || i >= raw.q1 - raw.q0) {  // of no sequence
+      any = false;
+      if (lane == 0) set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
+    }
     const AttnSide& sd = p.side[warp ? (p.side[1].own ? 1 : 0) : (p.side[1].prefix ? 1 : 0)];
     if (any) {
       // The batch's own entries are as the split kernel saw them: it lets this
       // kernel start only after everything before it is complete.
-      const AttnSet a = attn_set(p, sd, b, attn_load(p, b));
+      const AttnSet a = attn_set(p, sd, b, raw);
       t.units = a.units;
       t.tiles = a.tiles;
       t.i = i;
@@ -291,6 +297,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const AttnParams 
       t.unit0 = sd.unit_start[b];
       t.per = sd.unit_start[p.b.batch + 1];
       t.tile0 = sd.tile_start[b];
+      if (t.per == 0) t.units = 0;
     }
     if (lane == 0) sh_part[warp] = t;
   } else {

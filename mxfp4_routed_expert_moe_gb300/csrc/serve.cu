@@ -32,7 +32,7 @@ int check_batch(const moe_kv_batch* b) {
   if (b->table_stride < b->table_pages || (b->q_start && !aligned(b->q_start, 4))) return MOE_ERR_INVALID_ARG;
   if (!b->q_start && b->tokens != b->batch) return MOE_ERR_INVALID_ARG;
   if (b->prefix_len > 0 && (!b->prefix_table || !aligned(b->prefix_table, 4))) return MOE_ERR_INVALID_ARG;
-  if (b->batch > MOE_SERVE_MAX_BATCH || b->tokens > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+  if (b->prefix_len > MOE_SERVE_MAX_LEN || b->batch > MOE_SERVE_MAX_BATCH || b->tokens > (1 << 22)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -89,7 +89,7 @@ struct AttnSide {
   int workers;           // most workers
   int tile_cost;         // units that a tile counts beside its tokens'
   float* slots;          // [workers + tiles][rows * (head_dim + 2)]
-  long long* unit_start; // [batch + 1] first unit of each set; [batch + 1]: units per worker
+  long long* unit_start; // [batch + 1] first unit of each set; [batch + 1]: units per worker, 0: nothing was done
   int32_t* tile_start;   // [batch + 1] first tile of each set
 };
 
@@ -151,7 +151,7 @@ struct AttnSet {
 // Whether a sequence's entries fit the batch and its table (reported if not).
 __device__ __forceinline__ bool attn_valid(const AttnParams& p, const AttnRaw& r) {
   if (r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.b.tokens && r.q1 - r.q0 <= p.b.max_q && r.len >= 0 &&
-      r.len <= (long long)p.b.table_pages * p.page_size)
+      r.len <= MOE_SERVE_MAX_LEN && r.len <= (long long)p.b.table_pages * p.page_size)
     return true;
   set_status_word(p.status, MOE_ERR_DEVICE_CHECK);
   return false;
@@ -234,8 +234,11 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
   const int s1 = s0 + per_thread < nsets ? s0 + per_thread : nsets;
   long long u = 0;
   int t = 0;
+  bool falls = false;
   for (int s = s0; s < s1; ++s) {
-    const AttnSet a = attn_set(p, sd, s, attn_load(p, s));
+    const AttnRaw raw = attn_load(p, s);
+    falls |= raw.q1 < raw.q0;
+    const AttnSet a = attn_set(p, sd, s, raw);
     const int tiles = a.tiles * p.kv_heads;
     u += (long long)tiles * a.units;
     t += tiles;
@@ -255,7 +258,10 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
     sh.part_u[warp] = eu;
     sh.part_t[warp] = et;
   }
-  __syncthreads();
+  // Where q_start falls, sequences may overlap, and their tiles be more than
+  // the workspace has slots for: nothing is done on their side (attn_valid has
+  // reported it).
+  const bool broken = __syncthreads_or(falls);
   long long total = 0;
   eu -= u;  // exclusive
   et -= t;
@@ -267,6 +273,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
     }
     total += x;
   }
+  if (broken) total = 0;
   if (tid == 0) {
     long long other = 0;
     if (two) {
@@ -309,7 +316,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
     if (blockIdx.x == 0) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (p.side[i].unit_start) p.side[i].unit_start[nsets] = sh.per[i];
+        if (p.side[i].unit_start) p.side[i].unit_start[nsets] = broken && i == own ? 0 : sh.per[i];
       if (two) {
         p.side[own ^ 1].unit_start[p.b.batch] = 0;
         p.side[own ^ 1].tile_start[p.b.batch] = 0;

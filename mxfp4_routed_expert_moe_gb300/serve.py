@@ -8,12 +8,14 @@ import ctypes
 from . import DT_BF16, DT_F32, MoeError, _check, _ptr, lib
 
 __all__ = ["KVCache", "KVBatch", "kv_append", "prefix_attention", "attention_workspace_bytes", "sample",
-           "rope_table", "SERVE_EXPORTS", "SAMPLE_MAX_VOCAB", "SERVE_MAX_BATCH"]
+           "rope_table", "SERVE_EXPORTS", "SAMPLE_MAX_VOCAB", "SERVE_MAX_BATCH",
+           "SERVE_MAX_LEN"]
 
 # Every symbol moe_serve.h declares (checked by the tests against the .so).
 SERVE_EXPORTS = ("moe_kv_append", "moe_attention_workspace_bytes", "moe_prefix_attention", "moe_sample")
 SAMPLE_MAX_VOCAB = 1 << 18   # MOE_SAMPLE_MAX_VOCAB
 SERVE_MAX_BATCH = 4096       # MOE_SERVE_MAX_BATCH
+SERVE_MAX_LEN = 1 << 30      # MOE_SERVE_MAX_LEN
 
 
 class _Cache(ctypes.Structure):

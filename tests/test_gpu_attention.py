@@ -231,3 +231,23 @@ def test_prefix_longer_than_the_cache_on_the_chip(moe, dim, hk, prefix):
     a, la = c.run()
     b, lb = c.run()
     assert torch().equal(a, b) and torch().equal(la, lb)
+
+
+def test_broken_starts_are_reported(moe):
+    """q_start that falls (sequences would overlap, and their tiles be more than the workspace holds), or that
+    leaves rows to no sequence: reported."""
+    t = torch()
+    for rows, capacity in ((1, 0), (1, LONG), (40, LONG), (300, LONG)):
+        c = Case(moe, 6, [rows] * 8, [rows + 50] * 8, 33, 16, 4, 2, 64, capacity=capacity, max_q=8 * rows)
+        good, lse = c.run()
+        keep = c.batch.q_start.clone()
+        for bad in ([0, 8 * rows] * 4 + [8 * rows], [0] * 8 + [7 * rows], [1] + [8 * rows] * 8):
+            c.batch.q_start.copy_(t.tensor(bad, dtype=t.int32))
+            out = t.empty_like(good)
+            status = t.zeros(1, dtype=t.int32, device="cuda")
+            moe.prefix_attention(c.cache, c.batch, c.q, out, c.ws, status=status)
+            t.cuda.synchronize()
+            assert int(status.item()) == moe.MOE_ERR_DEVICE_CHECK, bad
+        c.batch.q_start.copy_(keep)
+        again, lse2 = c.run()
+        assert t.equal(good, again) and t.equal(lse, lse2)

@@ -186,3 +186,10 @@ def test_binding_checks_shapes_and_types(moe):
         moe.sample(x, u, tok, top_k=u, stream=0)
     with pytest.raises(ValueError):
         moe.sample(x.t(), u, tok, stream=0)
+
+
+def test_lengths_past_what_attention_counts_are_refused(serve, moe):
+    assert re.search(r"MOE_SERVE_MAX_LEN \(1 << 30\)", open(HEADER).read()) and moe.SERVE_MAX_LEN == 1 << 30
+    c, b = cache(serve), batch(serve, prefix_len=moe.SERVE_MAX_LEN + 1, prefix_table=A)
+    assert append(serve, c, b) == 2 and attend(serve, c, b) == 2
+    assert serve._lib().moe_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 4) == 0
