@@ -21,12 +21,10 @@
 // rescales O_t in Tensor Memory): any reference gives the same quotient, and
 // 2^8 keeps every partial sum far inside fp32.
 //
-// A unit takes about 2.0 us with all SMs at work, 1.34 at the chip's measured
-// tensor rate: each half's chain of scores, softmax and P V is longer than the
-// other half's MMAs.  256 sequences of 56 query and 8 key heads over 32,768 shared
-// tokens take 212 us, start-up and join included: 1.1 PFLOP/s.  Scores in
-// buffers of 64 tokens, so that the next are computed during a softmax, took
-// 245 us: MMAs of 64 columns cost nearly as much as those of 128.
+// A unit takes 1.51 us with all SMs at work, 1.34 at the chip's measured tensor
+// rate: 256 sequences of 56 query and 8 key heads over a shared prefix alone take
+// 172 us for 32,768 tokens and 315 for 65,536, start-up and join included, 1.69
+// PFLOP/s between the two.
 #pragma once
 
 #include "serve.cuh"

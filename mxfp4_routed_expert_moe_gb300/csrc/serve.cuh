@@ -116,9 +116,13 @@ __host__ __device__ constexpr int attn_warp_unit(int head_dim) { return head_dim
 // tokens.
 constexpr int kAttnTcRows = 256;
 constexpr int kAttnTcUnit = 128;
-// Measured time of a unit in us: of a worker among seven, and of a tile of more
-// than 128 rows; and how much longer the Tensor Memory side takes to get going.
-constexpr float kAttnWarpUnitCost = 1.65f, kAttnTcUnitCost = 1.65f, kAttnTcStart = 5.f;
+// For sharing the CTAs out: time of a unit in us, of a worker among seven and of
+// a tile of more than 128 rows; how much longer the Tensor Memory side takes to
+// get going; and the units that a tile of the warp side counts beside its
+// tile_cost, since few CTAs take many tiles in turn next to a busy other side
+// (256 sequences with one token each of their own behind 32,768: 190 us, 212
+// without).
+constexpr float kAttnWarpUnitCost = 1.5f, kAttnTcUnitCost = 1.6f, kAttnTcStart = 5.f, kAttnWarpTileMore = 0.7f;
 
 // What a set's entries say, as loaded.
 struct AttnRaw {
@@ -263,6 +267,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
   // reported it).
   const bool broken = __syncthreads_or(falls);
   long long total = 0;
+  int tiles = 0;
   eu -= u;  // exclusive
   et -= t;
   for (int i = 0; i < nwarps; ++i) {
@@ -272,6 +277,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
       et += sh.part_t[i];
     }
     total += x;
+    tiles += sh.part_t[i];
   }
   if (broken) total = 0;
   if (tid == 0) {
@@ -287,7 +293,9 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
     // with c the time that their units cost one CTA.  Sides with units get one
     // CTA at least.
     const int n = gridDim.x;
-    const float c1 = (float)sh.total[1] * kAttnTcUnitCost, c0 = (float)sh.total[0] * (kAttnWarpUnitCost / kAttnWarpWorkers);
+    const float more = own == 0 ? kAttnWarpTileMore * (float)tiles : 0.f;
+    const float c1 = (float)sh.total[1] * kAttnTcUnitCost;
+    const float c0 = ((float)sh.total[0] + more) * (kAttnWarpUnitCost / kAttnWarpWorkers);
     int n1 = sh.total[1] == 0 ? 0 : n;
     if (n1 > 0 && sh.total[0] > 0) {
       int lo = 1, hi = n - 1;
