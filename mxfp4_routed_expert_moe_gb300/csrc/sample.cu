@@ -49,6 +49,7 @@ constexpr int kMostScores = 65536;       // of a CTA
 constexpr int kMostBytes = 84 << 10;
 constexpr float kFix = 2147483648.f;     // 2^31
 constexpr float kBinScale = 45.9f;       // times kCut: below kBins - 1
+constexpr uint32_t kSureBins = 700;      // weights of 2^31 exp(-15) and more
 constexpr float kCut = 22.25f;           // below m - kCut every W is 0
 constexpr unsigned long long kKeyAll = ~0ull;
 
@@ -230,6 +231,10 @@ class Sampler {
   int cl, rank;
   Row row;
   cg::cluster_group cluster;
+  // What this CTA's tokens add to the bins of the last histogram by sums, bins
+  // kBins / kThreads * tid and on; and the tokens that it gave to the list.
+  unsigned long long own_sum[kBins / kThreads];
+  uint32_t own_cnt[kBins / kThreads], own_listed;
 
   __device__ Sampler(SampleShared& s, const Scores<T>& scores, int n, uint32_t f)
       : sh(s), sc(scores), n4((n + 3) / 4), first(f), cluster(cg::this_cluster()) {
@@ -242,29 +247,33 @@ class Sampler {
     return cluster.map_shared_rank(p, r);
   }
 
-  // f(score, index) for the CTA's scores from `cut` on, eight per thread and
-  // step; FEW: most steps are expected to have none.
+  // f(score, index) for the CTA's scores from `cut` to `top`, eight per thread
+  // and step; FEW: most steps are expected to have none.
   template <bool FEW = false, typename F>
-  __device__ __forceinline__ void each(float cut, F f) const {
+  __device__ __forceinline__ void each(float cut, float top, F f) const {
     const float kNone = -CUDART_INF_F;
     for (int v = threadIdx.x; v < n4; v += 2 * kThreads) {
       const float4 a = sc.get(v);
       const float4 b = v + kThreads < n4 ? sc.get(v + kThreads) : make_float4(kNone, kNone, kNone, kNone);
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       if (FEW) {
-        float most = x[0];
+        bool any = false;
 #pragma unroll
-        for (int e = 1; e < 8; ++e) most = fmaxf(most, x[e]);
-        if (!(most >= cut)) continue;
+        for (int e = 0; e < 8; ++e) any |= x[e] >= cut && x[e] <= top;
+        if (!any) continue;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (x[e] >= cut) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
+        if (x[e] >= cut && x[e] <= top) f(x[e], first + 4 * (v + (e >> 2) * kThreads) + (e & 3));
     }
   }
   // No score of a bin up to b0 is below this.
   __device__ __forceinline__ float bin_cut(int b0) const {
     return fmaxf(row.least, row.m - ((float)b0 + 1.f) / kBinScale);
+  }
+  // No score that matches is above this.
+  __device__ __forceinline__ float bin_top(const Match& mt) const {
+    return mt.level < 1 ? CUDART_INF_F : row.m - ((float)mt.b0 - 1.f) / kBinScale;
   }
 
   __device__ __forceinline__ bool matches(const Match& mt, float zi, uint32_t idx) const {
@@ -310,7 +319,7 @@ class Sampler {
           if (x[e] >= row.least && row.within(x[e], first + 4 * v + e)) add(row.bin(x[e]), w[e]);
       }
     } else {
-      each(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
+      each(bin_cut(mt.b0), bin_top(mt), [&](float zi, uint32_t idx) {
         if (matches(mt, zi, idx)) add(pc.piece(rank_key(zi, idx)), SUMS ? Row::fixed(row.w(zi)) : 0u);
       });
     }
@@ -337,6 +346,14 @@ class Sampler {
         }
       }
     }
+    if (SUMS) {
+#pragma unroll
+      for (int i = 0; i < kBins / kThreads; ++i) {
+        const int b = tid * (kBins / kThreads) + i;
+        own_cnt[i] = sh.cnt[b];
+        own_sum[i] = sh.lo[b] + ((unsigned long long)sh.hi[b] << 16);
+      }
+    }
     if (tid == 0) sh.list_n = 0;
     cluster.sync();
   }
@@ -357,6 +374,21 @@ class Sampler {
     __syncthreads();
     low = ~warp_max(~sh.warp_low[threadIdx.x & (kWarps - 1)]);
     high = warp_max(sh.warp_best[threadIdx.x & (kWarps - 1)]);
+  }
+
+  // Sums of weights by bin within a CTA: the halves are added apart, on native
+  // atomics, and joined by the thread that reads the bin in find_bin.
+  __device__ __forceinline__ void add_weight(int b, uint32_t w) {
+    uint32_t* half = reinterpret_cast<uint32_t*>(&sh.tsum[b]);
+    atomicAdd(half, w & 0xFFFFu);
+    atomicAdd(half + 1, w >> 16);
+  }
+  __device__ __forceinline__ void join_weights() {
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; ++i) {
+      const unsigned long long x = sh.tsum[threadIdx.x * (kBins / kThreads) + i];
+      sh.tsum[threadIdx.x * (kBins / kThreads) + i] = (x & 0xFFFFFFFFull) + ((x >> 32) << 16);
+    }
   }
 
   // The bin that holds the target, given what ranks before this histogram;
@@ -448,13 +480,13 @@ class Sampler {
     if (threadIdx.x == 0) sh.few_n = 0;
     for (int b = threadIdx.x; b < kBins; b += kThreads) sh.cursor[b] = 0u;
     __syncthreads();
-    each<true>(bin_cut(mt.b0), [&](float zi, uint32_t idx) {
+    each<true>(bin_cut(mt.b0), bin_top(mt), [&](float zi, uint32_t idx) {
       if (!matches(mt, zi, idx)) return;
       const uint32_t at = atomicAdd(&sh.few_n, 1u);
       if (at < kList) sh.tsum[at] = rank_key(zi, idx);
     });
     __syncthreads();
-    const uint32_t n = sh.few_n;
+    const uint32_t n = own_listed = sh.few_n;
     if (threadIdx.x == 0) sh.list_at = n ? atomicAdd(remote(&sh.list_n, 0), n) : 0u;
     __syncthreads();
     const uint32_t at = sh.list_at;
@@ -476,7 +508,7 @@ class Sampler {
     while (cnt > kList) {  // uniform: every CTA of the cluster has the same totals
       unsigned long long low, high;
       key_range([&](auto f) {
-        each(bin_cut(mt.b0), [&](float zi, uint32_t idx) { if (matches(mt, zi, idx)) f(rank_key(zi, idx)); });
+        each(bin_cut(mt.b0), bin_top(mt), [&](float zi, uint32_t idx) { if (matches(mt, zi, idx)) f(rank_key(zi, idx)); });
       }, low, high);
       if ((int)threadIdx.x < cl) {
         SampleShared* o = remote(&sh, threadIdx.x);
@@ -529,9 +561,10 @@ class Sampler {
       left([&](unsigned long long k) {
         const int b = pc.piece(k);
         atomicAdd(&sh.tcnt[b], 1u);
-        if (SUMS) atomicAdd(&sh.tsum[b], (unsigned long long)row.weight(k));
+        if (SUMS) add_weight(b, row.weight(k));
       });
       __syncthreads();
+      if (SUMS) join_weights();
       find_bin<SUMS>(tg, before_cnt, before_sum, -1.f);
       pc.narrow((int)sh.f_bin, lo, hi);
       before_cnt = sh.f_before_cnt;
@@ -664,7 +697,7 @@ class Sampler {
         sh.few.key[e] = idx;
         sh.few.w[e] = w[i];
       } else {
-        atomicAdd(&sh.tsum[idx / kPiece], (unsigned long long)w[i]);
+        add_weight(idx / kPiece, w[i]);
       }
     }
     __syncthreads();
@@ -677,6 +710,7 @@ class Sampler {
       return;
     }
     // Of many: first the piece of the index range, then the token in it.
+    join_weights();
     find_bin<true>(tg, 0u, 0ull, -1.f);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -857,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     // Only the best token, the lowest index among equals: the least key.
     s.row.least = m;
     unsigned long long low, high;
-    s.key_range([&](auto f) { s.each(m, [&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
+    s.key_range([&](auto f) { s.each(m, m, [&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
     if (tid < cl) cluster.map_shared_rank(&sh, tid)->cl_low[rank] = low;
     cluster.sync();
     for (int i = 0; i < cl; ++i) low = sh.cl_low[i] < low ? sh.cl_low[i] : low;
@@ -866,7 +900,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   Match all;
   all.level = all.b0 = 0;
   all.lo = all.hi = 0;
-  bool short_list = false;
+  bool short_list = false, by_bins = false;
+  unsigned long long sum = 0;  // by_bins: of this thread's share of the CTA's kept tokens
+  uint32_t count = 0;
   unsigned long long total = 0;
   uint32_t kept = 0;
   const bool one = s.row.bounded;
@@ -878,7 +914,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     if (!s.template find_bin<SUMS>(tg, 0u, 0ull, share, rank == 0)) return;
     const uint32_t upto = sh.f_before_cnt + sh.f_cnt;
     if (upto > kList) {
-      s.row.set_max(s.template resolve<SUMS>(tg));
+      const uint32_t bin = sh.f_bin, cnt = sh.f_cnt;
+      const unsigned long long key = s.template resolve<SUMS>(tg);
+      s.row.set_max(key);
+      // With the bin's tokens listed one by one, each CTA knows what its kept
+      // tokens weigh without another pass.  (In the bins up to kSureBins no
+      // weight rounds to 0, so that tokens counted are tokens kept.)
+      if (SUMS && s.row.min_p == 0.f && cnt <= kList && bin < kSureBins) {
+        by_bins = true;
+#pragma unroll
+        for (int i = 0; i < kBins / kThreads; ++i)
+          if (tid * (kBins / kThreads) + i < (int)bin) sum += s.own_sum[i], count += s.own_cnt[i];
+        // The first CTA's own copy is gone, but it has the list.
+        const unsigned long long* list = rank == 0 ? sh.list : sh.tsum;
+        const uint32_t listed = rank == 0 ? cnt : s.own_listed;
+        for (uint32_t i = tid; i < listed; i += kThreads) {
+          const unsigned long long x = list[i];
+          if (x <= key && (rank != 0 || ((uint32_t)x & ((1u << kIdxBits) - 1)) < (uint32_t)n)) {
+            sum += s.row.weight(x);
+            ++count;
+          }
+        }
+      }
       return;
     }
     short_list = true;
@@ -928,33 +985,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     w[3] = row.kept(x.w, (uint32_t)(base + 4 * v + 3));
   };
   if (!short_list) {
-    unsigned long long sum = 0;
-    uint32_t cnt = 0;
-    if (!row.bounded && row.min_p == 0.f) {  // no filter: exp and add
+    auto pass = [&] {
+      if (!row.bounded && row.min_p == 0.f) {  // no filter: exp and add
 #pragma unroll 2
-      for (int v = p0 + lane; v < p1; v += 32) {
-        const float4 x = sc.get(v);
-        const float z[4] = {x.x, x.y, x.z, x.w};
+        for (int v = p0 + lane; v < p1; v += 32) {
+          const float4 x = sc.get(v);
+          const float z[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = Row::fixed(row.w(z[e]));
-          sum += w;
-          cnt += w != 0u;
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = Row::fixed(row.w(z[e]));
+            sum += w;
+            count += w != 0u;
+          }
+        }
+      } else {
+#pragma unroll 2
+        for (int v = p0 + lane; v < p1; v += 32) {
+          uint32_t w[4];
+          kept4(v, w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += w[e], count += w[e] != 0u;
         }
       }
-    } else {
-#pragma unroll 2
-      for (int v = p0 + lane; v < p1; v += 32) {
-        uint32_t w[4];
-        kept4(v, w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += w[e], cnt += w[e] != 0u;
-      }
-    }
+    };
+    if (!by_bins) pass();
     sum = warp_add(sum);
-    cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
     __syncthreads();  // warp_sum, warp_cnt are also find_bin's
-    if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_cnt[warp] = cnt;
+    if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_cnt[warp] = count;
     __syncthreads();
     if (warp == 0) {
       const unsigned long long a = warp_add(lane < kWarps ? sh.warp_sum[lane] : 0ull);
@@ -969,10 +1027,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     const unsigned long long of_cta = lane < cl ? sh.cl_sum[lane] : 0ull;
     total = warp_add(of_cta);
     kept = __reduce_add_sync(0xFFFFFFFFu, lane < cl ? sh.cl_kept[lane] : 0u);
-    unsigned long long before = warp_add((lane < rank ? of_cta : 0ull) + (lane < warp ? sh.warp_sum[lane] : 0ull));
+    unsigned long long before = warp_add(lane < rank ? of_cta : 0ull);
     if (tid == 0) sh.target = Sampler<T>::draw(u, total);
     __syncthreads();
     const unsigned long long target = sh.target;
+    if (by_bins) {
+      // Only the CTA of the target looks where it is.
+      sum = 0;
+      if (target >= before && target < before + sh.cl_sum[rank]) {
+        pass();
+        sum = warp_add(sum);
+        if (lane == 0) sh.warp_sum[warp] = sum;
+        __syncthreads();
+      }
+    }
+    before += warp_add(lane < warp ? sh.warp_sum[lane] : 0ull);
     if (target >= before && target < before + sum) {  // one warp of the cluster
       unsigned long long run = before;
       for (int v0 = p0; v0 < p1; v0 += 32) {
