@@ -24,7 +24,7 @@
 // some 38 rows of 128,000 scores on the chip at a time.  Reading the scores
 // again from L2 for each pass instead, with more CTAs resident, was slower
 // (512 rows of 128,000 with all filters and probabilities: 391 against 377 us,
-// 280 by now; 64 rows of 163,840: 74 against 64 us, 49 by now; one row of
+// 258 by now; 64 rows of 163,840: 74 against 64 us, 49 by now; one row of
 // 100,003: 10 us).
 #include <cooperative_groups.h>
 
@@ -615,9 +615,10 @@ class Sampler {
   // filters and draw (one CTA, no cluster barrier).  The filters are top-k (k >
   // 0), then top-p as a limit on the sum of better ranks: that of the search by
   // sums, or (`own_limit`) the share tp of what top-k keeps.  f_key and f_w are
-  // the drawn token's index and weight.
+  // the drawn token's index and weight.  `probs` (or null) is the row's, all
+  // zero (the CTAs stored the zeros before a cluster barrier).
   __device__ void finish(uint32_t cnt, int k, float tp, bool own_limit, float u, unsigned long long& total,
-                         uint32_t& kept) {
+                         uint32_t& kept, float* probs) {
     constexpr int E = kList / kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr uint32_t kIdxMask = (1u << kIdxBits) - 1;
@@ -702,6 +703,12 @@ class Sampler {
     }
     __syncthreads();
     total = sh.end_total;
+    if (probs) {
+      const float scale = 1.f / __ull2float_rn(total);
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (in[i]) probs[(uint32_t)key[i] & kIdxMask] = __uint2float_rn(w[i]) * scale;
+    }
     // The first token in index order at which the running sum exceeds the target.
     Target tg;
     tg.limit = sh.target + 1;
@@ -851,6 +858,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     if (tid < mis) zbuf[tid] = L::none();
     if (tid < 4) z[n + tid] = L::none();
   }
+  // Where few tokens will be kept, the zeros of the probabilities go out now,
+  // while there is other work; the kept ones follow when they are known.
+  const bool single = greedy || tp <= 0.f;  // only the best token passes
+  float* probs = p.probs ? p.probs + (int64_t)r * p.vocab + start : nullptr;
+  const bool zero_first = probs && (single || (k > 0 && k <= kList));
+  const bool aligned4 = (((uintptr_t)(probs - mis)) & 15) == 0;
+  if (zero_first) {
+    for (int v = tid; v < (mis + n + 3) / 4; v += kThreads) {
+      const int i = 4 * v - mis;
+      if (aligned4 && i >= 0 && i + 4 <= n) {
+        __stcs(reinterpret_cast<float4*>(probs + i), make_float4(0.f, 0.f, 0.f, 0.f));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e >= 0 && i + e < n) __stcs(&probs[i + e], 0.f);
+      }
+    }
+  }
   // Largest score of the row.
   const uint32_t warp_most = __reduce_max_sync(0xFFFFFFFFu, order_bits(best));
   if (lane == 0) sh.warp_cnt[warp] = warp_most;
@@ -862,14 +887,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   cluster.sync();
   float m = order_float(__reduce_max_sync(0xFFFFFFFFu, lane < cl ? sh.cl_cnt[lane] : 0u));
   const bool empty = !valid || m == -CUDART_INF_F;
-  float* probs = p.probs ? p.probs + (int64_t)r * p.vocab + start : nullptr;
   if (empty) {  // uniform over the cluster; no remote access follows
     if (rank == 0 && tid == 0) {
       p.token[r] = -1;
       if (p.logprob) p.logprob[r] = -CUDART_INF_F;
       if (p.kept) p.kept[r] = 0;
     }
-    if (probs)
+    if (probs && !zero_first)
       for (int i = tid; i < n; i += kThreads) probs[i] = 0.f;
     return;
   }
@@ -887,15 +911,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   s.row.least = m - kCut;
   s.row.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;  // the best token passes
   s.row.bounded = false;
-  if (greedy || tp <= 0.f) {
-    // Only the best token, the lowest index among equals: the least key.
-    s.row.least = m;
+  if (single) {
+    // The lowest index among equals: the least key.
     unsigned long long low, high;
     s.key_range([&](auto f) { s.each(m, m, [&](float zi, uint32_t idx) { f(rank_key(zi, idx)); }); }, low, high);
-    if (tid < cl) cluster.map_shared_rank(&sh, tid)->cl_low[rank] = low;
-    cluster.sync();
-    for (int i = 0; i < cl; ++i) low = sh.cl_low[i] < low ? sh.cl_low[i] : low;
-    s.row.set_max(low);
+    if (tid == 0) cluster.map_shared_rank(&sh, 0)->cl_low[rank] = low;
+    cluster.sync();  // no remote access follows
+    if (rank == 0 && warp == 0) {
+      low = ~warp_max(lane < cl ? ~sh.cl_low[lane] : 0ull);
+      if (lane == 0) {
+        const int idx = (int)((uint32_t)low & ((1u << kIdxBits) - 1));
+        p.token[r] = idx;
+        if (p.logprob) p.logprob[r] = 0.f;
+        if (p.kept) p.kept[r] = 1;
+        if (p.probs) p.probs[(int64_t)r * p.vocab + idx] = 1.f;
+      }
+    }
+    return;
   }
   Match all;
   all.level = all.b0 = 0;
@@ -905,8 +937,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   uint32_t count = 0;
   unsigned long long total = 0;
   uint32_t kept = 0;
-  const bool one = s.row.bounded;
-  const bool use_k = k > 0 && k < p.vocab && !one, use_p = tp < 1.f && !one;
+  const bool use_k = k > 0 && k < p.vocab, use_p = tp < 1.f;
   // Top-k, then top-p of what it left.  A short list of candidates ends the row.
   auto search = [&](auto by_sum, Target tg, float share) {
     constexpr bool SUMS = decltype(by_sum)::value;
@@ -944,18 +975,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     to.b0 = (int)sh.f_bin;
     s.gather(to);
     if (rank == 0) {
-      s.finish(upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept);
+      s.finish(upto, SUMS ? 0 : k, tp, !SUMS, u, total, kept, zero_first ? p.probs + (int64_t)r * p.vocab : nullptr);
       if (tid == 0) {
         p.token[r] = (int)sh.f_key;
         if (p.logprob) p.logprob[r] = logf(__uint2float_rn(sh.f_w) / __ull2float_rn(total));
       }
-      if (p.probs && tid > 0 && tid < cl) {
+      if (probs && !zero_first && tid > 0 && tid < cl) {
         SampleShared* o = cluster.map_shared_rank(&sh, tid);
         o->end_total = sh.end_total;
         o->end_key = sh.end_key;
       }
     }
-    if (p.probs) {  // the others need the bound; no remote access follows
+    if (probs && !zero_first) {  // the others need the bound; no remote access follows
       cluster.sync();
       total = sh.end_total;
       s.row.set_max(sh.end_key);
@@ -1074,9 +1105,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
     }
   }
   if (rank == 0 && tid == 0 && p.kept) p.kept[r] = (int)kept;
-  if (probs) {
+  if (probs && !(short_list && zero_first)) {
     const float scale = 1.f / __ull2float_rn(total);
-    const bool aligned4 = (((uintptr_t)(probs - mis)) & 15) == 0;
     for (int v = tid; v < s.n4; v += kThreads) {
       uint32_t w[4];
       kept4(v, w);
