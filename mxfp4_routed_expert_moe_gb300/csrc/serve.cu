@@ -37,6 +37,13 @@ int check_batch(const moe_kv_batch* b) {
 }
 
 // ------------------------------------------------------ attention: the plan --
+// Most new tokens a sequence can have: max_q is the caller's bound and may be
+// any number above that.
+int most_new(const moe_kv_batch& b) {
+  const int most = b.q_start ? b.tokens : 1;
+  return b.max_q < most ? b.max_q : most;
+}
+
 // Row tiles per key head that the kernel may have: the sum over sets of
 // ceil(rows / tile), bounded by what the host knows.
 int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
@@ -48,10 +55,13 @@ int64_t max_tiles(const moe_kv_batch& b, int group, const AttnSide& s) {
 }
 
 // Which side of the split kernel takes which part: the warps take parts of at
-// most 16 rows per key head (one tile), the Tensor Memory side the others.
+// most 16 rows per key head (one tile), the Tensor Memory side the others.  A
+// sequence has no more rows than the batch, so own parts on the Tensor Memory
+// side have their prefix there too: attn_plan scans one side and takes the other
+// for a prefix alone.
 void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)[2]) {
   memset(side, 0, sizeof side);
-  const bool own_tc = (int64_t)b.max_q * group > kAttnWarpRows, prefix = b.prefix_len > 0;
+  const bool own_tc = (int64_t)most_new(b) * group > kAttnWarpRows, prefix = b.prefix_len > 0;
   const bool prefix_tc = (int64_t)b.tokens * group > kAttnWarpRows;
   AttnSide &w = side[0], &t = side[1];
   w.own = !own_tc;
@@ -83,7 +93,7 @@ void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)
 // / 36.0; 32 of 100 behind 1,000 (two waves, 6 units each) 28.3 / 33.0; 64 of
 // 200 (four waves) 26.6 / 14.9.
 int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
-  const int64_t row_tiles = ((int64_t)b.max_q * group + kAttnWarpRows - 1) / kAttnWarpRows;
+  const int64_t row_tiles = ((int64_t)most_new(b) * group + kAttnWarpRows - 1) / kAttnWarpRows;
   const int64_t tiles = b.batch * c.kv_heads * row_tiles;
   const int unit = attn_warp_unit(c.head_dim);
   const int64_t units = ((int64_t)b.prefix_len + unit - 1) / unit + ((int64_t)b.table_pages * c.page_size + unit - 1) / unit;
@@ -92,7 +102,7 @@ int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
   const int64_t each = (units + cl * kAttnWarpWorkers - 1) / (cl * kAttnWarpWorkers);
   if (tiles * cl <= kNumSMs) return each <= 16 ? cl : 0;
   const bool two_kernels = b.prefix_len > 0 && (int64_t)b.tokens * group > kAttnWarpRows &&
-                           (int64_t)b.max_q * group <= kAttnWarpRows;
+                           (int64_t)most_new(b) * group <= kAttnWarpRows;
   return tiles <= 2 * kNumSMs && two_kernels && each <= 6 ? cl : 0;
 }
 
@@ -229,7 +239,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
     const int box = attn_box(cache->page_size, attn_warp_unit(cache->head_dim));
     if ((st = cache_map(&km, cache, cache->k, box)) != MOE_OK || (st = cache_map(&vm, cache, cache->v, box)) != MOE_OK)
       return st;
-    p.tile_rows = (int)(((int64_t)batch->max_q * p.group + kAttnWarpRows - 1) / kAttnWarpRows);
+    p.tile_rows = (int)(((int64_t)most_new(*batch) * p.group + kAttnWarpRows - 1) / kAttnWarpRows);
     return cuda_status(launch_attn_tile(p, cl, km, vm, s));
   }
   CUtensorMap maps[4];  // K and V in the boxes of either side

@@ -316,10 +316,13 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, AttnPlan& sh) {
       const long long x = workers > 0 ? (sh.total[i] + workers - 1) / workers : 0;
       sh.per[i] = x < 1 ? 1 : x;
     }
+    // A prefix alone on its side: every worker's range begins in it.
     if (two) {
-      sh.set[0] = p.b.batch;
-      sh.unit0[0] = 0;
-      sh.tile0[0] = 0;
+      for (int w = 0; w < kAttnWarpWorkers; ++w) {
+        sh.set[w] = p.b.batch;
+        sh.unit0[w] = 0;
+        sh.tile0[w] = 0;
+      }
     }
     if (blockIdx.x == 0) {
 #pragma unroll

@@ -251,3 +251,30 @@ def test_broken_starts_are_reported(moe):
         c.batch.q_start.copy_(keep)
         again, lse2 = c.run()
         assert t.equal(good, again) and t.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("capacity", [0, LONG])
+@pytest.mark.parametrize("hq,hk", [(3, 3), (14, 2), (56, 8)])
+@pytest.mark.parametrize("q_lens,lens,prefix", [([2], [9], 32768), ([1, 1], [3, 40], 200), ([1], [0], 77), ([2, 0, 1], [5, 9, 1], 513)])
+def test_max_q_far_above_the_new_tokens(moe, q_lens, lens, prefix, hq, hk, capacity):
+    """max_q is an upper bound that a server may keep for all its steps: past the batch's new tokens, which are what
+    the call knows without reading q_start, it changes no bit."""
+    kw = dict(seed=31, q_lens=q_lens, lens=lens, prefix=prefix, page=64, hq=hq, hk=hk, dim=128, capacity=capacity)
+    tight = Case(moe, max_q=sum(q_lens), **kw)
+    out, lse = tight.run()
+    if prefix < 1000:
+        tight.check()
+    for max_q in (8, 64, 5000):
+        c = Case(moe, max_q=max_q, **kw)
+        assert c.ws.numel() == tight.ws.numel()
+        got, got_lse = c.run()
+        assert torch().equal(got, out) and torch().equal(got_lse, lse)
+
+
+def test_max_q_above_one_without_starts(moe):
+    """Without q_start every sequence has one new token, whatever max_q says."""
+    kw = dict(seed=32, q_lens=[1] * 2, lens=[70, 9], prefix=300, page=32, hq=14, hk=2, dim=64, single=True, capacity=LONG)
+    c = Case(moe, max_q=8, **kw)
+    c.check()
+    got, want = c.run(), Case(moe, **kw).run()
+    assert torch().equal(got[0], want[0]) and torch().equal(got[1], want[1])

@@ -193,3 +193,16 @@ def test_lengths_past_what_attention_counts_are_refused(serve, moe):
     c, b = cache(serve), batch(serve, prefix_len=moe.SERVE_MAX_LEN + 1, prefix_table=A)
     assert append(serve, c, b) == 2 and attend(serve, c, b) == 2
     assert serve._lib().moe_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 4) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=1, tokens=2, q_start=A, prefix_len=32768, prefix_table=A), dict(batch=2, tokens=2, q_start=A, prefix_len=200, prefix_table=A),
+    dict(batch=1, tokens=1, prefix_len=100, prefix_table=A), dict(batch=1, tokens=1), dict(batch=3, tokens=3)])
+@pytest.mark.parametrize("group", [1, 7])
+def test_max_q_past_what_the_batch_can_have_changes_no_plan(serve, kw, group):
+    """max_q is an upper bound: no sequence has more new tokens than the batch, nor more than one without q_start.
+    Own parts planned by a larger bound went to the other side of the split kernel than the prefix."""
+    L = serve._lib()
+    most = kw["tokens"] if "q_start" in kw else 1
+    size = lambda m: L.moe_attention_workspace_bytes(ctypes.byref(cache(serve)), ctypes.byref(batch(serve, max_q=m, **kw)), 2 * group)  # noqa: E731
+    assert 0 < size(most) == size(8) == size(100) == size((1 << 31) - 1)
