@@ -121,7 +121,7 @@ struct Row {
   __device__ __forceinline__ uint32_t weight(unsigned long long key) const {
     return fixed(w(order_float(~(uint32_t)(key >> kIdxBits))));
   }
-  // Bin of a score that is not below m - kCut: adding 2^23 leaves the rounded
+  // Bin of a score with m - z <= kCut: adding 2^23 leaves the rounded
   // product in the low bits (monotone in z; cheaper than a conversion).
   __device__ __forceinline__ int bin(float z) const {
     return (int)(__float_as_uint(fmaf(m - z, kBinScale, 8388608.f)) & (kBins - 1));
@@ -908,7 +908,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   }
   Sampler<T> s(sh, sc, mis + n, (uint32_t)(start - mis));
   s.row.m = m;
-  s.row.least = m - kCut;
+  // Rounded up: a large m has no float at m - kCut, and one below it would be
+  // past the last bin (every W between is 0 all the same).
+  s.row.least = __fsub_ru(m, kCut);
   s.row.min_p = mp > 0.f ? fminf(mp, 1.f) : 0.f;  // the best token passes
   s.row.bounded = false;
   if (single) {

@@ -200,3 +200,37 @@ def test_candidate_lists_of_all_lengths(moe, dtype):
         check(moe, x, [u] * len(ks), temp, top_k=ks, min_p=[0.2] * len(ks))
     peaked = [0.25] * len(ks)
     check(moe, x, rng.random(len(ks)).astype(np.float32).tolist(), peaked, top_p=np.linspace(0.05, 0.999, len(ks)).astype(np.float32).tolist())
+
+
+@pytest.mark.parametrize("top", [4194304.5, 5000000.5, 8000001.0, -5210070.5, 4e7, -4e7, 1e8, 1.2e8, 3e8, 2.0 ** 31])
+def test_large_scaled_scores(moe, top):
+    """Floats of this size have none at the cut below which weights are 0: scores on both sides of it, and between it
+    and the maximum, rank in their order."""
+    rng = np.random.default_rng(12)
+    below = np.concatenate([[0, 0, 4, 4, 8, 16, 20, 21.5, 22, 22.25, 22.5, 23, 24, 24, 26, 28, 32, 64], rng.uniform(0, 40, 3000)])
+    x = np.tile((np.float64(top) - below).astype(np.float32), (6, 1))
+    for row in x[1:]:
+        rng.shuffle(row)
+    logits = torch().from_numpy(x).cuda()
+    u = [0.0, 0.2, 0.5, 0.9, 0.999, 0.99999994]
+    check(moe, logits, u)
+    check(moe, logits, u, None, top_k=[1, 2, 3, 40, 1500, 3017])
+    check(moe, logits, u, None, top_p=[0.1, 0.5, 0.9, 0.99, 0.9999, 0.99999994])
+    check(moe, logits, u, None, min_p=[0.5, 1e-3, 1e-6, 1e-9, 1e-10, 0.0])
+    check(moe, logits, u, None, top_k=[2, 3, 100, 2000, 5000, 3000], top_p=[0.99, 0.9, 0.999, 0.9999, 0.999, 0.5], min_p=[0.0, 1e-4, 0.0, 1e-9, 0.0, 1e-2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_small_temperatures(moe, dtype):
+    """Ordinary logits over temperatures that take them to such sizes."""
+    t = torch()
+    rng = np.random.default_rng(13)
+    x = t.from_numpy((5 + rng.random((5, 30011)) * 2.5e-5).astype(np.float32)).cuda()
+    x[:, 7::1001] = 5.0000224
+    if dtype == "bf16":
+        x = x.bfloat16()
+        x[:, ::1000] = 5.03125
+    temp, u = [1e-6, 3e-7, 1.3e-7, 5e-8, 2e-6], [0.1, 0.4, 0.6, 0.9, 0.3]
+    check(moe, x, u, temp)
+    check(moe, x, u, temp, top_k=[2, 50, 700, 5000, 30011], top_p=[0.9, 0.99, 0.5, 0.9999, 0.3])
+    check(moe, x, u, temp, top_p=[0.9, 0.99, 0.5, 0.9999, 0.3], min_p=[0.0, 0.1, 0.0, 1e-9, 0.2])
