@@ -757,6 +757,12 @@ class Sampler {
   }
 };
 
+// A CTA's shared memory may be accessed by the others of its cluster once it has
+// started: all arrive on entry and wait before the first remote access, which
+// the loads between have long covered.  No data is passed on by this one.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // How scores of a type are read and kept.
 template <typename T>
 struct Loader;
@@ -798,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   using L = Loader<T>;
   extern __shared__ __align__(32) uint8_t smp_dyn[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smp_dyn);
+  cluster_arrive();
   pdl_trigger();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -880,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleParams p) {
   const uint32_t warp_most = __reduce_max_sync(0xFFFFFFFFu, order_bits(best));
   if (lane == 0) sh.warp_cnt[warp] = warp_most;
   __syncthreads();
+  cluster_wait();  // the first remote access follows
   if (warp == 0) {
     const uint32_t b = __reduce_max_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_cnt[lane] : 0u);
     if (lane < cl) cluster.map_shared_rank(&sh, lane)->cl_cnt[rank] = b;

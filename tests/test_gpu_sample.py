@@ -234,3 +234,24 @@ def test_small_temperatures(moe, dtype):
     check(moe, x, u, temp)
     check(moe, x, u, temp, top_k=[2, 50, 700, 5000, 30011], top_p=[0.9, 0.99, 0.5, 0.9999, 0.3])
     check(moe, x, u, temp, top_p=[0.9, 0.99, 0.5, 0.9999, 0.3], min_p=[0.0, 0.1, 0.0, 1e-9, 0.2])
+
+
+@pytest.mark.parametrize("rows", [1, 7, 400])
+@pytest.mark.parametrize("vocab", [4097, 8193, 16385, 32776])
+def test_uneven_pieces_of_a_cluster(moe, rows, vocab):
+    """The last CTA of a cluster has a piece of few or no scores and gives its maximum while the others still load;
+    the row's largest score lies in the first piece, or in the last one."""
+    t = torch()
+    rng = np.random.default_rng(vocab)
+    x = t.from_numpy(rng.standard_normal((rows, vocab)).astype(np.float32)).cuda()
+    x[:, 3] = 9
+    x[::2, -1] = 11
+    want = [vocab - 1 if r % 2 == 0 else 3 for r in range(rows)]
+    token = t.empty(rows, dtype=t.int32, device="cuda")
+    u = t.full((rows,), 0.5, device="cuda")
+    zero, k = t.zeros(rows, device="cuda"), t.ones(rows, dtype=t.int32, device="cuda")
+    for _ in range(20):
+        for kw in (dict(temperature=zero), dict(top_k=k), dict(top_p=zero + 0.01)):
+            token.fill_(-5)
+            moe.sample(x, u, token, **kw)
+            assert token.tolist() == want, kw.keys()
