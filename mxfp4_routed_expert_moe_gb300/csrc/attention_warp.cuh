@@ -102,6 +102,8 @@ struct WarpRows {
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
           *reinterpret_cast<uint4*>(stage + C::kMat + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+      // Before the tensor-map copy that refills the stage (the async proxy).
+      fence_async_smem();
       __syncwarp();
     }
     float sc[kUnit / 8][4];

@@ -278,3 +278,19 @@ def test_max_q_above_one_without_starts(moe):
     c.check()
     got, want = c.run(), Case(moe, **kw).run()
     assert torch().equal(got[0], want[0]) and torch().equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("capacity", [0, LONG])
+def test_short_parts_in_turn_through_the_same_buffers(moe, dim, capacity):
+    """Parts that end inside a unit, where the rows past the end are cleared, followed at once by others that refill
+    the same buffers: the prefix's last unit before the own part's, and many short sequences in turn."""
+    t = torch()
+    for q_lens, lens, prefix in (([1] * 2, [200, 37], 233), ([1] * 700, [1 + (7 * i) % 50 for i in range(700)], 0),
+                                 ([2] * 300, [2 + (11 * i) % 90 for i in range(300)], 17)):
+        c = Case(moe, 41, q_lens, lens, prefix, 16, 6, 3, dim, capacity=capacity)
+        c.check()
+        out, lse = c.run()
+        for _ in range(20):
+            again, lse2 = c.run()
+            assert t.equal(out, again) and t.equal(lse, lse2)
