@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
 #pragma unroll
   for (int h = 0; h < 2; ++h) vis[h] = (lane >> 2) + 8 * h < rows ? visible((lane >> 2) + 8 * h) : 0;
   int n = 0;
-  bool alive = true;
+  bool alive = true, odd = false;
   for (int u = u0; u < units; u += step, ++n) {
     const int st = n % C::kStages;
     alive = __all_sync(0xFFFFFFFFu, mbar_wait_for(&full[st], (n / C::kStages) & 1, p.wait_limit));
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
     int kv, end;
     const bool pre = unit_at(u, kv, end) == p.b.batch;
     const int see[2] = {(pre ? end : vis[0]) - kv, (pre ? end : vis[1]) - kv};
-    acc.unit(ring + st * C::kStage, p.scale_log2, kv + kUnit > (pre ? end : own_all), see, end - kv);
+    odd |= acc.unit(ring + st * C::kStage, p.scale_log2, (pre ? end : own_all) - kv, see, end - kv);
     __syncwarp();  // every lane has read the stage
     if (u + C::kStages * step < units) {
       load(u + C::kStages * step, st, next);
@@ -137,6 +137,16 @@ __global__ void __launch_bounds__(kWorkers * 32, 1)
     if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
   acc.close();
   acc.store(reinterpret_cast<float*>(ring), sh.ml[warp], rows);
+  if (odd) {
+    AttnSeg own;
+    own.set = b;
+    own.len = own.kv1 = raw.len;
+    own.first_vis = raw.len - ql + 1;
+    own.kvh = kvh;
+    own.row0 = row0;
+    own.kv0 = 0;
+    add_odd_values<D>(p, own, 0, rows, reinterpret_cast<float*>(ring));
+  }
   cluster.sync();
   // CTA `rank` joins rows rank, rank + cl, ...: D / 4 threads a row, the warps
   // in order.

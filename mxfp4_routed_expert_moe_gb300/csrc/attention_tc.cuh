@@ -14,6 +14,10 @@
 //   * a warp walks the CTA's range and hands its segments on through shared
 //     memory, so that the others hold no walk state (with it the softmax
 //     spilled, and its spills went past the 28 KB that L1 has left);
+//   * a warp prepares the values of units that not every row sees whole: what
+//     lies past the end is cleared, and so are infinities and NaN of tokens that
+//     only some rows see (0 * NaN is NaN), which the softmax warps add to the
+//     sums of those rows;
 //   * warpgroup t turns S_t into P_t = 2^(S_t scale - m) in bf16, written over
 //     S_t, one row per thread, so that row sums and maxima need no exchange.
 // While one half's softmax runs, the other half's MMAs do.  The reference m of
@@ -33,7 +37,7 @@
 namespace moe {
 
 constexpr int kHalfRows = 128;           // rows of an MMA tile
-constexpr int kAttnThreads = 12 * 32;    // 2 x 4 softmax warps, producer, MMA, walk, one idle
+constexpr int kAttnThreads = 12 * 32;    // 2 x 4 softmax warps, producer, MMA, walk, edge values
 constexpr int kBufs = 5;
 constexpr int kSegs = 4;                 // segments handed from the walking warp to the others
 constexpr uint32_t kTmemCols = 512;
@@ -53,6 +57,8 @@ struct TcCfg {
 struct TcShared {
   uint64_t full[kBufs], empty[kBufs];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t raw[kBufs];        // an edge unit's values have landed; `full` when they are prepared
+  uint64_t odd_known[kSegs];
   AttnSeg seg[kSegs];
   uint64_t q_ready[2], s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem_base;
@@ -157,6 +163,7 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.raw[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.q_ready[t], 4);
@@ -168,7 +175,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 10);
+      mbar_init(&sh.seg_empty[i], 11);
+      mbar_init(&sh.odd_known[i], 1);
     }
     sh.abort_flag = 0;
     mbar_init_fence();
@@ -197,11 +205,13 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
     // ------------------------------------------------------------ producer --
     const int box = attn_box(p.page_size, kUnit);
     int bi = 0, use = 0;
+    uint32_t raw = 0, nraw = 0;  // by buffer: whether it was last used for edge values; how often, modulo 2
     bool ok = true;
     while (ok) {
       const AttnSeg* sg = take_seg();
       if (!sg) break;
       const AttnSeg g = *sg;
+      const int common = attn_visible(p, g, g.row0 / p.group);  // tokens that every row sees
       drop_seg();
       const int32_t* table = attn_table(p, g.set);
       int kv = attn_first(p, g) - kUnit;
@@ -227,13 +237,17 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[bi], (uint32_t)(nb * box * D * 2));
+          const bool edge = m && common - kv < kUnit;
+          raw = edge ? raw | 1u << bi : raw & ~(1u << bi);
+          if (edge) nraw ^= 1u << bi;
+          uint64_t* bar = edge ? &sh.raw[bi] : &sh.full[bi];
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(nb * box * D * 2));
           __syncwarp();
           if (lane < nb) {
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
               tma_load_4d(ring + bi * C::kMat + h * C::kSub + lane * box * 128, m ? &vmap : &kmap, h * 64, y, g.kvh,
-                          page, &sh.full[bi]);
+                          page, bar);
           }
           __syncwarp();
           if (++bi == kBufs) bi = 0, ++use;
@@ -244,7 +258,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
     if (lane == 0)
       for (int i = 0; i < kBufs; ++i) {
         const int n = use + (i < bi ? 1 : 0);
-        if (n > 0 && !mbar_wait(&sh.full[i], (n - 1) & 1)) set_status_word(p.status, MOE_ERR_TIMEOUT);
+        if (n > 0 && !(raw >> i & 1 ? mbar_wait(&sh.raw[i], (nraw >> i & 1) ^ 1) : mbar_wait(&sh.full[i], (n - 1) & 1)))
+          set_status_word(p.status, MOE_ERR_TIMEOUT);
       }
     } else if (warp == 9) {
     // ----------------------------------------------------------------- MMA --
@@ -290,7 +305,6 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       const AttnSeg* sg = take_seg();
       if (!sg) break;
       const int kv0 = sg->kv0, kv1 = sg->kv1;
-      int left = kv1 - attn_first(p, *sg);  // tokens from the current unit on
       const bool two = sg->rows > kHalfRows;
       drop_seg();
       const int nt = (kv1 - kv0 + kUnit - 1) / kUnit;
@@ -312,16 +326,6 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       if (nt > 1) take(kbuf);
       for (int j = 0; j < nt && ok; ++j) {
         const bool more = j + 1 < nt;
-        if (left < kUnit) {
-          // Rows of V past the length may hold anything, and 0 * NaN is NaN.
-          uint8_t* vb = ring + vbuf * C::kMat;
-          const int n16 = (kUnit - left) * 8;
-          for (int h = 0; h < D / 64; ++h)
-            for (int i = lane; i < n16; i += 32)
-              *reinterpret_cast<uint4*>(vb + h * C::kSub + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
-        }
         int vnext = 0, knext = 0;
         values(0, vbuf, j == 0);
         if (!ok) break;
@@ -342,7 +346,6 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         }
         vbuf = vnext;
         kbuf = knext;
-        left = left > kUnit ? left - kUnit : kv1 - kv0;
       }
     }
     // No MMA may be in flight when Tensor Memory is released.
@@ -366,6 +369,41 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
         }
         __syncwarp();
         if (!more) break;
+      }
+    } else {
+      // ------------------------------------------------------- edge values --
+      uint32_t unit = 0, nraw = 0;  // units of all segments so far; by buffer: its edge values so far, modulo 2
+      bool ok = true;
+      for (;;) {
+        if (!take_seg()) break;
+        AttnSeg* sg = &sh.seg[nseg % kSegs];
+        const int kv0 = sg->kv0, kv1 = sg->kv1, common = attn_visible(p, *sg, sg->row0 / p.group);
+        bool odd = false;
+        int kv = attn_first(p, *sg);
+        for (int n = (kv1 - kv0 + kUnit - 1) / kUnit; n > 0; --n, ++unit, kv = kv + kUnit < kv1 ? kv + kUnit : kv0) {
+          if (common - kv >= kUnit) continue;
+          const uint32_t b = (2 * unit + 1) % kBufs;  // a unit's values follow its keys
+          ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.raw[b], nraw >> b & 1, p));
+          if (!ok) break;
+          nraw ^= 1u << b;
+          uint8_t* v = ring + b * C::kMat;
+          const int t0 = common > kv ? common - kv : 0, t1 = kv1 - kv < kUnit ? kv1 - kv : kUnit;
+          odd |= clear_odd_values<D / 64>(v, C::kSub, t0, t1);
+#pragma unroll 1
+          for (int h = 0; h < D / 64; ++h) {
+            for (int i = t1 * 8 + lane; i < kUnit * 8; i += 32)
+              *reinterpret_cast<uint4*>(v + h * C::kSub + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[b]);
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          sg->odd = odd;
+          mbar_arrive(&sh.odd_known[nseg % kSegs]);
+        }
+        drop_seg();
       }
     }
   } else {
@@ -510,7 +548,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
       float* slot = sd.slots + (int64_t)sg->slot * kAttnTcRows * (D + 2);
       const int rows = sg->rows;
       if (kv0 < kv1) {
-        ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.o_done[t], no++ & 1, p));
+        ok = __all_sync(0xFFFFFFFFu, tc_wait(sh, &sh.o_done[t], no++ & 1, p) && (sg->set == p.b.batch ||  // all rows see all of a prefix
+                                         tc_wait(sh, &sh.odd_known[nseg % kSegs], (nseg / kSegs) & 1, p)));
         if (!ok) break;
         tc_fence_after();
         // Through this warp's part of the query tile, so that whole lines
@@ -535,6 +574,8 @@ __device__ __forceinline__ void attn_tc_role(const AttnParams& p, const CUtensor
           __syncwarp();
         }
         tc_fence_before();
+        const int w0 = t * kHalfRows + q * 32;
+        if (__builtin_expect(sg->odd, 0)) add_odd_values<D>(p, *sg, w0, rows < w0 + 32 ? rows : w0 + 32, slot);
       }
       if (r < rows) {
         slot[kAttnTcRows * D + r] = m;

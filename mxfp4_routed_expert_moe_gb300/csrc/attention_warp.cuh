@@ -88,20 +88,24 @@ struct WarpRows {
     l[0] = l[1] = 0.f;
   }
 
-  // One unit: its tokens of K and V in a stage of the warp's ring.  With
-  // `edge`, row h sees its first see[h] tokens and the V rows from n on are not
-  // to be used.
-  __device__ __forceinline__ void unit(uint8_t* stage, float scale_log2, bool edge, const int (&see)[2], int n) {
+  // One unit: its tokens of K and V in a stage of the warp's ring.  Every row
+  // of the tile sees the first `all` tokens (all, if that is kUnit or more), row
+  // h the first see[h], and the V rows from n on are not to be used.  True if
+  // values were taken out (clear_odd_values).
+  __device__ __forceinline__ bool unit(uint8_t* stage, float scale_log2, int all, const int (&see)[2], int n) {
     using C = WarpCfg<D>;
     constexpr int kHalf = C::kHalf;
     const int lane = threadIdx.x & 31;
     const uint32_t kb = smem_u32(stage), vb = kb + C::kMat;
+    const bool edge = all < kUnit;
+    bool odd = false;
     if (edge) {
       // Rows of V past the length may hold anything, and 0 * NaN is NaN.
       for (int i = n * 8 + lane; i < kUnit * 8; i += 32)
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
           *reinterpret_cast<uint4*>(stage + C::kMat + h * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+      odd = all < n && clear_odd_values<D / 64>(stage + C::kMat, kHalf, all < 0 ? 0 : all, n < kUnit ? n : kUnit);
       // Before the tensor-map copy that refills the stage (the async proxy).
       fence_async_smem();
       __syncwarp();
@@ -173,6 +177,7 @@ struct WarpRows {
         mma_bf16(o[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
       }
     }
+    return odd;
   }
 
   // The four lanes of a row add up its sum.
@@ -309,7 +314,7 @@ __device__ __forceinline__ void attn_warp_role(const AttnParams& p, const CUtens
         break;
       }
       const int see[2] = {vis[0] - kv, vis[1] - kv};
-      rows.unit(ring + st * C::kStage, scale, kv + kUnit > vis_min, see, g.kv1 - kv);
+      if (rows.unit(ring + st * C::kStage, scale, vis_min - kv, see, g.kv1 - kv)) segs[seg_out % kWarpSegs].odd = 1;
       ++un;
       kv += kUnit;
       __syncwarp();  // every lane has read the stage
@@ -318,6 +323,8 @@ __device__ __forceinline__ void attn_warp_role(const AttnParams& p, const CUtens
       rows.close();
       float* slot = sd.slots + (int64_t)g.slot * kAttnWarpRows * (D + 2);
       rows.store(slot, slot + kAttnWarpRows * D, g.rows);
+      const AttnSeg& whole = segs[seg_out % kWarpSegs];
+      if (__builtin_expect(whole.odd, 0)) add_odd_values<D>(p, whole, 0, whole.rows, slot);
       ++seg_out;
       in_seg = false;
     }

@@ -230,6 +230,10 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   for (p.page_shift = 0; (1 << p.page_shift) < cache->page_size; ++p.page_shift) {
   }
   p.num_pages = cache->num_pages;
+  p.v = (const uint16_t*)cache->v;
+  p.page_stride = cache->page_stride;
+  p.token_stride = cache->token_stride;
+  p.head_stride = cache->head_stride;
   p.b = *batch;
   p.status = status;
   p.wait_limit = wait_limit();

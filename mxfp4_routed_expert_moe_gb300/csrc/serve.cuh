@@ -101,6 +101,8 @@ struct AttnParams {
   int q_heads, group;  // query heads, query heads per key head
   float scale_log2;    // scale * log2(e)
   int kv_heads, head_dim, page_size, page_shift, num_pages;
+  const uint16_t* v;  // the cache's values, for what the tensor maps do not serve
+  int64_t page_stride, token_stride, head_stride;
   moe_kv_batch b;
   AttnSide side[2];    // 0: warps, 1: Tensor Memory
   int tile_rows;       // tile kernel: row tiles of a sequence and key head
@@ -394,6 +396,7 @@ struct AttnSeg {
   int row0;      // first row of the tile in its set
   int rows;      // rows of the tile
   int kv0, kv1;  // token range [kv0, kv1) of the set, cut to what the tile's last row sees (may be empty)
+  int odd;       // values were taken out of it (clear_odd_values)
 };
 
 // Where in [kv0, kv1) a segment begins; the rest follows in order, then what is
@@ -458,6 +461,7 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& s
   const long long e = r1 << sd.unit_shift;
   g.kv1 = e < vis ? (int)e : vis;
   if (g.kv1 < g.kv0) g.kv1 = g.kv0;
+  g.odd = 0;
   if (g.set == p.b.batch) g.first_vis = g.kv0;
   if (TURN && g.set == p.b.batch && 4ll * p.head_dim * p.kv_heads * g.len > kAttnTurnBytes &&
       sh.per[1] <= 0x7FFFFFFF) {
@@ -467,6 +471,65 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& s
     if (turn < ((g.kv1 - g.kv0 + sd.unit - 1) >> sd.unit_shift)) g.first_vis += turn << sd.unit_shift;
   }
   return true;
+}
+
+// Values of tokens that some rows of a tile see and others do not: in the product
+// with the others' weights of 0 an infinity or NaN would become NaN.  So these
+// are taken out of the copy in shared memory (clear_odd_values) and added to the
+// sums of the rows that see them (add_odd_values), which a positive weight leaves
+// what they are.  Looking for them costs 9 prompts of up to 301 tokens behind
+// 4,001 123 us instead of 118, and batches with one new token each, whose tiles
+// have no such tokens, 1 to 3 % of code in the way.
+__device__ __forceinline__ bool odd_bf16(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
+
+// By one warp: tokens [t0, t1) of V in shared memory, 128 bytes a token in each
+// half of 64 values.  True, in all lanes, if there were any.
+template <int HALVES>
+__device__ __forceinline__ bool clear_odd_values(uint8_t* v, int half_bytes, int t0, int t1) {
+  const int lane = threadIdx.x & 31;
+  uint32_t most = 0;  // largest magnitudes, as integers
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h)
+#pragma unroll 4
+    for (int i = t0 * 8 + lane; i < t1 * 8; i += 32) {
+      const uint4 x = *reinterpret_cast<const uint4*>(v + h * half_bytes + i * 16);
+      most = __vmaxu2(__vmaxu2(most, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+      most = __vmaxu2(__vmaxu2(most, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+    }
+  if (__builtin_expect(!__any_sync(0xFFFFFFFFu, odd_bf16(most) || odd_bf16(most >> 16)), 1)) return false;
+#pragma unroll 1
+  for (int h = 0; h < HALVES; ++h)
+#pragma unroll 1
+    for (int i = t0 * 64 + lane; i < t1 * 64; i += 32) {
+      uint16_t* x = reinterpret_cast<uint16_t*>(v + h * half_bytes) + i;
+      if (odd_bf16(*x)) *x = 0;
+    }
+  return true;
+}
+
+// By one warp, whose other values are in `dst` already: rows [r0, r1) of the
+// segment's tile, D floats each.  The values are read from the cache again.
+template <int D>
+__device__ __forceinline__ void add_odd_values(const AttnParams& p, const AttnSeg& g, int r0, int r1, float* dst) {
+  const int32_t* table = attn_table(p, g.set);
+  const int all = attn_visible(p, g, g.row0 / p.group), first = all > g.kv0 ? all : g.kv0;
+  __syncwarp();
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    const int vis = attn_visible(p, g, (g.row0 + r) / p.group), end = vis < g.kv1 ? vis : g.kv1;
+#pragma unroll 1
+    for (int d = threadIdx.x & 31; d < D; d += 32) {
+#pragma unroll 1
+      for (int tok = first; tok < end; ++tok) {
+        const int page = __ldg(&table[tok >> p.page_shift]);
+        if (page < 0 || page >= p.num_pages) continue;  // reported where it was loaded
+        const uint32_t x = __ldg(p.v + page * p.page_stride + (tok & (p.page_size - 1)) * p.token_stride +
+                                 g.kvh * p.head_stride + d);
+        if (odd_bf16(x)) dst[r * D + d] += __uint_as_float(x << 16);
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // Token rows of one tensor-map box: pages shorter than a unit give several.

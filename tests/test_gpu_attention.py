@@ -294,3 +294,66 @@ def test_short_parts_in_turn_through_the_same_buffers(moe, dim, capacity):
         for _ in range(20):
             again, lse2 = c.run()
             assert t.equal(out, again) and t.equal(lse, lse2)
+
+
+UNSEEN = {  # q_lens, own lengths, prefix, page, q heads, kv heads, dim, capacity
+    "tile": ([8, 3], [40, 3], 50, 16, 14, 2, 128, 0),
+    "tile_64": ([5, 16], [70, 30], 0, 16, 4, 4, 64, 0),
+    "warps": ([2, 1, 2], [90, 33, 64], 20, 32, 14, 2, 128, LONG),
+    "warps_64": ([16, 7], [64, 100], 0, 16, 3, 3, 64, LONG),
+    "half": ([40], [333], 70, 64, 6, 2, 128, LONG),
+    "both_halves": ([70, 0, 129], [70, 3, 300], 150, 32, 8, 2, 128, LONG),
+    "many_tokens_a_tile": ([300, 40], [431, 40], 1, 128, 2, 2, 64, LONG),
+}
+
+
+@pytest.mark.parametrize("name", UNSEEN)
+def test_values_that_a_row_does_not_see_do_not_reach_it(moe, name):
+    """Infinities and NaN in the values of a new token reach the rows that see it, and no earlier one."""
+    q_lens, lens, prefix, page, hq, hk, dim, capacity = UNSEEN[name]
+    c = Case(moe, 51, q_lens, lens, prefix, page, hq, hk, dim, capacity=capacity)
+    for b, ql in enumerate(q_lens):
+        for n, i in enumerate({ql - 1, ql // 2, ql // 3 + 1}):
+            j = lens[b] - ql + i
+            if not 0 < i < ql or j < 0:
+                continue
+            for h in range(hk):
+                for d, x in ((0, np.inf), (dim - 1, np.nan), ((17 + 5 * n + h) % dim, -np.inf), (40 + n, np.inf)):
+                    c.pg.v[int(c.pg.table[b, j // page]), j % page, h, d] = float(x)
+                    c.values[b][prefix + j, h, d] = x
+    out, lse = c.run()
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    scale, grp, n0, seen = dim ** -0.5, hq // hk, 0, 0
+    for b, ql in enumerate(q_lens):
+        vis = [prefix + max(0, lens[b] - ql + 1 + i) for i in range(ql)]
+        for h in range(hq):
+            with np.errstate(invalid="ignore"):
+                ref, rl, weight, mag = attend(c.qd[n0:n0 + ql, h], c.keys[b][:, h // grp], c.values[b][:, h // grp], vis, scale)
+            got = out[n0:n0 + ql, h]
+            fin = np.isfinite(ref)
+            seen += (~fin).sum()
+            assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)]), (b, h)
+            # The tolerances of Case.check.
+            e = (dim + 4) * 2.0 ** -24 * scale * mag + 2.0 ** -20
+            tol = (1.01 * 2.0 ** -8 * (weight + np.abs(ref)) + 2 * e[:, None] * weight + 1e-30)[fin]
+            assert np.all(np.abs(got[fin] - ref[fin]) <= tol), (b, h)
+            assert np.all(np.abs(lse[n0:n0 + ql, h] - rl) <= e + 2.0 ** -21 * (1 + np.abs(rl)))
+        n0 += ql
+    assert seen > 0
+
+
+@pytest.mark.parametrize("name", UNSEEN)
+def test_keys_that_a_row_does_not_see_do_not_reach_it(moe, name):
+    """The same of the keys: the last new token's are NaN; its own row is NaN, the others are as they were."""
+    t = torch()
+    q_lens, lens, prefix, page, hq, hk, dim, capacity = UNSEEN[name]
+    c = Case(moe, 52, q_lens, lens, prefix, page, hq, hk, dim, capacity=capacity)
+    good, glse = c.run()
+    for b, n in enumerate(lens):
+        if q_lens[b]:
+            c.pg.k[int(c.pg.table[b, (n - 1) // page]), (n - 1) % page] = float("nan")
+    out, lse = c.run()
+    last = [int(x) - 1 for x in np.cumsum(q_lens) if x]
+    rest = [i for i in range(c.n) if i not in last]
+    assert t.equal(out[rest], good[rest]) and t.equal(lse[rest], glse[rest])
+    assert out[last].isnan().all() and lse[last].isnan().all()
