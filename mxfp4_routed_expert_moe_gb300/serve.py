@@ -1,11 +1,15 @@
 """The operators around the layer in a serving step (``include/moe_serve.h``): new keys and values into
 a paged cache with rotary positions on the way, attention of a batch that shares a prefix over that cache,
-and sampling from logits.  Argument marshalling only, as in the package itself."""
+and sampling from logits.  Argument marshalling only, as in the package itself.
+
+What a kernel finds wrong in the values of its arguments (a page id, length or position out of range, a wait
+that gave up) it can only write down: pass ``status``, a GPU int32 word, and read it when the results matter.
+Without one such a call leaves unspecified outputs and no sign."""
 from __future__ import annotations
 
 import ctypes
 
-from . import DT_BF16, DT_F32, MoeError, _check, _ptr, lib
+from . import DT_BF16, DT_F32, MoeError, _check, lib
 
 __all__ = ["KVCache", "KVBatch", "kv_append", "prefix_attention", "attention_workspace_bytes", "sample",
            "rope_table", "SERVE_EXPORTS", "SAMPLE_MAX_VOCAB", "SERVE_MAX_BATCH",
@@ -80,6 +84,25 @@ def _want(t, what, dtype, shape=None):
     return t.data_ptr()
 
 
+def _same_gpu(device, tensors):
+    """Every (tensor or None, name) has to be on the GPU ``device``: the kernels would follow a host address."""
+    if device < 0:
+        raise ValueError("the tensors of a call must be on a GPU")
+    for t, what in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{what} must be on GPU {device}, as the others")
+
+
+def _status(status, device):
+    """Address of a status word: None, an address, or a GPU int32 tensor."""
+    if status is None or isinstance(status, int):
+        return status
+    if status.dtype is not torch.int32 or status.numel() < 1:
+        raise TypeError("status must be a torch.int32 word")
+    _same_gpu(device, ((status, "status"),))
+    return status.data_ptr()
+
+
 class KVCache:
     """A paged cache over two bf16 tensors [num_pages][page_size][kv_heads][head_dim].  Views of another
     order (head-major pages, one tensor that holds both) are taken as they are, by their strides."""
@@ -98,6 +121,9 @@ class KVCache:
         self.struct = _Cache(k.data_ptr(), v.data_ptr(), pages, size, heads, dim, *k.stride()[:3])
         self.ref = ctypes.byref(self.struct)
         self.heads, self.dim = heads, dim
+        self.device = k.get_device()
+        if v.get_device() != self.device:
+            raise ValueError("k and v of a cache must be on one device")
 
 
 class KVBatch:
@@ -128,6 +154,14 @@ class KVBatch:
         self.prefix_tokens = 0 if prefix_table is None else prefix_table.numel()
         self.ref = ctypes.byref(self.struct)
         self.tokens = self.struct.tokens
+        self.device = kv_len.get_device()
+        for t in (table, q_start, prefix_table):
+            if t is not None and t.get_device() != self.device:
+                raise ValueError("the tensors of a batch must be on one device")
+
+    def check_device(self, cache):
+        if self.device != cache.device:
+            raise ValueError("a batch must be on its cache's device")
 
     def check_prefix(self, cache):
         if self.struct.prefix_len > self.prefix_tokens * cache.struct.page_size:
@@ -178,8 +212,11 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope=Non
     if rope is not None:
         rows = rope.shape[0]
         rp = _want(rope, "rope", torch.float32, (rows, rot_dim))
+    sp = _status(status, cache.device)
+    batch.check_device(cache)
+    _same_gpu(cache.device, ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (rope, "rope")))
     _check(_READY.moe_kv_append(cache.ref, batch.ref, dt, qp, k.data_ptr(), v.data_ptr(), qh, qs, ks, vs, op, os, rp, rows,
-                                rot_dim, bool(interleaved), _ptr(status), _stream(stream, k)), "moe_kv_append")
+                                rot_dim, bool(interleaved), sp, _stream(stream, k)), "moe_kv_append")
 
 
 def attention_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int) -> int:
@@ -201,8 +238,13 @@ def prefix_attention(cache: KVCache, batch: KVBatch, q, out, ws, scale=None, lse
         raise TypeError(f"q and out must be torch.bfloat16, not {q.dtype} and {out.dtype}")
     batch.check_prefix(cache)
     lp = None if lse is None else _want(lse, "lse", torch.float32, (n, qh))
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    sp = _status(status, cache.device)
+    batch.check_device(cache)
+    _same_gpu(cache.device, ((q, "q"), (out, "out"), (ws, "ws"), (lse, "lse")))
     _check(_READY.moe_prefix_attention(cache.ref, batch.ref, q.data_ptr(), qh, qs, dim ** -0.5 if scale is None else scale,
-                                       out.data_ptr(), os, lp, ws.data_ptr(), ws.nbytes, _ptr(status),
+                                       out.data_ptr(), os, lp, ws.data_ptr(), ws.nbytes, sp,
                                        _stream(stream, q)), "moe_prefix_attention")
 
 
@@ -219,13 +261,15 @@ def sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=Non
     if vocab > 1 and one != 1:
         raise ValueError("logits must be contiguous in the last dimension")
     f32, i32, row = torch.float32, torch.int32, (rows,)
-    _check(L.moe_sample(rows, vocab, logits.data_ptr(), _dtype_of(logits, "logits"), stride if rows > 1 else vocab,
-                        _want(u, "u", f32, row),
-                        None if temperature is None else _want(temperature, "temperature", f32, row),
-                        None if top_k is None else _want(top_k, "top_k", i32, row),
-                        None if top_p is None else _want(top_p, "top_p", f32, row),
-                        None if min_p is None else _want(min_p, "min_p", f32, row), _want(token, "token", i32, row),
-                        None if logprob is None else _want(logprob, "logprob", f32, row),
-                        None if kept is None else _want(kept, "kept", i32, row),
-                        None if probs is None else _want(probs, "probs", f32, (rows, vocab)),
-                        _stream(stream, logits)), "moe_sample")
+    args = (rows, vocab, logits.data_ptr(), _dtype_of(logits, "logits"), stride if rows > 1 else vocab,
+            _want(u, "u", f32, row),
+            None if temperature is None else _want(temperature, "temperature", f32, row),
+            None if top_k is None else _want(top_k, "top_k", i32, row),
+            None if top_p is None else _want(top_p, "top_p", f32, row),
+            None if min_p is None else _want(min_p, "min_p", f32, row), _want(token, "token", i32, row),
+            None if logprob is None else _want(logprob, "logprob", f32, row),
+            None if kept is None else _want(kept, "kept", i32, row),
+            None if probs is None else _want(probs, "probs", f32, (rows, vocab)))
+    _same_gpu(logits.get_device(), ((u, "u"), (temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p"),
+                                    (token, "token"), (logprob, "logprob"), (kept, "kept"), (probs, "probs")))
+    _check(L.moe_sample(*args, _stream(stream, logits)), "moe_sample")

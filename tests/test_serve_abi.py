@@ -206,3 +206,63 @@ def test_max_q_past_what_the_batch_can_have_changes_no_plan(serve, kw, group):
     most = kw["tokens"] if "q_start" in kw else 1
     size = lambda m: L.moe_attention_workspace_bytes(ctypes.byref(cache(serve)), ctypes.byref(batch(serve, max_q=m, **kw)), 2 * group)  # noqa: E731
     assert 0 < size(most) == size(8) == size(100) == size((1 << 31) - 1)
+
+
+def test_tensors_off_the_gpu_are_refused(moe, monkeypatch):
+    """Each tensor argument of a call has to be on the cache's (or the logits') GPU: a host address is not followed.
+    Nothing is launched here, whatever the checks say."""
+    import torch as t
+    from mxfp4_routed_expert_moe_gb300 import serve as s
+
+    class Gpu(t.Tensor):  # a host tensor that says it is on device 0
+        def get_device(self):
+            return 0
+
+    calls = []
+    fake = type("L", (), {n: staticmethod(lambda *a, n=n: calls.append(n) or 0) for n in moe.SERVE_EXPORTS})()
+    s._lib()
+    monkeypatch.setattr(s, "_READY", fake)
+    gpu = lambda x: x.as_subclass(Gpu)  # noqa: E731
+    bf = lambda *x: t.zeros(*x, dtype=t.bfloat16)  # noqa: E731
+    i32 = lambda *x: t.zeros(*x, dtype=t.int32)  # noqa: E731
+
+    def refused(f, args, launch):
+        """Fails with every single argument on the host, passes with none."""
+        f(**{k: gpu(v) for k, v in args.items()})
+        assert calls == [launch]
+        calls.clear()
+        for name in args:
+            with pytest.raises(ValueError):
+                f(**{k: v if k == name else gpu(v) for k, v in args.items()})
+            assert not calls, name
+
+    def batch_of(kv_len, table, q_start, prefix_table):
+        return moe.KVBatch(kv_len, table, tokens=3, q_start=q_start, prefix_table=prefix_table, prefix_len=20)
+
+    here = dict(ck=bf(10, 16, 2, 64), cv=bf(10, 16, 2, 64), kv_len=i32(3), table=i32(3, 4), q_start=i32(4), prefix_table=i32(2))
+
+    def append(ck, cv, kv_len, table, q_start, prefix_table, **kw):
+        moe.kv_append(moe.KVCache(ck, cv), batch_of(kv_len, table, q_start, prefix_table), rot_dim=64, stream=0, **kw)
+
+    refused(append, here | dict(k=bf(3, 2, 64), v=bf(3, 2, 64), q=bf(3, 4, 64), q_out=bf(3, 4, 64), rope=t.zeros(9, 64),
+                                status=i32(1)), "moe_kv_append")
+
+    def attend(ck, cv, kv_len, table, q_start, prefix_table, **kw):
+        moe.prefix_attention(moe.KVCache(ck, cv), batch_of(kv_len, table, q_start, prefix_table), stream=0, **kw)
+
+    refused(attend, here | dict(q=bf(3, 4, 64), out=bf(3, 4, 64), ws=t.zeros(256, dtype=t.uint8), lse=t.zeros(3, 4),
+                                status=i32(1)), "moe_prefix_attention")
+    refused(lambda **kw: moe.sample(stream=0, **kw),
+            dict(logits=t.zeros(3, 50), u=t.zeros(3), token=i32(3), temperature=t.zeros(3), top_k=i32(3), top_p=t.zeros(3),
+                 min_p=t.zeros(3), logprob=t.zeros(3), kept=i32(3), probs=t.zeros(3, 50)), "moe_sample")
+
+
+def test_workspace_and_status_of_another_form_are_refused(serve, moe):
+    import torch as t
+    c = moe.KVCache(t.zeros(10, 16, 2, 64, dtype=t.bfloat16), t.zeros(10, 16, 2, 64, dtype=t.bfloat16))
+    b = moe.KVBatch(t.zeros(3, dtype=t.int32), t.zeros(3, 4, dtype=t.int32))
+    q = t.zeros(3, 4, 64, dtype=t.bfloat16)
+    with pytest.raises(ValueError, match="ws"):  # one byte, said to be many
+        moe.prefix_attention(c, b, q, q, t.zeros(1, dtype=t.uint8).expand(1 << 30), stream=0)
+    with pytest.raises(TypeError, match="status"):
+        moe.prefix_attention(c, b, q, q, t.zeros(256, dtype=t.uint8), status=t.zeros(1, dtype=t.int64), stream=0)
