@@ -159,9 +159,8 @@ class KVBatch:
             if t is not None and t.get_device() != self.device:
                 raise ValueError("the tensors of a batch must be on one device")
 
-    def check_device(self, cache):
-        if self.device != cache.device:
-            raise ValueError("a batch must be on its cache's device")
+    def get_device(self):
+        return self.device
 
     def check_prefix(self, cache):
         if self.struct.prefix_len > self.prefix_tokens * cache.struct.page_size:
@@ -213,8 +212,11 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope=Non
         rows = rope.shape[0]
         rp = _want(rope, "rope", torch.float32, (rows, rot_dim))
     sp = _status(status, cache.device)
-    batch.check_device(cache)
-    _same_gpu(cache.device, ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (rope, "rope")))
+    gpu = cache.device
+    # One expression where all is well: a list of names each time would be a tenth of the call.
+    if not (batch.device == gpu == k.get_device() == v.get_device() and gpu >= 0 and (q is None or q.get_device() == gpu)
+            and (q_out is None or q_out.get_device() == gpu) and (rope is None or rope.get_device() == gpu)):
+        _same_gpu(gpu, ((batch, "the batch"), (k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (rope, "rope")))
     _check(_READY.moe_kv_append(cache.ref, batch.ref, dt, qp, k.data_ptr(), v.data_ptr(), qh, qs, ks, vs, op, os, rp, rows,
                                 rot_dim, bool(interleaved), sp, _stream(stream, k)), "moe_kv_append")
 
@@ -241,8 +243,10 @@ def prefix_attention(cache: KVCache, batch: KVBatch, q, out, ws, scale=None, lse
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
     sp = _status(status, cache.device)
-    batch.check_device(cache)
-    _same_gpu(cache.device, ((q, "q"), (out, "out"), (ws, "ws"), (lse, "lse")))
+    gpu = cache.device
+    if not (batch.device == gpu == q.get_device() == out.get_device() == ws.get_device() and gpu >= 0
+            and (lse is None or lse.get_device() == gpu)):
+        _same_gpu(gpu, ((batch, "the batch"), (q, "q"), (out, "out"), (ws, "ws"), (lse, "lse")))
     _check(_READY.moe_prefix_attention(cache.ref, batch.ref, q.data_ptr(), qh, qs, dim ** -0.5 if scale is None else scale,
                                        out.data_ptr(), os, lp, ws.data_ptr(), ws.nbytes, sp,
                                        _stream(stream, q)), "moe_prefix_attention")
@@ -270,6 +274,12 @@ def sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=Non
             None if logprob is None else _want(logprob, "logprob", f32, row),
             None if kept is None else _want(kept, "kept", i32, row),
             None if probs is None else _want(probs, "probs", f32, (rows, vocab)))
-    _same_gpu(logits.get_device(), ((u, "u"), (temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p"),
-                                    (token, "token"), (logprob, "logprob"), (kept, "kept"), (probs, "probs")))
+    gpu = logits.get_device()
+    if not (gpu == u.get_device() == token.get_device() and gpu >= 0
+            and (temperature is None or temperature.get_device() == gpu) and (top_k is None or top_k.get_device() == gpu)
+            and (top_p is None or top_p.get_device() == gpu) and (min_p is None or min_p.get_device() == gpu)
+            and (logprob is None or logprob.get_device() == gpu) and (kept is None or kept.get_device() == gpu)
+            and (probs is None or probs.get_device() == gpu)):
+        _same_gpu(gpu, ((u, "u"), (token, "token"), (temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"),
+                        (min_p, "min_p"), (logprob, "logprob"), (kept, "kept"), (probs, "probs")))
     _check(L.moe_sample(*args, _stream(stream, logits)), "moe_sample")
