@@ -14,7 +14,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mxfp4.so")
 SOURCES = ["abi.cu", "route.cu", "route_tc.cu", "decode.cu", "decode_mx.cu", "prefill.cu", "serve.cu",
            "kv_append.cu", "attention.cu", "attention_split.cu", "sample.cu"]
-HEADERS = ["common.cuh", "kernels.h", "async.cuh", "route_small.cuh", "tcgen05.cuh", "decode_mx.cuh", "serve.cuh",
+HEADERS = ["common.cuh", "kernels.h", "launch_tables.h", "async.cuh", "route_small.cuh", "tcgen05.cuh", "decode_mx.cuh", "serve.cuh",
            "attention_warp.cuh", "attention_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

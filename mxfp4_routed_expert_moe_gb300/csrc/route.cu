@@ -12,6 +12,7 @@
 
 #include "async.cuh"
 #include "kernels.h"
+#include "launch_tables.h"
 #include "decode_mx.cuh"
 #include "route_small.cuh"
 
@@ -612,33 +613,20 @@ cudaError_t launch_plan_from_offsets(const BucketParams& b, const int32_t* offse
 }
 
 namespace {
-struct KeyVal { const void* k; int a; size_t b; int v; };
-KeyVal g_smem_attr[64];
-KeyVal g_occ[64];
-int g_n_smem = 0, g_n_occ = 0;
+SmemTable g_smem;
+OccupancyTable g_occ;
 }  // namespace
 
 cudaError_t ensure_smem_attr(const void* kernel, size_t bytes) {
-  for (int i = 0; i < g_n_smem; ++i)
-    if (g_smem_attr[i].k == kernel && g_smem_attr[i].b >= bytes) return cudaSuccess;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err != cudaSuccess) return err;
-  for (int i = 0; i < g_n_smem; ++i)
-    if (g_smem_attr[i].k == kernel) { g_smem_attr[i].b = bytes; return cudaSuccess; }
-  if (g_n_smem < 64) g_smem_attr[g_n_smem++] = {kernel, 0, bytes, 0};
-  return cudaSuccess;
+  return (cudaError_t)g_smem.ensure(kernel, bytes, [](const void* k, size_t n) {
+    return (int)cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n);
+  });
 }
 
 cudaError_t cached_occupancy(const void* kernel, int threads, size_t smem, int* out) {
-  for (int i = 0; i < g_n_occ; ++i)
-    if (g_occ[i].k == kernel && g_occ[i].a == threads && g_occ[i].b == smem) { *out = g_occ[i].v; return cudaSuccess; }
-  int occ = 0;
-  cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem);
-  if (err != cudaSuccess) return err;
-  if (occ < 1) occ = 1;
-  if (g_n_occ < 64) g_occ[g_n_occ++] = {kernel, threads, smem, occ};
-  *out = occ;
-  return cudaSuccess;
+  return (cudaError_t)g_occ.get(kernel, threads, smem, out, [](const void* k, int t, size_t n, int* ctas) {
+    return (int)cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, k, t, n);
+  });
 }
 
 int device_sm_count() {
