@@ -103,3 +103,11 @@ def test_traffic_record_follows_the_kernel_sources(tmp_path, monkeypatch):
     src.write_text(src.read_text() + "// changed\n")
     got, new_sha = bench.traffic_from_profiles(kernel, wl)
     assert got is None and new_sha != sha
+
+
+@pytest.mark.parametrize("kernel,workload,n", [("dec_gateup", "decode_T1_H7168_E896_k16_I1408", 175099136),
+                                               ("pf_gateup", "long_prefill_T4096_H7168_E896_k16_I1408_zipf1.1", 11420083712)])
+def test_recorded_traffic_belongs_to_the_present_kernels(kernel, workload, n):
+    """The captures that the bench's rooflines use were taken from the sources as they are: a change to them drops the
+    record, and the capture is to be taken again with it."""
+    assert bench.traffic_from_profiles(kernel, workload)[0] == n
