@@ -75,7 +75,8 @@ typedef struct {
  *   x_dtype      of q, k and v (MOE_DT_F32 / MOE_DT_BF16); the arithmetic is
  *                fp32, rounded once to bf16
  *   q, q_out     [tokens][q_heads][head_dim]; both NULL: keys and values only.
- *                q_out is bf16 and may be q itself (bf16, the same stride).
+ *                q_out is bf16 and may be q itself (bf16, the same stride);
+ *                its rows must not overlap.
  *   *_stride     elements between tokens; heads lie head_dim apart.  Pointers
  *                are 16-byte aligned, strides a multiple of 16 bytes.
  *   rope         [rope_rows][rot_dim] fp32: row p holds the rot_dim / 2 cosines
@@ -107,7 +108,8 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_bat
  * whatever they hold, and an infinity or NaN in a new token's key or value
  * reaches the rows that see the token alone.
  *   q, out       bf16 [tokens][q_heads][head_dim], *_stride elements between
- *                tokens (multiples of 8; 16-byte aligned pointers)
+ *                tokens (multiples of 8; 16-byte aligned pointers; rows of out
+ *                must not overlap)
  *   scale        > 0, finite
  *   lse          [tokens][q_heads] fp32 (natural logarithm) or NULL
  *   ws           moe_attention_workspace_bytes, 256-byte aligned, uninitialised

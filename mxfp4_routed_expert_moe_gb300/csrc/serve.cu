@@ -154,6 +154,11 @@ int check_heads(const moe_kv_cache* c, int q_heads) {
   return MOE_OK;
 }
 
+// Whether the rows of an output lie apart.
+bool rows_apart(const moe_kv_batch* b, int64_t stride, int64_t width) {
+  return b->tokens == 1 || stride >= width || stride <= -width;
+}
+
 }  // namespace
 
 extern "C" {
@@ -171,6 +176,9 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, int x_dt
   if (q) {
     if ((st = check_heads(cache, q_heads)) != MOE_OK) return st;
     if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % vec || q_out_stride % 8) return MOE_ERR_INVALID_ARG;
+    if (!rows_apart(batch, q_out_stride, (int64_t)q_heads * cache->head_dim)) return MOE_ERR_INVALID_ARG;
+    // In place: every row over itself.
+    if (q_out == q && (x_dtype != MOE_DT_BF16 || (q_out_stride != q_stride && batch->tokens > 1))) return MOE_ERR_INVALID_ARG;
   }
   if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (interleaved != 0 && interleaved != 1)) return MOE_ERR_INVALID_ARG;
   if (rot_dim > 0 && (!rope || !aligned(rope, 16) || rope_rows < 1)) return MOE_ERR_INVALID_ARG;
@@ -209,6 +217,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   if ((st = check_cache(cache)) != MOE_OK || (st = check_batch(batch)) != MOE_OK) return st;
   if ((st = check_heads(cache, q_heads)) != MOE_OK) return st;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8) return MOE_ERR_INVALID_ARG;
+  if (!rows_apart(batch, out_stride, (int64_t)q_heads * cache->head_dim)) return MOE_ERR_INVALID_ARG;
   if ((lse && !aligned(lse, 4)) || (status && !aligned(status, 4))) return MOE_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;

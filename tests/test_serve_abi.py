@@ -266,3 +266,15 @@ def test_workspace_and_status_of_another_form_are_refused(serve, moe):
         moe.prefix_attention(c, b, q, q, t.zeros(1, dtype=t.uint8).expand(1 << 30), stream=0)
     with pytest.raises(TypeError, match="status"):
         moe.prefix_attention(c, b, q, q, t.zeros(256, dtype=t.uint8), status=t.zeros(1, dtype=t.int64), stream=0)
+
+
+@pytest.mark.parametrize("kw", [dict(os=0), dict(os=248), dict(os=-248), dict(q_out=A, q=A, qs=512, os=256),
+                                dict(q_out=A, q=A, dtype=0, qs=256, os=256)])
+def test_append_refuses_query_rows_over_one_another(serve, kw):
+    """Rows of q_out that overlap, or that lie over rows of q other than their own, would hold what came last."""
+    assert append(serve, cache(serve), batch(serve), **kw) == 1
+
+
+@pytest.mark.parametrize("os", [0, 248, -248])
+def test_attention_refuses_result_rows_over_one_another(serve, os):
+    assert attend(serve, cache(serve), batch(serve), os=os) == 1
