@@ -110,7 +110,7 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_bat
  *   q, out       bf16 [tokens][q_heads][head_dim], *_stride elements between
  *                tokens (multiples of 8; 16-byte aligned pointers; rows of out
  *                must not overlap)
- *   scale        > 0, finite
+ *   scale        > 0; scale log2(e) finite in fp32
  *   lse          [tokens][q_heads] fp32 (natural logarithm) or NULL
  *   ws           moe_attention_workspace_bytes, 256-byte aligned, uninitialised
  * The sums of a row are joined in a fixed order: results are the same from run

@@ -219,7 +219,8 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8) return MOE_ERR_INVALID_ARG;
   if (!rows_apart(batch, out_stride, (int64_t)q_heads * cache->head_dim)) return MOE_ERR_INVALID_ARG;
   if ((lse && !aligned(lse, 4)) || (status && !aligned(status, 4))) return MOE_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !isfinite(scale_log2)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   AttnParams p;
   memset(&p, 0, sizeof p);
@@ -232,7 +233,7 @@ int moe_prefix_attention(const moe_kv_cache* cache, const moe_kv_batch* batch, c
   p.q_stride = q_stride;
   p.out_stride = out_stride;
   p.q_heads = q_heads;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.kv_heads = cache->kv_heads;
   p.head_dim = cache->head_dim;
   p.page_size = cache->page_size;

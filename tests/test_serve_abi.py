@@ -278,3 +278,8 @@ def test_append_refuses_query_rows_over_one_another(serve, kw):
 @pytest.mark.parametrize("os", [0, 248, -248])
 def test_attention_refuses_result_rows_over_one_another(serve, os):
     assert attend(serve, cache(serve), batch(serve), os=os) == 1
+
+
+def test_a_scale_past_the_range_of_its_base_2_form_is_refused(serve):
+    """The kernels take scale log2(e): of a finite scale above 2.36e38 it is infinite, and 0 times it NaN."""
+    assert attend(serve, cache(serve), batch(serve), scale=3e38) == 1
