@@ -7,7 +7,8 @@ numbers.  The dense projections are plain torch products.
 
     python examples/decode_step.py [--sequences 8] [--prompt 300] [--steps 16] [--private]
 
-``--private`` gives every sequence its own copy of the prompt instead: the same tokens from a larger cache.
+``--private`` gives every sequence its own copy of the prompt instead: the same computation from a larger cache,
+in other tiles (rounding may part the drawn tokens after some steps).
 """
 from __future__ import annotations
 

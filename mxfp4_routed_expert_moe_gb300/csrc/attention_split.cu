@@ -4,9 +4,10 @@
 // (attention_warp.cuh); a batch behind a prefix has both, one bound by the
 // tensor cores and the other by HBM, and the plan gives each side as many CTAs
 // as its units need, so that they end together.  As two kernels after one
-// another, each with the whole chip, their start-up and tails added up: 64
-// sequences of up to 2,047 tokens behind 8,192 (56 query, 8 key heads of 128)
-// took 99 us in all against 86.
+// another, each with the whole chip, their start-up and tails added up: when the
+// two were joined, 64 sequences of up to 2,047 tokens behind 8,192 (56 query, 8
+// key heads of 128) went from 99 us in all to 86.  They take 88 to 91 with what
+// the kernel does today.
 #include "attention_tc.cuh"
 #include "attention_warp.cuh"
 
@@ -52,8 +53,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // The warp side alone, for calls that have nothing for the other: the smaller
-// kernel starts faster (24 sequences of up to 32,771 tokens, with the join: 93
-// us, 104 us on the split kernel, when this was taken; 90 us now).
+// kernel starts faster (24 sequences of up to 32,771 tokens, 4 key heads of 64,
+// with the join: 79 us, 87 us on the split kernel).
 template <int D>
 __global__ void __launch_bounds__(kAttnWarpWorkers * 32, 1)
     k_attn_warp(const AttnParams p, const __grid_constant__ CUtensorMap warp_k, const __grid_constant__ CUtensorMap warp_v) {

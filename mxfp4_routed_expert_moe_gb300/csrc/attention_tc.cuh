@@ -25,9 +25,9 @@
 // rescales O_t in Tensor Memory): any reference gives the same quotient, and
 // 2^8 keeps every partial sum far inside fp32.
 //
-// A unit takes 1.51 us with all SMs at work, 1.34 at the chip's measured tensor
+// A unit takes 1.48 us with all SMs at work, 1.34 at the chip's measured tensor
 // rate: 256 sequences of 56 query and 8 key heads over a shared prefix alone take
-// 172 us for 32,768 tokens and 315 for 65,536, start-up and join included, 1.69
+// 172 us for 32,768 tokens and 312 for 65,536, start-up and join included, 1.72
 // PFLOP/s between the two.
 #pragma once
 

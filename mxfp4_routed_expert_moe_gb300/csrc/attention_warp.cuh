@@ -15,8 +15,8 @@ namespace moe {
 // with tensor-map boxes and takes them in turn, so that no warp waits for
 // another and short sequences cost no CTA-wide joins (four warps that shared
 // each unit spent 1.0 us of a 3.2 us one-unit segment on joining).  48 sequences
-// of up to 32,768 tokens: 6.5 TB/s with 8 key heads of 128, 4.6 TB/s with 4 of 64
-// and 16 query heads each (bound by instructions there: twice the scores a byte).
+// of up to 32,768 tokens, with the join: 6.6 TB/s with 8 key heads of 128 (492
+// us), 6.0 TB/s with 4 of 64 and 16 query heads each (135 us).
 constexpr int kWorkers = kAttnWarpWorkers;
 
 template <int D>

@@ -23,9 +23,9 @@
 // instructions of the passes and the barriers for many: shared memory holds
 // some 38 rows of 128,000 scores on the chip at a time.  Reading the scores
 // again from L2 for each pass instead, with more CTAs resident, was slower
-// (512 rows of 128,000 with all filters and probabilities: 391 against 377 us,
-// 258 by now; 64 rows of 163,840: 74 against 64 us, 49 by now; one row of
-// 100,003: 10 us).
+// (512 rows of 128,000 with all filters and probabilities: 391 against 377 us
+// then; 64 rows of 163,840: 74 against 64 us).  They take 259 and 49 us now, one
+// row of 100,003 10.7.
 #include <cooperative_groups.h>
 
 #include <cuda/std/type_traits>

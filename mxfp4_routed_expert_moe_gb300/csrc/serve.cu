@@ -83,15 +83,16 @@ void plan_sides(const moe_kv_batch& b, int group, int head_dim, AttnSide (&side)
 }
 
 // Whether the tile kernel takes the call, and on clusters of how many CTAs
-// (0: no).  It goes by the most tokens a sequence may have (its table's
-// width): as many CTAs a tile as keep all tiles on the chip at once.  A wave of
-// it costs about 6 us and each unit that a warp takes in turn 1.2 us; the
-// split kernels cost 10 us and more before their first byte, or 30 us where the
-// prefix and the own parts go to two kernels.  Measured at 56 / 8 heads of 128,
-// tile against split: 1 sequence of 200 tokens 6.6 / 12.3 us, of 16,000 (11
-// units in turn) 26.4 / 34.7; 16 of 1,000 14.3 / 16.4, of 4,000 (21 units) 37.7
-// / 36.0; 32 of 100 behind 1,000 (two waves, 6 units each) 28.3 / 33.0; 64 of
-// 200 (four waves) 26.6 / 14.9.
+// (0: no): as many CTAs a tile as keep all tiles on the chip at once.  A wave of
+// it costs about 6 us and each unit that a warp takes in turn 1.2 us; the split
+// kernel and its join cost 10 us and more before their first byte, or 20 us
+// where prefix and own parts go to different sides.  Measured at 56 / 8 heads of
+// 128, tile against split: 1 sequence of 200 tokens 6.7 / 11.2 us, of 16,000 (11
+// units in turn) 23.3 / 50.8; 16 of 1,000 11.2 / 16.1, of 4,000 (21 units) 31.8
+// / 34.9; 32 of 100 behind 1,000 (two waves, 6 units each) 23.0 / 25.6; 64 of
+// 200 (four waves) 22.5 / 15.1.  The call does not know lengths, so the rule
+// goes by the most tokens a sequence may have, its table's width: with a table
+// for 40,000 tokens the sequence of 200 takes the 11.2 us.
 int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
   const int64_t row_tiles = ((int64_t)most_new(b) * group + kAttnWarpRows - 1) / kAttnWarpRows;
   const int64_t tiles = b.batch * c.kv_heads * row_tiles;
@@ -101,9 +102,9 @@ int tile_cluster(const moe_kv_batch& b, const moe_kv_cache& c, int group) {
   while (cl < 8 && tiles * cl * 2 <= kNumSMs && (int64_t)cl * kAttnWarpWorkers < units) cl *= 2;
   const int64_t each = (units + cl * kAttnWarpWorkers - 1) / (cl * kAttnWarpWorkers);
   if (tiles * cl <= kNumSMs) return each <= 16 ? cl : 0;
-  const bool two_kernels = b.prefix_len > 0 && (int64_t)b.tokens * group > kAttnWarpRows &&
-                           (int64_t)most_new(b) * group <= kAttnWarpRows;
-  return tiles <= 2 * kNumSMs && two_kernels && each <= 6 ? cl : 0;
+  const bool two_sides = b.prefix_len > 0 && (int64_t)b.tokens * group > kAttnWarpRows &&
+                         (int64_t)most_new(b) * group <= kAttnWarpRows;
+  return tiles <= 2 * kNumSMs && two_sides && each <= 6 ? cl : 0;
 }
 
 size_t side_layout(const moe_kv_batch& b, int group, int kv_heads, int head_dim, AttnSide (&side)[2], void* base) {
@@ -137,7 +138,7 @@ int cache_map(CUtensorMap* m, const moe_kv_cache* c, void* base, int rows) {
   const cuuint32_t step[4] = {1, 1, 1, 1};
   // L2 fetches what one token of a head holds: with more, short heads bring in
   // their neighbours, which other CTAs read at other times (24 sequences of up
-  // to 32,771 tokens, 4 key heads of 64: 80 us, 89 with 256 bytes; no difference
+  // to 32,771 tokens, 4 key heads of 64: 79 us, 89 with 256 bytes; no difference
   // for heads of 128).
   const CUtensorMapL2promotion fetch =
       c->head_dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;

@@ -131,8 +131,8 @@ constexpr int kAttnTcUnit = 128;
 // a tile of more than 128 rows; how much longer the Tensor Memory side takes to
 // get going; and the units that a tile of the warp side counts beside its
 // tile_cost, since few CTAs take many tiles in turn next to a busy other side
-// (256 sequences with one token each of their own behind 32,768: 190 us, 212
-// without).
+// (256 sequences with one token each of their own behind 32,768: 190 us, 221
+// without; with up to 509 tokens 235 and 240).
 constexpr float kAttnWarpUnitCost = 1.5f, kAttnTcUnitCost = 1.6f, kAttnTcStart = 5.f, kAttnWarpTileMore = 0.7f;
 
 // What a set's entries say, as loaded.
@@ -424,11 +424,11 @@ __device__ __forceinline__ int attn_visible(const AttnParams& p, const AttnSeg& 
 // at the same time, unit x as near as can be to x modulo the ranges' length
 // after the start.  The row tiles of a key head read the same cache; with every
 // range in plain order each unit came from HBM for most of them, once the
-// prefix was longer than L2 holds (256 sequences of up to 509 tokens behind
-// 32,768, 134 MB of prefix, 7 tiles a key head: 247 us in plain order, 229
-// turned).  What L2 holds is left in plain order, in which the CTAs ask for
-// different lines (9 prompts of up to 301 tokens behind 4,001: 117 us, 122
-// turned).
+// prefix was longer than L2 holds (256 sequences of one token behind 32,768, 134
+// MB of prefix, 7 tiles a key head: 207 us in plain order, 190 turned; of up to
+// 509 tokens 240 and 235).  What L2 holds is left in plain order, in which the
+// CTAs ask for different lines (9 prompts of up to 301 tokens behind 4,001: 123.5
+// us either way).
 constexpr long long kAttnTurnBytes = 96ll << 20;
 template <bool TURN>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& sh, const AttnSide& sd, AttnWalk& w,
@@ -486,9 +486,10 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, const AttnPlan& s
 // with the others' weights of 0 an infinity or NaN would become NaN.  So these
 // are taken out of the copy in shared memory (clear_odd_values) and added to the
 // sums of the rows that see them (add_odd_values), which a positive weight leaves
-// what they are.  Looking for them costs 9 prompts of up to 301 tokens behind
-// 4,001 123 us instead of 118, and batches with one new token each, whose tiles
-// have no such tokens, 1 to 3 % of code in the way.
+// what they are.  With the search for them 9 prompts of up to 301 tokens behind
+// 4,001 take 123 us instead of 118 and 8 tokens over 16,001 34.6 instead of 33.3;
+// tiles of one new token have none, and pay for code in the way alone (256
+// sequences of up to 509 tokens behind 32,768: 235 instead of 229).
 __device__ __forceinline__ bool odd_bf16(uint32_t x) { return (x & 0x7F80u) == 0x7F80u; }
 
 // By one warp: tokens [t0, t1) of V in shared memory, 128 bytes a token in each
@@ -547,7 +548,8 @@ __host__ __device__ __forceinline__ int attn_box(int page_size, int unit) { retu
 cudaError_t launch_attn_split(const AttnParams& p, const CUtensorMap (&maps)[4], cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tile(const AttnParams& p, int cl, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s);
-// One CTA per SM.
+// One CTA per SM of the chip that the library is built for: the workspace goes by
+// it, so it is not asked of the device as the layer's launches do.
 constexpr int kAttnCtas = kNumSMs;
 
 }  // namespace moe
