@@ -106,7 +106,7 @@ size_t moe_attention_workspace_bytes(const moe_kv_cache* cache, const moe_kv_bat
  * A row that sees nothing (kv_len[b] - q_len[b] + i < 0 and no prefix) gives
  * zeros and lse = -inf.  Cache rows past a sequence's length are never used,
  * whatever they hold, and an infinity or NaN in a new token's key or value
- * reaches the rows that see the token alone.
+ * reaches only the rows that see the token.
  *   q, out       bf16 [tokens][q_heads][head_dim], *_stride elements between
  *                tokens (multiples of 8; 16-byte aligned pointers; rows of out
  *                must not overlap)
