@@ -13,9 +13,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mxfp4.so")
 SOURCES = ["abi.cu", "route.cu", "route_tc.cu", "decode.cu", "decode_mx.cu", "prefill.cu", "serve.cu",
-           "kv_append.cu", "attention.cu", "attention_split.cu", "sample.cu"]
+           "kv_append.cu", "attention.cu", "attention_split.cu", "sample.cu", "dense.cu", "mx.cu", "rms_norm.cu",
+           "mx_linear.cu", "token_logprobs.cu"]
 HEADERS = ["common.cuh", "kernels.h", "launch_tables.h", "async.cuh", "route_small.cuh", "tcgen05.cuh", "decode_mx.cuh", "serve.cuh",
-           "attention_warp.cuh", "attention_tc.cuh"]
+           "attention_warp.cuh", "attention_tc.cuh", "dense.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC] + ARCH
@@ -23,7 +24,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-r
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS if os.path.exists(os.path.join(CSRC, f))]
-    files += [os.path.join(INCLUDE, f) for f in ("moe_mxfp4.h", "moe_serve.h")]
+    files += [os.path.join(INCLUDE, f) for f in ("moe_mxfp4.h", "moe_serve.h", "moe_dense.h")]
     return files
 
 
