@@ -11,66 +11,179 @@
 // memory (128 or 256 elements), four MMAs, and one or two 4-byte scale words a row.
 //
 // A CTA's warps: one copies operand tiles by tensor maps, one issues the MMAs, four
-// bring scale words from global memory into the 32 x 4 word blocks that tcgen05.cp
-// spreads to Tensor Memory, and write the result in the end.
-#include <cooperative_groups.h>
-
+// bring the scales to Tensor Memory, the epilogue's warps write the results.
+//
+// Scales lie in rows as stored, 16 bytes (four words) a row at a time; the MMA
+// wants the words of rows l, l + 32, l + 64, l + 96 side by side in lane l, in each
+// of the four lane quarters.  The four warps read a row a thread, several steps
+// ahead, exchange the words through shared memory and store them with tcgen05.st,
+// four words (two or four slices) a step.  (tcgen05.cp from shared memory needs a
+// proxy fence after the writes, which waits for the thread's loads in flight as
+// well: 1 us a slice.)
 #include "dense.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kRows = 128;           // weight rows of a tile
 constexpr int kTileBytes = kRows * 128;
 constexpr int kMaxNt = 256;          // activation rows of a tile
 constexpr int kMaxStages = 8;
 constexpr int kMaxCl = 8;
+constexpr int kSfRing = 3;           // steps of scales in Tensor Memory
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kSfWarp0 = 2, kSfWarps = 4;
 constexpr int kThreads = (kSfWarp0 + kSfWarps) * 32;
+constexpr int kSfBarrier = 1;        // named barrier of the scale warps
 
-// MX instruction descriptor of kind::mxf4 (E2M1 both, UE8M0 scales, K = 64): a_sf,
+// Instruction descriptor of kind::mxf4 (E2M1 both, UE8M0 scales, K = 64): a_sf,
 // b_sf are 0 or 2, the first of the two scale bytes.
 __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t a_sf, uint32_t b_sf) {
   return (b_sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27) |
          (a_sf << 29);
 }
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
+
+// ------------------------------------------- instructions of one CTA or a pair --
+// G = 1: one CTA's tile; G = 2: a pair's, issued by its first CTA for both.
+template <int G>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t acc) {
+  if (G == 1)
+    umma_mx(d, a, b, idesc, sfa, sfb, acc);
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
 }
-// 32 rows of 16 bytes from shared memory to 32 lanes x 4 columns, in each of the
-// four lane quarters.  In order with the MMAs that the same thread issues.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(128u >> 4) << 32;  // eight rows of 16 bytes
-  d |= (uint64_t)1u << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+template <int G>
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t acc) {
+  if (G == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+// Arrive on the barrier (of both CTAs of a pair) when all that this thread issued
+// has completed.
+template <int G>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (G == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+template <int G>
+__device__ __forceinline__ void lin_alloc(uint32_t* dst, uint32_t cols) {
+  if (G == 1) {
+    tmem_alloc(dst, cols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int G>
+__device__ __forceinline__ void lin_dealloc(uint32_t taddr, uint32_t cols) {
+  if (G == 1)
+    tmem_dealloc(taddr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Address of rank's copy of a shared-memory place of this CTA.
+__device__ __forceinline__ uint32_t remote_smem(const void* p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Tensor-map load into this CTA's shared memory, its bytes counted on a barrier of
+// the pair's first CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Shared memory of this CTA to another's, completing on a barrier there.
+__device__ __forceinline__ void bulk_s2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <bool TRY>
+__device__ __forceinline__ bool bar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  if (TRY)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return done != 0;
+}
+
+// ------------------------------------------------------------------ common parts --
 struct LinShared {
-  uint64_t full[kMaxStages];   // stage filled: the copies' bytes and the scale warps
-  uint64_t empty[kMaxStages];  // stage consumed: tcgen05.commit
-  uint64_t done;               // all MMAs of the tile
+  uint64_t full[kMaxStages];    // operands landed (a pair: the first CTA's, for both)
+  uint64_t empty[kMaxStages];   // consumed: commit
+  uint64_t sf_full[kSfRing];    // scales stored: scale warps (a pair: the first CTA's)
+  uint64_t sf_empty[kSfRing];   // used: commit
+  uint64_t sums;                // a tile's MMAs have finished: commit
+  uint64_t drained;             // pairs: the sums have been read
+  uint64_t recv;                // clusters: the others' sums have arrived
   uint32_t tmem_base;
   int abort_flag;
 };
 
 // What the launch fixes.
 struct LinTile {
-  int nt;            // activation rows of a tile, a multiple of 16
+  int nt;            // activation rows of a tile
+  int xrows;         // of them in one CTA's shared memory
+  int nb;            // blocks of 128 in nt, rounded up
   int stages;
   uint32_t stage_bytes;
-  int slices;        // of the whole inner size
+  int slices;        // of the inner size
   int per;           // of a CTA
-  uint32_t tmem_cols;
+  int tiles_n, tiles;
+  uint32_t tmem_cols, sf_col;
+  uint32_t recv_off;  // of the others' sums, behind the ring and this CTA's own
 };
 
 struct LinCtx {
@@ -79,32 +192,61 @@ struct LinCtx {
   long long wait_limit;
 };
 
+__device__ __forceinline__ void report(int32_t* status) {
+  if (status) atomicCAS((unsigned*)status, 0u, (unsigned)MOE_ERR_TIMEOUT);
+}
 __device__ __forceinline__ bool lin_wait(const LinCtx& c, uint64_t* bar, uint32_t parity) {
   LinShared& sh = *c.sh;
   const bool diag = c.wait_limit < kWaitCycles;
-  if (diag ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (diag ? bar_poll<false>(bar, parity) : bar_poll<true>(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (diag ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (diag ? bar_poll<false>(bar, parity) : bar_poll<true>(bar, parity)) return true;
     if (*(volatile int*)&sh.abort_flag) return false;
     if (clock64() - t0 > c.wait_limit) {
-      if (c.status) atomicCAS((unsigned*)c.status, 0u, (unsigned)MOE_ERR_TIMEOUT);
+      report(c.status);
       *(volatile int*)&sh.abort_flag = 1;
       return false;
     }
   }
 }
+__device__ __forceinline__ bool lin_warp_wait(const LinCtx& c, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, lin_wait(c, bar, parity));
+}
 
-// Scale words of one row: 16 bytes (four words) a step.
+// Place in a ring: index, and the parity of its current round.
+struct Ring {
+  int i = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) i = 0, ++round;
+  }
+  // Parity of the phase that frees the place for this round (rounds from 1).
+  __device__ __forceinline__ uint32_t freed() const { return (round - 1) & 1; }
+  __device__ __forceinline__ uint32_t filled() const { return round & 1; }
+};
+
+template <bool F4>
+struct LinCfg {
+  static constexpr int kWords = F4 ? 2 : 1;       // scale words of a row in a slice
+  static constexpr int kStep = 4 / kWords;        // slices of a step of scales
+};
+
+// Scale words of one row: 16 bytes (four words) a step; past the end, and rows past
+// the end, scale 1.
 struct ScaleRow {
-  const uint32_t* p;  // word 0, or null: a row past the end reads as scale 1
+  const uint32_t* p;
   int words;
   bool wide;
+  __device__ __forceinline__ ScaleRow(const uint8_t* base, int64_t stride, int row, int rows, int w0, int count)
+      : p(row < rows ? reinterpret_cast<const uint32_t*>(base + row * stride) + w0 : nullptr),
+        words(count - w0),
+        wide((((uintptr_t)base | (uintptr_t)stride | (uintptr_t)(4 * w0)) & 15) == 0) {}
   __device__ __forceinline__ uint4 load(int w) const {
     const uint32_t one = 0x7F7F7F7Fu;
-    if (!p || w >= words) return make_uint4(one, one, one, one);
-    if (wide && w + 4 <= words) return __ldg(reinterpret_cast<const uint4*>(p + w));
     uint4 v = make_uint4(one, one, one, one);
+    if (!p || w >= words) return v;
+    if (wide && w + 4 <= words) return __ldg(reinterpret_cast<const uint4*>(p + w));
     v.x = __ldg(p + w);
     if (w + 1 < words) v.y = __ldg(p + w + 1);
     if (w + 2 < words) v.z = __ldg(p + w + 2);
@@ -113,20 +255,181 @@ struct ScaleRow {
   }
 };
 
-template <bool F4>
-struct LinCfg {
-  static constexpr int kWords = F4 ? 2 : 1;  // scale words of a row in a slice
-  static constexpr int kSfBytes = 512 * kWords;  // of 128 rows
-};
+// One tile's scales by the four scale warps: `steps` steps of words from w0 on, of
+// weight rows n0.. and activation rows t0...  ok turns false where a wait gave up;
+// the steps are walked all the same, since the warps meet at each.
+constexpr int kSfAhead = 4;  // steps in flight: more than HBM's latency
+constexpr uint32_t kSwapWords = 4 * 3 * kRows;  // of one exchange buffer (there are two)
+template <int G>
+__device__ __forceinline__ void scales_of_tile(const LinearParams& p, const LinTile& t, const LinCtx& c, uint32_t* swap,
+                                               uint32_t tmem, int n0, int t0, int w0, int steps, Ring& ring, int& step,
+                                               bool& ok) {
+  const int tid = threadIdx.x - kSfWarp0 * 32, lane = tid & 31, q = (threadIdx.x >> 5) & 3;
+  // Thread tid reads row tid / 4 + 32 (tid % 4) of each block: the word's place
+  // among the blocks of four is tid.
+  const int r = (tid >> 2) + 32 * (tid & 3), words = p.K / 128;
+  const ScaleRow rw(p.ws, p.ws_stride, n0 + r, p.N, w0, words);
+  const ScaleRow rx0(p.xs, p.xs_stride, t0 + r, r < t.nt ? p.T : 0, w0, words);
+  const ScaleRow rx1(p.xs, p.xs_stride, t0 + 128 + r, 128 + r < t.nt ? p.T : 0, w0, words);
+  const int nb = t.nb, blocks = 1 + nb;
+  uint4 vw[kSfAhead], va[kSfAhead], vb[kSfAhead];
+#pragma unroll
+  for (int d = 0; d < kSfAhead; ++d) {
+    vw[d] = rw.load(4 * d);
+    va[d] = rx0.load(4 * d);
+    vb[d] = nb > 1 ? rx1.load(4 * d) : va[d];
+  }
+  const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + t.sf_col;
+  for (int g0 = 0; g0 < steps; g0 += kSfAhead) {
+#pragma unroll
+    for (int d = 0; d < kSfAhead; ++d) {
+      if (g0 + d >= steps) break;
+      uint32_t* buf = swap + (step & 1) * kSwapWords;
+      const uint32_t a[4] = {vw[d].x, vw[d].y, vw[d].z, vw[d].w}, b0[4] = {va[d].x, va[d].y, va[d].z, va[d].w},
+                     b1[4] = {vb[d].x, vb[d].y, vb[d].z, vb[d].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        buf[(3 * w + 0) * kRows + tid] = a[w];
+        buf[(3 * w + 1) * kRows + tid] = b0[w];
+        if (nb > 1) buf[(3 * w + 2) * kRows + tid] = b1[w];
+      }
+      // Everyone has read the other buffer, too, before it is written again.
+      named_sync(kSfBarrier, kSfWarps * 32);
+      if (g0 + d + kSfAhead < steps) {
+        const int w = 4 * (g0 + d + kSfAhead);
+        vw[d] = rw.load(w);
+        va[d] = rx0.load(w);
+        if (nb > 1) vb[d] = rx1.load(w);
+      }
+      if (ok && ring.round > 0) ok = lin_warp_wait(c, &c.sh->sf_empty[ring.i], ring.freed());
+      if (!ok) {
+        ++step;
+        continue;
+      }
+      tc_fence_after();
+      const uint32_t col = lanes + (uint32_t)(ring.i * 16 * blocks);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint4 x = *reinterpret_cast<const uint4*>(&buf[(3 * w + 0) * kRows + 4 * lane]);
+        const uint4 y = *reinterpret_cast<const uint4*>(&buf[(3 * w + 1) * kRows + 4 * lane]);
+        tmem_st4(col + (uint32_t)(4 * blocks * w), x.x, x.y, x.z, x.w);
+        tmem_st4(col + (uint32_t)(4 * blocks * w + 4), y.x, y.y, y.z, y.w);
+        if (nb > 1) {
+          const uint4 z = *reinterpret_cast<const uint4*>(&buf[(3 * w + 2) * kRows + 4 * lane]);
+          tmem_st4(col + (uint32_t)(4 * blocks * w + 8), z.x, z.y, z.z, z.w);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (G == 1)
+          mbar_arrive(&c.sh->sf_full[ring.i]);
+        else
+          mbar_arrive_cluster(remote_smem(&c.sh->sf_full[ring.i], 0));
+      }
+      ring.next(kSfRing);
+      ++step;
+    }
+  }
+}
 
-// Scale bytes and Tensor Memory columns of a stage.
-template <bool F4>
-__host__ __device__ constexpr uint32_t sf_bytes(int nt) { return LinCfg<F4>::kSfBytes * (1 + (nt + 127) / 128); }
-template <bool F4>
-__host__ __device__ constexpr uint32_t sf_cols(int nt) { return 4 * LinCfg<F4>::kWords * (1 + (nt + 127) / 128); }
+// One tile's MMAs, `count` slices, by one thread.
+template <bool F4, int G>
+__device__ __forceinline__ bool mmas_of_tile(const LinTile& t, const LinCtx& c, uint32_t ring0, uint32_t tmem, int count,
+                                             Ring& ring, Ring& sf) {
+  using C = LinCfg<F4>;
+  const int blocks = 1 + t.nb;
+  const uint32_t id0 = F4 ? idesc_mxf4(G * kRows, t.nt, 0, 0) : idesc_mx_f32(G * kRows, t.nt, kMxE2M1, kMxE4M3, 0, 0);
+  uint32_t acc = 0u;
+  for (int s0 = 0; s0 < count; s0 += C::kStep) {
+    if (!lin_wait(c, &c.sh->sf_full[sf.i], sf.filled())) return false;
+    const uint32_t col = tmem + t.sf_col + (uint32_t)(sf.i * 16 * blocks);
+#pragma unroll
+    for (int j = 0; j < C::kStep; ++j) {
+      if (s0 + j >= count) break;
+      if (!lin_wait(c, &c.sh->full[ring.i], ring.filled())) return false;
+      tc_fence_after();
+      const uint32_t sb = ring0 + (uint32_t)ring.i * t.stage_bytes;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        const uint64_t ad = sdesc_sw128(sb + 32 * kb), bd = sdesc_sw128(sb + kTileBytes + 32 * kb);
+        const uint32_t w = F4 ? 2 * j + (kb >> 1) : j, id = F4 ? 2 * (kb & 1) : kb;
+        const uint32_t sfa = col + 4 * blocks * w, idesc = id0 | (id << 4) | (id << 29);
+        if (F4)
+          mma_mxf4<G>(tmem, ad, bd, idesc, sfa, sfa + 4, acc);
+        else
+          mma_mx<G>(tmem, ad, bd, idesc, sfa, sfa + 4, acc);
+        acc = 1u;
+      }
+      commit<G>(&c.sh->empty[ring.i]);
+      ring.next(t.stages);
+    }
+    commit<G>(&c.sh->sf_empty[sf.i]);
+    sf.next(kSfRing);
+  }
+  return true;
+}
 
-// One tile, its inner size cut among the CTAs of a cluster, which add their sums in
-// rank order through distributed shared memory.
+// After the last __syncthreads of a CTA in which a wait gave up: copies may be in
+// flight, and have to land before the CTA may exit.  Their barriers miss other
+// arrivals, so a time is waited that covers any.
+__device__ __forceinline__ void let_copies_land(const LinShared& sh) {
+  if (sh.abort_flag) {
+    const long long w0 = clock64();
+    while (clock64() - w0 < 20000000) __nanosleep(1000);
+  }
+}
+
+// Four neighbouring results of a row from n on.
+template <bool OUT_BF16>
+__device__ __forceinline__ void put4(const LinearParams& p, int64_t t, int n, float4 y, bool wide) {
+  if (n >= p.N) return;
+  if (wide && n + 4 <= p.N) {
+    if (OUT_BF16) {
+      if (p.add) {
+        const uint2 a = *reinterpret_cast<const uint2*>((const uint16_t*)p.add + t * p.add_stride + n);
+        y.x += __uint_as_float(a.x << 16), y.y += __uint_as_float(a.x & 0xFFFF0000u);
+        y.z += __uint_as_float(a.y << 16), y.w += __uint_as_float(a.y & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint2*>((uint16_t*)p.out + t * p.out_stride + n) = make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w));
+    } else {
+      if (p.add) {
+        const float4 a = *reinterpret_cast<const float4*>((const float*)p.add + t * p.add_stride + n);
+        y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+      }
+      *reinterpret_cast<float4*>((float*)p.out + t * p.out_stride + n) = y;
+    }
+    return;
+  }
+  const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < p.N) {
+      float x = v[e];
+      if (OUT_BF16) {
+        if (p.add) x += bf16_f32(((const uint16_t*)p.add)[t * p.add_stride + n + e]);
+        ((uint16_t*)p.out)[t * p.out_stride + n + e] = (uint16_t)(bf16x2_rn(x, 0.f) & 0xFFFFu);
+      } else {
+        if (p.add) x += ((const float*)p.add)[t * p.add_stride + n + e];
+        ((float*)p.out)[t * p.out_stride + n + e] = x;
+      }
+    }
+}
+// Whether all groups of four of all rows of out and the addend are aligned.
+template <bool OUT_BF16>
+__device__ __forceinline__ bool wide_rows(const LinearParams& p) {
+  const uintptr_t size = OUT_BF16 ? 2 : 4;
+  const uintptr_t bits = (uintptr_t)p.out | (uintptr_t)(p.out_stride * size) | (p.add ? (uintptr_t)p.add | (uintptr_t)(p.add_stride * size) : 0);
+  return (bits & (4 * size - 1)) == 0;
+}
+
+// --------------------------------------------------------------------- clusters --
+// Small products, bound by the weights' bytes: a tile's inner size is cut among the
+// CTAs of a cluster, so that all SMs stream weights.  Each CTA owns some of the
+// tile's activation rows; the others send it their sums (one bulk copy between
+// shared memories each: remote stores and loads of single words took 4 cycles a
+// word), and it adds them in rank order.
 template <bool F4, bool OUT_BF16>
 __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const LinTile t,
                                                      const __grid_constant__ CUtensorMap wmap,
@@ -134,214 +437,288 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   using C = LinCfg<F4>;
   extern __shared__ uint8_t lin_dyn[];
   __shared__ LinShared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int cl = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  __shared__ __align__(16) uint32_t swap[2 * kSwapWords];
+  const int cl = (int)cluster_size(), rank = (int)cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_dyn) + 1023) & ~(uintptr_t)1023);
   const int n0 = (blockIdx.x / cl) * kRows, t0 = blockIdx.y * t.nt;
-  const int s0 = rank * t.per, s1 = min(s0 + t.per, t.slices);
-  const int ns = s1 > s0 ? s1 - s0 : 0;
-  if (warp == kMmaWarp) {
-    tmem_alloc(&sh.tmem_base, t.tmem_cols);
-    tmem_relinquish();
-  }
+  const int s0 = rank * t.per, ns = max(min(s0 + t.per, t.slices) - s0, 0);
+  // Rows of the tile that this CTA owns.
+  const int valid = min(t.nt, p.T - t0), own = (valid + cl - 1) / cl;
+  const int own0 = min(rank * own, valid), mine = min(own, valid - own0);
+  if (warp == kMmaWarp) lin_alloc<1>(&sh.tmem_base, t.tmem_cols);
   if (tid == 0) {
     for (int i = 0; i < t.stages; ++i) {
-      mbar_init(&sh.full[i], 1 + kSfWarps);
+      mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
-    mbar_init(&sh.done, 1);
+    for (int i = 0; i < kSfRing; ++i) {
+      mbar_init(&sh.sf_full[i], kSfWarps);
+      mbar_init(&sh.sf_empty[i], 1);
+    }
+    mbar_init(&sh.sums, 1);
+    mbar_init(&sh.recv, 1);
+    sh.abort_flag = 0;
+    mbar_init_fence();
+    if (cl > 1) mbar_arrive_expect_tx(&sh.recv, (uint32_t)((cl - 1) * mine * kRows * 4));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (cl > 1) cluster_arrive();
+  const uint32_t tmem = sh.tmem_base;
+  const LinCtx c = {&sh, p.status, p.wait_limit};
+  // Not before Tensor Memory is held: a CTA of the next kernel that took it would
+  // wait for this one to end.
+  pdl_trigger();
+  pdl_wait();
+
+  bool fine = false;
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      const uint32_t tx = (F4 ? kTileBytes : kTileBytes / 2) + (uint32_t)t.nt * 128;
+      Ring r;
+      for (int i = 0; i < ns; ++i, r.next(t.stages)) {
+        if (r.round > 0 && !lin_wait(c, &sh.empty[r.i], r.freed())) break;
+        uint8_t* sb = ring + (size_t)r.i * t.stage_bytes;
+        mbar_arrive_expect_tx(&sh.full[r.i], tx);
+        tma_load_2d(sb, &wmap, (s0 + i) * 128, n0, &sh.full[r.i]);
+        tma_load_2d(sb + kTileBytes, &xmap, (s0 + i) * 128, t0, &sh.full[r.i]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      Ring r, sf;
+      mmas_of_tile<F4, 1>(t, c, smem_u32(ring), tmem, ns, r, sf);
+      commit<1>(&sh.sums);
+      // Everything issued has finished before Tensor Memory is released.
+      if (!mbar_wait(&sh.sums, 0)) report(p.status);
+    }
+  } else {
+    Ring sf;
+    int step = 0;
+    bool ok = true;
+    scales_of_tile<1>(p, t, c, swap, tmem, n0, t0, s0 * C::kWords, (ns + C::kStep - 1) / C::kStep, sf, step, ok);
+    fine = lin_warp_wait(c, &sh.sums, 0) && ns > 0;
+    tc_fence_after();
+  }
+  __syncwarp();
+  if (cl > 1) cluster_wait();  // every CTA has started
+  if (warp >= kSfWarp0) {
+    // Sums to shared memory (the ring is free), an activation row's 128 in a row.
+    const int q = warp & 3, etid = tid - kSfWarp0 * 32;
+    const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+    float* stage = reinterpret_cast<float*>(ring);
+    float* recv = reinterpret_cast<float*>(ring + t.recv_off);
+    for (int c0 = 0; c0 < valid; c0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(tbase + (uint32_t)c0, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (c0 + e < valid) stage[(c0 + e) * kRows + q * 32 + lane] = fine ? __uint_as_float(v[e]) : 0.f;
+    }
+    tc_fence_before();
+    if (cl > 1) fence_async_smem();
+    named_sync(kSfBarrier, kSfWarps * 32);
+    if (cl > 1) {
+      if (etid < cl && etid != rank) {
+        const int o0 = min(etid * own, valid), n = min(own, valid - o0);
+        if (n > 0)
+          bulk_s2s(remote_smem(recv + (size_t)(rank < etid ? rank : rank - 1) * own * kRows, etid), stage + o0 * kRows,
+                   (uint32_t)(n * kRows * 4), remote_smem(&sh.recv, etid));
+      }
+      lin_warp_wait(c, &sh.recv, 0);
+    }
+    const bool wide = wide_rows<OUT_BF16>(p);
+    for (int i = etid; i < mine * (kRows / 4); i += kSfWarps * 32) {
+      const int tt = i / (kRows / 4), r4 = i % (kRows / 4) * 4;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < cl; ++j) {
+        const float* from = j == rank ? stage + (own0 + tt) * kRows : recv + ((size_t)(j < rank ? j : j - 1) * own + tt) * kRows;
+        const float4 a = *reinterpret_cast<const float4*>(from + r4);
+        y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+      }
+      put4<OUT_BF16>(p, t0 + own0 + tt, n0 + r4, y, wide);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  let_copies_land(sh);
+  __syncwarp();
+  if (cl > 1) {
+    cluster_arrive();
+    cluster_wait();  // no CTA leaves while its sums are being copied
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    lin_dealloc<1>(tmem, t.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------------ pairs --
+// Large products: a pair of CTAs on neighbouring SMs takes 256 weight rows by up to
+// 256 activation rows, one MMA for both (cta_group::2).  Each CTA holds its 128
+// weight rows and half of the activation rows in shared memory, and the sums of its
+// weight rows in its Tensor Memory, so that a byte from L2 or shared memory feeds up
+// to twice the products of a tile of one CTA.  Scales of all activation rows go to
+// both.  The first CTA's thread issues the MMAs of both; barriers of full stages, of
+// stored scales and of drained sums are the first CTA's, those of consumed stages and
+// finished sums are signalled in both.  Pairs walk the tiles in turn.
+constexpr int kPairEpWarp0 = kSfWarp0 + kSfWarps, kPairEpWarps = 8;
+constexpr int kPairThreads = (kPairEpWarp0 + kPairEpWarps) * 32;
+constexpr int kPairs = kNumSMs / 2;
+
+template <bool F4, bool OUT_BF16>
+__global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearParams p, const LinTile t,
+                                                                 const __grid_constant__ CUtensorMap wmap,
+                                                                 const __grid_constant__ CUtensorMap xmap) {
+  using C = LinCfg<F4>;
+  extern __shared__ uint8_t lin_dyn[];
+  __shared__ LinShared sh;
+  __shared__ __align__(16) uint32_t swap[2 * kSwapWords];
+  const int rank = (int)cluster_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_dyn) + 1023) & ~(uintptr_t)1023);
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  if (warp == kMmaWarp) lin_alloc<2>(&sh.tmem_base, t.tmem_cols);
+  if (tid == 0) {
+    for (int i = 0; i < t.stages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kSfRing; ++i) {
+      mbar_init(&sh.sf_full[i], 2 * kSfWarps);
+      mbar_init(&sh.sf_empty[i], 1);
+    }
+    mbar_init(&sh.sums, 1);
+    mbar_init(&sh.drained, 2 * kPairEpWarps);
     sh.abort_flag = 0;
     mbar_init_fence();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_arrive();
   const uint32_t tmem = sh.tmem_base;
-  LinCtx c = {&sh, p.status, p.wait_limit};
-  // Not before Tensor Memory is held: a CTA of the next kernel that took it would
-  // wait for this one to end.
+  const LinCtx c = {&sh, p.status, p.wait_limit};
+  cluster_wait();  // both CTAs' barriers are ready, both hold Tensor Memory
   pdl_trigger();
-  const uint32_t x_off = kTileBytes, sf_off = x_off + t.nt * 128;
   pdl_wait();
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      const uint32_t tx = (F4 ? kTileBytes : kTileBytes / 2) + (uint32_t)t.nt * 128;
-      for (int i = 0; i < ns; ++i) {
-        const int st = i % t.stages, use = i / t.stages;
-        if (use > 0 && !lin_wait(c, &sh.empty[st], (use - 1) & 1)) break;
-        uint8_t* sb = ring + (size_t)st * t.stage_bytes;
-        mbar_arrive_expect_tx(&sh.full[st], tx);
-        tma_load_2d(sb, &wmap, (s0 + i) * 128, n0, &sh.full[st]);
-        tma_load_2d(sb + x_off, &xmap, (s0 + i) * 128, t0, &sh.full[st]);
+      const uint32_t tx = (F4 ? kTileBytes : kTileBytes / 2) + (uint32_t)t.xrows * 128;
+      Ring r;
+      bool ok = true;
+      for (int tile = pair; tile < t.tiles && ok; tile += pairs) {
+        const int n0 = ((tile % t.tiles_n) * 2 + rank) * kRows, t0 = (tile / t.tiles_n) * t.nt + rank * t.xrows;
+        for (int i = 0; i < t.slices; ++i, r.next(t.stages)) {
+          ok = r.round == 0 || lin_wait(c, &sh.empty[r.i], r.freed());
+          if (!ok) break;
+          uint8_t* sb = ring + (size_t)r.i * t.stage_bytes;
+          // The first CTA's barrier counts both CTAs' bytes.
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[r.i], 2 * tx);
+          const uint32_t bar = remote_smem(&sh.full[r.i], 0);
+          tma_load_2d_pair(sb, &wmap, i * 128, n0, bar);
+          tma_load_2d_pair(sb + kTileBytes, &xmap, i * 128, t0, bar);
+        }
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      for (int i = 0; i < ns; ++i) {
-        const int st = i % t.stages;
-        if (!lin_wait(c, &sh.full[st], (i / t.stages) & 1)) break;
+    if (lane == 0 && rank == 0) {
+      Ring r, sf;
+      int ti = 0;
+      for (int tile = pair; tile < t.tiles; tile += pairs) {
+        if (ti > 0 && !lin_wait(c, &sh.drained, (ti - 1) & 1)) break;
         tc_fence_after();
-        const uint32_t sbase = smem_u32(ring + (size_t)st * t.stage_bytes);
-        const uint32_t sfa = tmem + (uint32_t)t.nt + (uint32_t)st * sf_cols<F4>(t.nt);
-        const uint32_t sfb = sfa + 4 * C::kWords;
-        const int nb = (t.nt + 127) / 128;
-#pragma unroll
-        for (int w = 0; w < C::kWords; ++w) {
-          tmem_cp_scales(sfa + 4 * w, sbase + sf_off + 512 * w);
-          for (int b = 0; b < nb; ++b)
-            tmem_cp_scales(sfb + 4 * (w * nb + b), sbase + sf_off + C::kSfBytes + 512 * (w * nb + b));
-        }
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          const uint64_t ad = sdesc_sw128(sbase + 32 * kb), bd = sdesc_sw128(sbase + x_off + 32 * kb);
-          const uint32_t acc = (i > 0 || kb > 0) ? 1u : 0u;
-          if (F4) {
-            const uint32_t id = 2 * (kb & 1);
-            umma_mxf4(tmem, ad, bd, idesc_mxf4(kRows, t.nt, id, id), sfa + 4 * (kb >> 1), sfb + 4 * nb * (kb >> 1), acc);
-          } else {
-            umma_mx(tmem, ad, bd, idesc_mx_f32(kRows, t.nt, kMxE2M1, kMxE4M3, kb, kb), sfa, sfb, acc);
-          }
-        }
-        umma_commit(&sh.empty[st]);
-      }
-      umma_commit(&sh.done);
-      // Everything issued has finished before Tensor Memory is released.
-      if (!mbar_wait(&sh.done, 0) && p.status) atomicCAS((unsigned*)p.status, 0u, (unsigned)MOE_ERR_TIMEOUT);
-    }
-  } else {
-    const int i = tid - kSfWarp0 * 32;  // weight row; activation rows i and i + 128
-    const int words = p.K / 128, w0 = s0 * C::kWords;
-    const int nb = (t.nt + 127) / 128;
-    auto row = [&](const uint8_t* base, int64_t stride, int at, int rows) {
-      ScaleRow s;
-      s.p = at < rows ? reinterpret_cast<const uint32_t*>(base + at * stride) + w0 : nullptr;
-      s.words = words - w0;
-      s.wide = (((uintptr_t)base | (uintptr_t)stride | (uintptr_t)(4 * w0)) & 15) == 0;
-      return s;
-    };
-    const ScaleRow rw = row(p.ws, p.ws_stride, n0 + i, p.N);
-    const ScaleRow rx0 = row(p.xs, p.xs_stride, t0 + i, i < t.nt ? p.T : 0);
-    const ScaleRow rx1 = row(p.xs, p.xs_stride, t0 + 128 + i, 128 + i < t.nt ? p.T : 0);
-    constexpr int PER = 4 / C::kWords;  // slices of a step of four words
-    uint4 vw = rw.load(0), va = rx0.load(0), vb = rx1.load(0);
-    bool ok = true;
-    for (int g = 0; g < ns && ok; g += PER) {
-      const int next = (g + PER) * C::kWords;
-      const bool more = g + PER < ns;
-      const uint4 nw = more ? rw.load(next) : vw, na = more ? rx0.load(next) : va, nbv = more && nb > 1 ? rx1.load(next) : vb;
-      const uint32_t a[4] = {vw.x, vw.y, vw.z, vw.w}, b0[4] = {va.x, va.y, va.z, va.w}, b1[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int sl = g + j;
-        if (sl >= ns) break;
-        const int st = sl % t.stages, use = sl / t.stages;
-        ok = use == 0 || lin_wait(c, &sh.empty[st], (use - 1) & 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        const bool ok = mmas_of_tile<F4, 2>(t, c, smem_u32(ring), tmem, t.slices, r, sf);
+        commit<2>(&sh.sums);
+        ++ti;
         if (!ok) break;
-        uint32_t* sf = reinterpret_cast<uint32_t*>(ring + (size_t)st * t.stage_bytes + sf_off) + (i & 31) * 4 + (i >> 5);
-#pragma unroll
-        for (int w = 0; w < C::kWords; ++w) {
-          sf[128 * w] = a[j * C::kWords + w];
-          sf[128 * (C::kWords + w * nb)] = b0[j * C::kWords + w];
-          if (nb > 1) sf[128 * (C::kWords + w * nb + 1)] = b1[j * C::kWords + w];
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[st]);
       }
-      vw = nw, va = na, vb = nbv;
+      // Everything issued has finished before Tensor Memory is released.
+      if (ti > 0 && !mbar_wait(&sh.sums, (ti - 1) & 1)) report(p.status);
     }
-    // The sums, by way of shared memory (the ring is free) where others add to
-    // them: token t's 128 in a row.
-    const int q = warp & 3;
-    const int valid = min(t.nt, p.T - t0);
-    const bool fine = __all_sync(0xFFFFFFFFu, lin_wait(c, &sh.done, 0));
-    tc_fence_after();
+  } else if (warp < kPairEpWarp0) {
+    Ring sf;
+    int step = 0;
+    bool ok = true;
+    for (int tile = pair; tile < t.tiles; tile += pairs)
+      scales_of_tile<2>(p, t, c, swap, tmem, ((tile % t.tiles_n) * 2 + rank) * kRows, (tile / t.tiles_n) * t.nt, 0,
+                        (t.slices + C::kStep - 1) / C::kStep, sf, step, ok);
+  } else {
+    const int q = warp & 3, part = (warp - kPairEpWarp0) >> 2;  // lanes 32 q ..; half of the columns
     const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
-    float* stage = reinterpret_cast<float*>(ring);
-    const int n = n0 + q * 32 + lane;
-    for (int c0 = 0; c0 < valid; c0 += 16) {
-      uint32_t v[16];
-      if (ns > 0 && fine) {
+    int ti = 0;
+    for (int tile = pair; tile < t.tiles; tile += pairs, ++ti) {
+      const int n = ((tile % t.tiles_n) * 2 + rank) * kRows + q * 32 + lane, t0 = (tile / t.tiles_n) * t.nt;
+      const int valid = min(t.nt, p.T - t0), e0 = part * t.xrows, e1 = min(valid, e0 + t.xrows);
+      if (!lin_warp_wait(c, &sh.sums, ti & 1)) break;
+      tc_fence_after();
+      for (int c0 = e0; c0 < e1; c0 += 16) {
+        uint32_t v[16];
         tmem_ld16(tbase + (uint32_t)c0, v);
         tmem_ld_wait();
-      } else {
+        if (n < p.N) {
+          const int64_t tt = t0 + c0;
+          if (OUT_BF16) {
+            uint16_t* o = (uint16_t*)p.out + tt * p.out_stride + n;
+            float a[16];
+            if (p.add) {
+              const uint16_t* ad = (const uint16_t*)p.add + tt * p.add_stride + n;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0u;
-      }
-      if (cl > 1) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (c0 + e < valid) stage[(c0 + e) * kRows + q * 32 + lane] = __uint_as_float(v[e]);
-      } else if (n < p.N) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (c0 + e < valid) {
-            const int64_t tt = t0 + c0 + e;
-            float y = __uint_as_float(v[e]);
-            if (OUT_BF16) {
-              if (p.add) y += bf16_f32(((const uint16_t*)p.add)[tt * p.add_stride + n]);
-              ((uint16_t*)p.out)[tt * p.out_stride + n] = (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu);
+              for (int e = 0; e < 16; ++e) a[e] = c0 + e < e1 ? bf16_f32(ad[e * p.add_stride]) : 0.f;
             } else {
-              if (p.add) y += ((const float*)p.add)[tt * p.add_stride + n];
-              ((float*)p.out)[tt * p.out_stride + n] = y;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[e] = 0.f;
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e < e1) o[e * p.out_stride] = (uint16_t)(bf16x2_rn(__uint_as_float(v[e]) + a[e], 0.f) & 0xFFFFu);
+          } else {
+            float* o = (float*)p.out + tt * p.out_stride + n;
+            float a[16];
+            if (p.add) {
+              const float* ad = (const float*)p.add + tt * p.add_stride + n;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[e] = c0 + e < e1 ? ad[e * p.add_stride] : 0.f;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) a[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e < e1) o[e * p.out_stride] = __uint_as_float(v[e]) + a[e];
           }
-      }
-    }
-    tc_fence_before();
-  }
-  if (cl > 1) {
-    cluster.sync();
-    // This CTA's share of the rows: kRows / cl of each token's.
-    const float* stage = reinterpret_cast<const float*>(ring);
-    const int valid = min(t.nt, p.T - t0), share = kRows / cl;
-    const float* from[kMaxCl];
-#pragma unroll
-    for (int j = 0; j < kMaxCl; ++j) from[j] = j < cl ? cluster.map_shared_rank(stage, j) : nullptr;
-    for (int i = tid; i < valid * share; i += kThreads) {
-      const int tt = i / share, rr = rank * share + i % share, n = n0 + rr;
-      float y = 0.f;
-#pragma unroll
-      for (int j = 0; j < kMaxCl; ++j)
-        if (j < cl) y += from[j][tt * kRows + rr];
-      if (n < p.N) {
-        const int64_t at = t0 + tt;
-        if (OUT_BF16) {
-          if (p.add) y += bf16_f32(((const uint16_t*)p.add)[at * p.add_stride + n]);
-          ((uint16_t*)p.out)[at * p.out_stride + n] = (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu);
-        } else {
-          if (p.add) y += ((const float*)p.add)[at * p.add_stride + n];
-          ((float*)p.out)[at * p.out_stride + n] = y;
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(remote_smem(&sh.drained, 0));
     }
-    cluster.sync();  // no CTA leaves while its sums are read
   }
   tc_fence_before();
   __syncthreads();
-  if (sh.abort_flag) {
-    // A wait gave up: copies may be in flight, and have to land before the CTA may
-    // exit.  Their barriers miss other arrivals, so a time is waited that covers any.
-    const long long w0 = clock64();
-    while (clock64() - w0 < 20000000) __nanosleep(1000);
-  }
+  let_copies_land(sh);
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();  // neither CTA leaves while the other may reach its shared memory
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, t.tmem_cols);
+    lin_dealloc<2>(tmem, t.tmem_cols);
   }
 }
 
-// Tensor map of an operand: rows of `row_bytes` bytes of codes, boxes of 128 bytes
-// of shared memory by `rows` rows, 128-byte swizzle.  spread: 4-bit codes that take
-// a byte each in shared memory.  Rows and columns past the end read as zero.
+// ----------------------------------------------------------------------- launch --
+// Tensor map of an operand: rows of codes, boxes of 128 bytes of shared memory by
+// `rows` rows, 128-byte swizzle.  spread: 4-bit codes that take a byte each in
+// shared memory.  Rows and columns past the end read as zero.
 cudaError_t operand_map(CUtensorMap* m, const moe_mx& a, bool spread, int rows) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t row_elems = spread ? a.cols : (a.type == MOE_MX_E4M3 ? a.cols : a.cols / 2);
-  const cuuint64_t dims[2] = {row_elems, (cuuint64_t)a.rows};
+  const cuuint64_t width = spread || a.type == MOE_MX_E4M3 ? a.cols : a.cols / 2;
+  const cuuint64_t dims[2] = {width, (cuuint64_t)a.rows};
   const cuuint64_t strides[1] = {(cuuint64_t)a.q_stride};
   const cuuint32_t box[2] = {128, (cuuint32_t)rows};
   const cuuint32_t step[2] = {1, 1};
@@ -351,44 +728,89 @@ cudaError_t operand_map(CUtensorMap* m, const moe_mx& a, bool spread, int rows) 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool F4, bool OUT_BF16>
-cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cudaStream_t s) {
-  LinTile t;
-  const int tiles_t = (p.T + kMaxNt - 1) / kMaxNt;
-  t.nt = ((p.T + tiles_t - 1) / tiles_t + 15) & ~15;
-  t.slices = (p.K + (F4 ? 255 : 127)) / (F4 ? 256 : 128);
-  const int tiles_n = (p.N + kRows - 1) / kRows;
-  // CTAs of a tile: while all run at once and each has four slices.
-  int cl = 1;
-  while (cl < kMaxCl && (long long)tiles_n * tiles_t * cl * 2 <= kNumSMs && t.slices >= 8 * cl) cl *= 2;
-  t.per = (t.slices + cl - 1) / cl;
-  t.stage_bytes = (uint32_t)align_up(kTileBytes + t.nt * 128 + sf_bytes<F4>(t.nt), 1024);
-  t.stages = (int)(220 * 1024 / t.stage_bytes);
-  if (t.stages > kMaxStages) t.stages = kMaxStages;
-  const uint32_t cols = t.nt + t.stages * sf_cols<F4>(t.nt);
-  t.tmem_cols = 32;
-  while (t.tmem_cols < cols) t.tmem_cols *= 2;
-  const size_t smem = (size_t)t.stages * t.stage_bytes + 1024;
+template <typename Kernel>
+cudaError_t start(Kernel kern, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t s, const LinearParams& p,
+                  const LinTile& t, const moe_mx& x, const moe_mx& w) {
   CUtensorMap wmap, xmap;
   cudaError_t err;
-  if ((err = operand_map(&wmap, w, !F4, kRows)) != cudaSuccess || (err = operand_map(&xmap, x, false, t.nt)) != cudaSuccess)
+  if ((err = operand_map(&wmap, w, x.type == MOE_MX_E4M3, kRows)) != cudaSuccess ||
+      (err = operand_map(&xmap, x, false, t.xrows)) != cudaSuccess ||
+      (err = ensure_smem_attr((const void*)kern, smem)) != cudaSuccess)
     return err;
-  auto kern = k_linear<F4, OUT_BF16>;
-  if ((err = ensure_smem_attr((const void*)kern, smem)) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles_n * cl), (unsigned)tiles_t);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p, t, wmap, xmap);
+}
+
+int up(int a, int b) { return (a + b - 1) / b; }
+
+template <bool F4, bool OUT_BF16>
+cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cudaStream_t s) {
+  LinTile t = {};
+  const int tiles_t = up(p.T, kMaxNt);
+  const size_t most = (size_t)214 * 1024;  // dynamic shared memory, beside 13 KB of static
+  t.slices = up(p.K, F4 ? 256 : 128);
+  auto shape = [&](int granule, int share) {
+    t.nt = up(up(p.T, tiles_t), granule) * granule;
+    t.xrows = t.nt / share;
+    t.nb = up(t.nt, 128);
+    t.stage_bytes = (uint32_t)(kTileBytes + t.xrows * 128);  // xrows a multiple of 16: 1024-byte atoms stay whole
+  };
+  auto columns = [&] {
+    t.sf_col = (uint32_t)t.nt;
+    const uint32_t cols = t.nt + kSfRing * 16 * (1 + t.nb);
+    t.tmem_cols = 32;
+    while (t.tmem_cols < cols) t.tmem_cols *= 2;
+  };
+  // Pairs where their tiles take most of the SMs.
+  if ((long long)up(p.N, 2 * kRows) * tiles_t >= kPairs * 3 / 4) {
+    shape(32, 2);
+    columns();
+    t.tmem_cols = 512;
+    t.per = t.slices;
+    t.tiles_n = up(p.N, 2 * kRows);
+    t.tiles = t.tiles_n * tiles_t;
+    t.stages = (int)((most - 1024) / t.stage_bytes);
+    if (t.stages > kMaxStages) t.stages = kMaxStages;
+    return start(k_linear_pair<F4, OUT_BF16>, dim3((unsigned)(2 * (t.tiles < kPairs ? t.tiles : kPairs))), kPairThreads, 2,
+                 (size_t)t.stages * t.stage_bytes + 1024, s, p, t, x, w);
+  }
+  shape(16, 1);
+  columns();
+  t.tiles_n = up(p.N, kRows);
+  const long long tiles = (long long)t.tiles_n * tiles_t;
+  t.tiles = (int)tiles;
+  // CTAs of a tile: while all run at once (two an SM) and each has four slices.
+  const int valid = p.T < t.nt ? p.T : t.nt;
+  const size_t sums = align_up((size_t)valid * kRows * 4, 1024);
+  auto recv = [&](int c) { return c > 1 ? (size_t)(c - 1) * up(valid, c) * kRows * 4 : 0; };
+  auto ring = [&](int n) { return (size_t)n * t.stage_bytes > sums ? (size_t)n * t.stage_bytes : sums; };
+  int cl = 1;
+  while (cl < kMaxCl && tiles * cl * 2 <= 2 * kNumSMs && t.slices >= 8 * cl && recv(2 * cl) + ring(3) + 1024 <= most) cl *= 2;
+  t.per = up(t.slices, cl);
+  // Two CTAs an SM where there are more than SMs and two rings of three stages fit;
+  // Tensor Memory goes by shared memory, half each.
+  const size_t half = (size_t)98 * 1024;
+  const bool two = tiles * cl > kNumSMs && recv(cl) + ring(3) + 1024 <= half && t.tmem_cols <= 256;
+  t.stages = (int)(((two ? half : most) - recv(cl) - 1024) / t.stage_bytes);
+  if (t.stages > kMaxStages) t.stages = kMaxStages;
+  t.recv_off = (uint32_t)ring(t.stages);
+  // No third CTA (or second) may share the SM and wait for Tensor Memory.
+  size_t smem = t.recv_off + recv(cl) + 1024;
+  const size_t least = two ? half : (size_t)110 * 1024;
+  if (smem < least) smem = least;
+  return start(k_linear<F4, OUT_BF16>, dim3((unsigned)(t.tiles_n * cl), (unsigned)tiles_t), kThreads, cl, smem, s, p, t, x, w);
 }
 
 }  // namespace
