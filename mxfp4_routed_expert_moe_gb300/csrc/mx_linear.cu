@@ -218,35 +218,47 @@ struct LinCfg {
   static constexpr int kStep = 4 / kWords;        // slices of a step of scales
 };
 
-// Scale words of one row: 16 bytes (four words) a step; past the end, and rows past
-// the end, scale 1.
+// Scale words of one row, four a step; past the end, and in rows past the end, scale
+// 1.  WIDE: by 16-byte loads (aligned rows of a multiple of four words).  Predicated
+// loads into the registers that keep the words: with branches the compiler moves
+// them there where paths join, and waits for each load on the spot (0.3 us a slice).
+template <bool WIDE>
 struct ScaleRow {
   const uint32_t* p;
   int words;
-  bool wide;
   __device__ __forceinline__ ScaleRow(const uint8_t* base, int64_t stride, int row, int rows, int w0, int count)
-      : p(row < rows ? reinterpret_cast<const uint32_t*>(base + row * stride) + w0 : nullptr),
-        words(count - w0),
-        wide((((uintptr_t)base | (uintptr_t)stride | (uintptr_t)(4 * w0)) & 15) == 0) {}
-  __device__ __forceinline__ uint4 load(int w) const {
-    const uint32_t one = 0x7F7F7F7Fu;
-    uint4 v = make_uint4(one, one, one, one);
-    if (!p || w >= words) return v;
-    if (wide && w + 4 <= words) return __ldg(reinterpret_cast<const uint4*>(p + w));
-    v.x = __ldg(p + w);
-    if (w + 1 < words) v.y = __ldg(p + w + 1);
-    if (w + 2 < words) v.z = __ldg(p + w + 2);
-    if (w + 3 < words) v.w = __ldg(p + w + 3);
-    return v;
+      : p(reinterpret_cast<const uint32_t*>(base + (row < rows ? row : 0) * stride) + w0), words(row < rows ? count - w0 : 0) {}
+  __device__ __forceinline__ void load(uint4& v, int w) const {
+    constexpr uint32_t one = 0x7F7F7F7Fu;
+    if (WIDE) {
+      asm volatile(
+          "{\n .reg .pred q;\n setp.lt.s32 q, %5, %6;\n mov.b32 %0, %7;\n mov.b32 %1, %7;\n mov.b32 %2, %7;\n mov.b32 %3, %7;\n"
+          " @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+          : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+          : "l"(p + w), "r"(w), "r"(words), "n"(one));
+    } else {
+      asm volatile(
+          "{\n .reg .pred q0, q1, q2, q3;\n setp.lt.s32 q0, %5, %6;\n setp.lt.s32 q1, %7, %6;\n setp.lt.s32 q2, %8, %6;\n"
+          " setp.lt.s32 q3, %9, %6;\n mov.b32 %0, %10;\n mov.b32 %1, %10;\n mov.b32 %2, %10;\n mov.b32 %3, %10;\n"
+          " @q0 ld.global.nc.u32 %0, [%4];\n @q1 ld.global.nc.u32 %1, [%4 + 4];\n @q2 ld.global.nc.u32 %2, [%4 + 8];\n"
+          " @q3 ld.global.nc.u32 %3, [%4 + 12];\n}"
+          : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+          : "l"(p + w), "r"(w), "r"(words), "r"(w + 1), "r"(w + 2), "r"(w + 3), "n"(one));
+    }
   }
 };
+// Whether all scale rows of both operands, from word w0 on, take 16-byte loads.
+__device__ __forceinline__ bool wide_scales(const LinearParams& p, int w0) {
+  return (((uintptr_t)p.ws | (uintptr_t)p.xs | (uintptr_t)p.ws_stride | (uintptr_t)p.xs_stride | (uintptr_t)(4 * w0) |
+           (uintptr_t)(p.K / 32)) & 15) == 0;
+}
 
 // One tile's scales by the four scale warps: `steps` steps of words from w0 on, of
 // weight rows n0.. and activation rows t0...  ok turns false where a wait gave up;
 // the steps are walked all the same, since the warps meet at each.
 constexpr int kSfAhead = 4;  // steps in flight: more than HBM's latency
 constexpr uint32_t kSwapWords = 4 * 3 * kRows;  // of one exchange buffer (there are two)
-template <int G, int WARP0>
+template <int G, int WARP0, bool WIDE>
 __device__ __forceinline__ void scales_of_tile(const LinearParams& p, const LinTile& t, const LinCtx& c, uint32_t* swap,
                                                uint32_t tmem, int n0, int t0, int w0, int steps, Ring& ring, int& step,
                                                bool& ok) {
@@ -254,16 +266,16 @@ __device__ __forceinline__ void scales_of_tile(const LinearParams& p, const LinT
   // Thread tid reads row tid / 4 + 32 (tid % 4) of each block: the word's place
   // among the blocks of four is tid.
   const int r = (tid >> 2) + 32 * (tid & 3), words = p.K / 128;
-  const ScaleRow rw(p.ws, p.ws_stride, n0 + r, p.N, w0, words);
-  const ScaleRow rx0(p.xs, p.xs_stride, t0 + r, r < t.nt ? p.T : 0, w0, words);
-  const ScaleRow rx1(p.xs, p.xs_stride, t0 + 128 + r, 128 + r < t.nt ? p.T : 0, w0, words);
+  const ScaleRow<WIDE> rw(p.ws, p.ws_stride, n0 + r, p.N, w0, words);
+  const ScaleRow<WIDE> rx0(p.xs, p.xs_stride, t0 + r, r < t.nt ? p.T : 0, w0, words);
+  const ScaleRow<WIDE> rx1(p.xs, p.xs_stride, t0 + 128 + r, 128 + r < t.nt ? p.T : 0, w0, words);
   const int nb = t.nb, blocks = 1 + nb;
   uint4 vw[kSfAhead], va[kSfAhead], vb[kSfAhead];
 #pragma unroll
   for (int d = 0; d < kSfAhead; ++d) {
-    vw[d] = rw.load(4 * d);
-    va[d] = rx0.load(4 * d);
-    vb[d] = nb > 1 ? rx1.load(4 * d) : va[d];
+    rw.load(vw[d], 4 * d);
+    rx0.load(va[d], 4 * d);
+    rx1.load(vb[d], 4 * d);
   }
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + t.sf_col;
   for (int g0 = 0; g0 < steps; g0 += kSfAhead) {
@@ -281,12 +293,11 @@ __device__ __forceinline__ void scales_of_tile(const LinearParams& p, const LinT
       }
       // Everyone has read the other buffer, too, before it is written again.
       named_sync(kSfBarrier, kSfWarps * 32);
-      if (g0 + d + kSfAhead < steps) {
-        const int w = 4 * (g0 + d + kSfAhead);
-        vw[d] = rw.load(w);
-        va[d] = rx0.load(w);
-        if (nb > 1) vb[d] = rx1.load(w);
-      }
+      // (Words of another CTA's part are read in vain at the end.)
+      const int w = 4 * (g0 + d + kSfAhead);
+      rw.load(vw[d], w);
+      rx0.load(va[d], w);
+      rx1.load(vb[d], w);
       if (ok && ring.round > 0) ok = lin_warp_wait(c, &c.sh->sf_empty[ring.i], ring.freed());
       if (!ok) {
         ++step;
@@ -517,7 +528,11 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
     Ring sf;
     int step = 0;
     bool ok = true;
-    scales_of_tile<1, kSfWarp0>(p, t, c, swap, tmem, n0, t0, s0 * C::kWords, (ns + C::kStep - 1) / C::kStep, sf, step, ok);
+    const int w0 = s0 * C::kWords, steps = (ns + C::kStep - 1) / C::kStep;
+    if (wide_scales(p, w0))
+      scales_of_tile<1, kSfWarp0, true>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
+    else
+      scales_of_tile<1, kSfWarp0, false>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
     fine = lin_warp_wait(c, &sh.sums, 0) && ns > 0;
     tc_fence_after();
   }
@@ -677,9 +692,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
     Ring sf;
     int step = 0;
     bool ok = true;
-    for (int tile = pair; tile < t.tiles; tile += pairs)
-      scales_of_tile<2, kPairSfWarp0>(p, t, c, swap, tmem, ((tile % t.tiles_n) * 2 + rank) * kRows, (tile / t.tiles_n) * t.nt, 0,
-                        (t.slices + C::kStep - 1) / C::kStep, sf, step, ok);
+    const int steps = (t.slices + C::kStep - 1) / C::kStep;
+    const bool wide = wide_scales(p, 0);
+    for (int tile = pair; tile < t.tiles; tile += pairs) {
+      const int n0 = ((tile % t.tiles_n) * 2 + rank) * kRows, t0 = (tile / t.tiles_n) * t.nt;
+      if (wide)
+        scales_of_tile<2, kPairSfWarp0, true>(p, t, c, swap, tmem, n0, t0, 0, steps, sf, step, ok);
+      else
+        scales_of_tile<2, kPairSfWarp0, false>(p, t, c, swap, tmem, n0, t0, 0, steps, sf, step, ok);
+    }
   } else {
     regs_inc<kRegsEpilogue>();
     const int q = warp & 3, part = (warp - kPairEpWarp0) >> 2;  // lanes 32 q ..; half of the columns
