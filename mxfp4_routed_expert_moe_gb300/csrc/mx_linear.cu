@@ -46,46 +46,71 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t a_sf, u
 }
 
 // ------------------------------------------- instructions of one CTA or a pair --
-// G = 1: one CTA's tile; G = 2: a pair's, issued by its first CTA for both.
+// G = 1: one CTA's tile; G = 2: a pair's, issued by its first CTA for both.  The
+// whole warp runs the issuing code with a predicate (`one`) that is true in one lane:
+// in a divergent branch every operand goes through a vector-to-uniform move of its
+// own (an MMA took 90 cycles).  Descriptors of operands are given by their low words.
+//
+// High words: stride offset 1024 bytes, fixed bit, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
+  return r;
+}
 template <int G>
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                       uint32_t acc) {
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, bool acc,
+                                       uint32_t one) {
   if (G == 1)
-    umma_mx(d, a, b, idesc, sfa, sfb, acc);
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n mov.b64 da, {%1, %8};\n"
+        " mov.b64 db, {%2, %8};\n"
+        " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)acc), "r"(one), "n"(kDescHigh)
+        : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n mov.b64 da, {%1, %8};\n"
+        " mov.b64 db, {%2, %8};\n"
+        " @e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)acc), "r"(one), "n"(kDescHigh)
         : "memory");
 }
 template <int G>
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t acc) {
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, bool acc,
+                                         uint32_t one) {
   if (G == 1)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n mov.b64 da, {%1, %8};\n"
+        " mov.b64 db, {%2, %8};\n"
+        " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)acc), "r"(one), "n"(kDescHigh)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n mov.b64 da, {%1, %8};\n"
+        " mov.b64 db, {%2, %8};\n"
+        " @e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)acc), "r"(one), "n"(kDescHigh)
         : "memory");
 }
-// Arrive on the barrier (of both CTAs of a pair) when all that this thread issued
-// has completed.
+// Arrive on the barrier (of both CTAs of a pair) when all that the elected lane
+// issued has completed.
 template <int G>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
   if (G == 1)
-    umma_commit(bar);
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
   else
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)3), "r"(one)
         : "memory");
 }
 template <int G>
@@ -331,38 +356,35 @@ __device__ __forceinline__ void scales_of_tile(const LinearParams& p, const LinT
   }
 }
 
-// One tile's MMAs, `count` slices, by one thread.
+// One tile's MMAs, `count` slices, by one warp.
 template <bool F4, int G>
 __device__ __forceinline__ bool mmas_of_tile(const LinTile& t, const LinCtx& c, uint32_t ring0, uint32_t tmem, int count,
-                                             Ring& ring, Ring& sf) {
+                                             Ring& ring, Ring& sf, uint32_t one) {
   using C = LinCfg<F4>;
-  const int blocks = 1 + t.nb;
+  const uint32_t blocks4 = 4 * (1 + t.nb);
   const uint32_t id0 = F4 ? idesc_mxf4(G * kRows, t.nt, 0, 0) : idesc_mx_f32(G * kRows, t.nt, kMxE2M1, kMxE4M3, 0, 0);
-  uint32_t acc = 0u;
   for (int s0 = 0; s0 < count; s0 += C::kStep) {
-    if (!lin_wait(c, &c.sh->sf_full[sf.i], sf.filled())) return false;
-    const uint32_t col = tmem + t.sf_col + (uint32_t)(sf.i * 16 * blocks);
+    if (!lin_warp_wait(c, &c.sh->sf_full[sf.i], sf.filled())) return false;
+    const uint32_t col = tmem + t.sf_col + (uint32_t)sf.i * 4 * blocks4;
 #pragma unroll
     for (int j = 0; j < C::kStep; ++j) {
       if (s0 + j >= count) break;
-      if (!lin_wait(c, &c.sh->full[ring.i], ring.filled())) return false;
+      if (!lin_warp_wait(c, &c.sh->full[ring.i], ring.filled())) return false;
       tc_fence_after();
-      const uint32_t sb = ring0 + (uint32_t)ring.i * t.stage_bytes;
+      const uint32_t a0 = desc_low(ring0 + (uint32_t)ring.i * t.stage_bytes), b0 = a0 + (kTileBytes >> 4);
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        const uint64_t ad = sdesc_sw128(sb + 32 * kb), bd = sdesc_sw128(sb + kTileBytes + 32 * kb);
         const uint32_t w = F4 ? 2 * j + (kb >> 1) : j, id = F4 ? 2 * (kb & 1) : kb;
-        const uint32_t sfa = col + 4 * blocks * w, idesc = id0 | (id << 4) | (id << 29);
+        const uint32_t sfa = col + blocks4 * w, idesc = id0 | (id << 4) | (id << 29);
         if (F4)
-          mma_mxf4<G>(tmem, ad, bd, idesc, sfa, sfa + 4, acc);
+          mma_mxf4<G>(tmem, a0 + 2 * kb, b0 + 2 * kb, idesc, sfa, sfa + 4, s0 + j > 0 || kb > 0, one);
         else
-          mma_mx<G>(tmem, ad, bd, idesc, sfa, sfa + 4, acc);
-        acc = 1u;
+          mma_mx<G>(tmem, a0 + 2 * kb, b0 + 2 * kb, idesc, sfa, sfa + 4, s0 + j > 0 || kb > 0, one);
       }
-      commit<G>(&c.sh->empty[ring.i]);
+      commit<G>(&c.sh->empty[ring.i], one);
       ring.next(t.stages);
     }
-    commit<G>(&c.sh->sf_empty[sf.i]);
+    commit<G>(&c.sh->sf_empty[sf.i], one);
     sf.next(kSfRing);
   }
   return true;
@@ -378,39 +400,43 @@ __device__ __forceinline__ void let_copies_land(const LinShared& sh) {
   }
 }
 
-// Four neighbouring results of a row from n on.
+// Four neighbouring addends, or results, of a row from n on.
 template <bool OUT_BF16>
-__device__ __forceinline__ void put4(const LinearParams& p, int64_t t, int n, float4 y, bool wide) {
-  if (n >= p.N) return;
+__device__ __forceinline__ float4 get4(const LinearParams& p, int64_t t, int n, bool wide) {
   if (wide && n + 4 <= p.N) {
     if (OUT_BF16) {
-      if (p.add) {
-        const uint2 a = *reinterpret_cast<const uint2*>((const uint16_t*)p.add + t * p.add_stride + n);
-        y.x += __uint_as_float(a.x << 16), y.y += __uint_as_float(a.x & 0xFFFF0000u);
-        y.z += __uint_as_float(a.y << 16), y.w += __uint_as_float(a.y & 0xFFFF0000u);
-      }
-      *reinterpret_cast<uint2*>((uint16_t*)p.out + t * p.out_stride + n) = make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w));
-    } else {
-      if (p.add) {
-        const float4 a = *reinterpret_cast<const float4*>((const float*)p.add + t * p.add_stride + n);
-        y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
-      }
-      *reinterpret_cast<float4*>((float*)p.out + t * p.out_stride + n) = y;
+      const uint2 a = *reinterpret_cast<const uint2*>((const uint16_t*)p.add + t * p.add_stride + n);
+      return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                         __uint_as_float(a.y & 0xFFFF0000u));
     }
+    return *reinterpret_cast<const float4*>((const float*)p.add + t * p.add_stride + n);
+  }
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = 0.f;
+    if (n + e < p.N)
+      v[e] = OUT_BF16 ? bf16_f32(((const uint16_t*)p.add)[t * p.add_stride + n + e]) : ((const float*)p.add)[t * p.add_stride + n + e];
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+template <bool OUT_BF16>
+__device__ __forceinline__ void put4(const LinearParams& p, int64_t t, int n, float4 y, bool wide) {
+  if (wide && n + 4 <= p.N) {
+    if (OUT_BF16)
+      *reinterpret_cast<uint2*>((uint16_t*)p.out + t * p.out_stride + n) = make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w));
+    else
+      *reinterpret_cast<float4*>((float*)p.out + t * p.out_stride + n) = y;
     return;
   }
   const float v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (n + e < p.N) {
-      float x = v[e];
-      if (OUT_BF16) {
-        if (p.add) x += bf16_f32(((const uint16_t*)p.add)[t * p.add_stride + n + e]);
-        ((uint16_t*)p.out)[t * p.out_stride + n + e] = (uint16_t)(bf16x2_rn(x, 0.f) & 0xFFFFu);
-      } else {
-        if (p.add) x += ((const float*)p.add)[t * p.add_stride + n + e];
-        ((float*)p.out)[t * p.out_stride + n + e] = x;
-      }
+      if (OUT_BF16)
+        ((uint16_t*)p.out)[t * p.out_stride + n + e] = (uint16_t)(bf16x2_rn(v[e], 0.f) & 0xFFFFu);
+      else
+        ((float*)p.out)[t * p.out_stride + n + e] = v[e];
     }
 }
 // One column's results of up to 32 rows from row t on.
@@ -503,6 +529,20 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   pdl_trigger();
   pdl_wait();
 
+  // Results in fours, kUnits a thread at a time; their addends are read before the
+  // sums are waited for, and all before the first store, which may be to the same place.
+  constexpr int kUnits = 4;
+  const int units = mine * (kRows / 4);
+  const bool wide = wide_rows<OUT_BF16>(p);
+  float4 add[kUnits];
+  auto addends = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const int i = i0 + k * kSfWarps * 32;
+      add[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.add && i < units) add[k] = get4<OUT_BF16>(p, t0 + own0 + i / (kRows / 4), n0 + i % (kRows / 4) * 4, wide);
+    }
+  };
   bool fine = false;
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -517,13 +557,12 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      Ring r, sf;
-      mmas_of_tile<F4, 1>(t, c, smem_u32(ring), tmem, ns, r, sf);
-      commit<1>(&sh.sums);
-      // Everything issued has finished before Tensor Memory is released.
-      if (!mbar_wait(&sh.sums, 0)) report(p.status);
-    }
+    Ring r, sf;
+    const uint32_t one = elect_one();  // commits track the elected lane's MMAs
+    mmas_of_tile<F4, 1>(t, c, smem_u32(ring), tmem, ns, r, sf, one);
+    commit<1>(&sh.sums, one);
+    // Everything issued has finished before Tensor Memory is released.
+    if (!mbar_wait(&sh.sums, 0)) report(p.status);
   } else {
     Ring sf;
     int step = 0;
@@ -533,6 +572,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       scales_of_tile<1, kSfWarp0, true>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
     else
       scales_of_tile<1, kSfWarp0, false>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
+    addends(tid - kSfWarp0 * 32);
     fine = lin_warp_wait(c, &sh.sums, 0) && ns > 0;
     tc_fence_after();
   }
@@ -564,16 +604,22 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       }
       lin_warp_wait(c, &sh.recv, 0);
     }
-    const bool wide = wide_rows<OUT_BF16>(p);
-    for (int i = etid; i < mine * (kRows / 4); i += kSfWarps * 32) {
-      const int tt = i / (kRows / 4), r4 = i % (kRows / 4) * 4;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j = 0; j < cl; ++j) {
-        const float* from = j == rank ? stage + (own0 + tt) * kRows : recv + ((size_t)(j < rank ? j : j - 1) * own + tt) * kRows;
-        const float4 a = *reinterpret_cast<const float4*>(from + r4);
-        y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+    for (int i0 = etid; i0 < units; i0 += kUnits * kSfWarps * 32) {
+      if (i0 != etid) addends(i0);
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        const int i = i0 + k * kSfWarps * 32;
+        if (i >= units) break;
+        const int tt = i / (kRows / 4), r4 = i % (kRows / 4) * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < cl; ++j) {
+          const float* from = j == rank ? stage + (own0 + tt) * kRows : recv + ((size_t)(j < rank ? j : j - 1) * own + tt) * kRows;
+          const float4 a = *reinterpret_cast<const float4*>(from + r4);
+          y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+        }
+        y.x += add[k].x, y.y += add[k].y, y.z += add[k].z, y.w += add[k].w;
+        put4<OUT_BF16>(p, t0 + own0 + tt, n0 + r4, y, wide);
       }
-      put4<OUT_BF16>(p, t0 + own0 + tt, n0 + r4, y, wide);
     }
   }
   tc_fence_before();
@@ -673,14 +719,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
         }
       }
     }
-    if (warp == kMmaWarp && lane == 0 && rank == 0) {
+    if (warp == kMmaWarp && rank == 0) {
       Ring r, sf;
+      const uint32_t one = elect_one();
       int ti = 0;
       for (int tile = pair; tile < t.tiles; tile += pairs) {
-        if (ti > 0 && !lin_wait(c, &sh.drained, (ti - 1) & 1)) break;
+        if (ti > 0 && !lin_warp_wait(c, &sh.drained, (ti - 1) & 1)) break;
         tc_fence_after();
-        const bool ok = mmas_of_tile<F4, 2>(t, c, smem_u32(ring), tmem, t.slices, r, sf);
-        commit<2>(&sh.sums);
+        const bool ok = mmas_of_tile<F4, 2>(t, c, smem_u32(ring), tmem, t.slices, r, sf, one);
+        commit<2>(&sh.sums, one);
         ++ti;
         if (!ok) break;
       }
@@ -785,57 +832,68 @@ int up(int a, int b) { return (a + b - 1) / b; }
 template <bool F4, bool OUT_BF16>
 cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cudaStream_t s) {
   LinTile t = {};
-  const int tiles_t = up(p.T, kMaxNt);
   const size_t most = (size_t)214 * 1024;  // dynamic shared memory, beside 13 KB of static
   t.slices = up(p.K, F4 ? 256 : 128);
-  auto shape = [&](int granule, int share) {
+  auto shape = [&](int nt, int granule, int share) {
+    const int tiles_t = up(p.T, nt);
     t.nt = up(up(p.T, tiles_t), granule) * granule;
-    t.xrows = t.nt / share;
+    t.xrows = t.nt / share;  // a multiple of 16: the operand's 1024-byte atoms stay whole
     t.nb = up(t.nt, 128);
-    t.stage_bytes = (uint32_t)(kTileBytes + t.xrows * 128);  // xrows a multiple of 16: 1024-byte atoms stay whole
-  };
-  auto columns = [&] {
+    t.stage_bytes = (uint32_t)(kTileBytes + t.xrows * 128);
     t.sf_col = (uint32_t)t.nt;
-    const uint32_t cols = t.nt + kSfRing * 16 * (1 + t.nb);
     t.tmem_cols = 32;
-    while (t.tmem_cols < cols) t.tmem_cols *= 2;
+    while (t.tmem_cols < t.nt + (uint32_t)(kSfRing * 16 * (1 + t.nb))) t.tmem_cols *= 2;
+    return tiles_t;
   };
-  // Pairs where their tiles take most of the SMs.
-  if ((long long)up(p.N, 2 * kRows) * tiles_t >= kPairs * 3 / 4) {
-    shape(32, 2);
-    columns();
+  // Clusters where the inner size can be cut in two or more with all CTAs on the chip
+  // at once, in tiles of up to 64 activation rows; pairs otherwise, in the smallest
+  // tiles that still make one round of the chip.  Measured, inner size 7,168, MXFP8
+  // activations (us, clusters / pairs): 1 and 16 x 9,216: 9.7 / -, 10.3 / 16.5; 64 x
+  // 7,168: 12.5 / 16.4; 64 x 16,384 (no room for a cut): 21.0 / 17.9; 128 x 9,216:
+  // 18.5 / 17.4; 256 x 1,408: 11.3 / 25; 256 x 9,216: 26.4 / 19.5 (tiles of 128;
+  // 23.3 of 256).  MXFP4 activations: 64 x 9,216: 11.7 / 10.8; 256 x 7,168: 19.8 / 12.7.
+  const int rows = up(p.N, kRows), pair_rows = up(p.N, 2 * kRows);
+  const long long tiles = (long long)rows * up(p.T, 64);
+  if (2 * tiles > kNumSMs) {
+    int nt = 32;
+    while (nt < kMaxNt && (long long)pair_rows * up(p.T, nt) > kPairs) nt *= 2;
+    const int tiles_t = shape(nt, 32, 2);
     t.tmem_cols = 512;
     t.per = t.slices;
-    t.tiles_n = up(p.N, 2 * kRows);
-    t.tiles = t.tiles_n * tiles_t;
+    t.tiles_n = pair_rows;
+    t.tiles = pair_rows * tiles_t;
     t.stages = (int)((most - 1024) / t.stage_bytes);
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     return start(k_linear_pair<F4, OUT_BF16>, dim3((unsigned)(2 * (t.tiles < kPairs ? t.tiles : kPairs))), kPairThreads, 2,
                  (size_t)t.stages * t.stage_bytes + 1024, s, p, t, x, w);
   }
-  shape(16, 1);
-  columns();
-  t.tiles_n = up(p.N, kRows);
-  const long long tiles = (long long)t.tiles_n * tiles_t;
+  const int tiles_t = shape(64, 16, 1);
+  t.tiles_n = rows;
   t.tiles = (int)tiles;
-  // CTAs of a tile: while all run at once (two an SM) and each has four slices.
-  const int valid = p.T < t.nt ? p.T : t.nt;
-  const size_t sums = align_up((size_t)valid * kRows * 4, 1024);
-  auto recv = [&](int c) { return c > 1 ? (size_t)(c - 1) * up(valid, c) * kRows * 4 : 0; };
-  auto ring = [&](int n) { return (size_t)n * t.stage_bytes > sums ? (size_t)n * t.stage_bytes : sums; };
-  int cl = 1;
-  while (cl < kMaxCl && tiles * cl * 2 <= 2 * kNumSMs && t.slices >= 8 * cl && recv(2 * cl) + ring(3) + 1024 <= most) cl *= 2;
+  // CTAs of a tile: as many as fit with one CTA an SM, or two where that leaves fewer
+  // SMs idle and the rings are small (1 x 7,168: 112 CTAs 9.2 us, 280 CTAs 7.7;
+  // 64 x 7,168: 12.5 and 14.2); two slices each at least.
+  auto fit = [&](int ctas) {
+    int c = (int)(ctas / tiles);
+    c = c < kMaxCl ? c : kMaxCl;
+    return c < t.slices / 2 ? c : (t.slices > 1 ? t.slices / 2 : 1);
+  };
+  const int one = fit(kNumSMs), both = fit(2 * kNumSMs);
+  const bool two = t.nt <= 32 && tiles * both * 10 > tiles * one * 20 + kNumSMs;
+  const int cl = two ? both : one;
   t.per = up(t.slices, cl);
-  // Two CTAs an SM where there are more than SMs and two rings of three stages fit;
-  // Tensor Memory goes by shared memory, half each.
-  const size_t half = (size_t)98 * 1024;
-  const bool two = tiles * cl > kNumSMs && recv(cl) + ring(3) + 1024 <= half && t.tmem_cols <= 256;
-  t.stages = (int)(((two ? half : most) - recv(cl) - 1024) / t.stage_bytes);
+  // The CTA's sums lie in the ring, those that it receives behind.
+  const int valid = p.T < t.nt ? p.T : t.nt;
+  const size_t recv = cl > 1 ? (size_t)(cl - 1) * up(valid, cl) * kRows * 4 : 0;
+  // Two CTAs share an SM's Tensor Memory as they share its shared memory; no other
+  // may join them and wait for some.
+  const size_t space = two ? (size_t)98 * 1024 : most;
+  t.stages = (int)((space - recv - 1024) / t.stage_bytes);
   if (t.stages > kMaxStages) t.stages = kMaxStages;
-  t.recv_off = (uint32_t)ring(t.stages);
-  // No third CTA (or second) may share the SM and wait for Tensor Memory.
-  size_t smem = t.recv_off + recv(cl) + 1024;
-  const size_t least = two ? half : (size_t)110 * 1024;
+  const size_t sums = align_up((size_t)valid * kRows * 4, 1024), ring = (size_t)t.stages * t.stage_bytes;
+  t.recv_off = (uint32_t)(ring > sums ? ring : sums);
+  size_t smem = t.recv_off + recv + 1024;
+  const size_t least = two ? space : (size_t)110 * 1024;
   if (smem < least) smem = least;
   return start(k_linear<F4, OUT_BF16>, dim3((unsigned)(t.tiles_n * cl), (unsigned)tiles_t), kThreads, cl, smem, s, p, t, x, w);
 }
