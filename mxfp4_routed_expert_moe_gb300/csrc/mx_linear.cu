@@ -159,6 +159,7 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 // Shared memory of this CTA to another's, completing on a barrier there.
 __device__ __forceinline__ void bulk_s2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -444,32 +445,38 @@ template <bool OUT_BF16>
 __device__ __forceinline__ void put_column(const LinearParams& p, int64_t t, int n, const uint32_t (&v)[32], int count) {
   typedef typename std::conditional<OUT_BF16, uint16_t, float>::type T;
   T* o = (T*)p.out + t * p.out_stride + n;
-  const T* ad = p.add ? (const T*)p.add + t * p.add_stride + n : nullptr;
+  auto put = [&](int e, float y) {
+    if constexpr (OUT_BF16)
+      o[e * p.out_stride] = (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu);
+    else
+      o[e * p.out_stride] = y;
+  };
+  if (!p.add) {
 #pragma unroll
-  for (int e0 = 0; e0 < 32; e0 += 8) {
-    float a[8];
+    for (int e = 0; e < 32; ++e)
+      if (e < count) put(e, __uint_as_float(v[e]));
+    return;
+  }
+  const T* ad = (const T*)p.add + t * p.add_stride + n;
+  // Addends 16 at a time, all before the first store, which may be to the same place
+  // (4,096 x 7,168 x 1,408, fp32: 70 us by 8, 61 by 16).
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = 0.f;
-    if (ad) {  // all before the first store, which may be to the same place
+  for (int e0 = 0; e0 < 32; e0 += 16) {
+    float a[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e0 + e < count) {
-          const T x = ad[(e0 + e) * p.add_stride];
-          if constexpr (OUT_BF16)
-            a[e] = bf16_f32(x);
-          else
-            a[e] = x;
-        }
+    for (int e = 0; e < 16; ++e) {
+      a[e] = 0.f;
+      if (e0 + e < count) {
+        const T x = ad[(e0 + e) * p.add_stride];
+        if constexpr (OUT_BF16)
+          a[e] = bf16_f32(x);
+        else
+          a[e] = x;
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e0 + e < count) {
-        const float y = __uint_as_float(v[e0 + e]) + a[e];
-        if constexpr (OUT_BF16)
-          o[(e0 + e) * p.out_stride] = (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu);
-        else
-          o[(e0 + e) * p.out_stride] = y;
-      }
+    for (int e = 0; e < 16; ++e)
+      if (e0 + e < count) put(e0 + e, __uint_as_float(v[e0 + e]) + a[e]);
   }
 }
 // Whether all groups of four of all rows of out and the addend are aligned.
@@ -527,6 +534,13 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   // Not before Tensor Memory is held: a CTA of the next kernel that took it would
   // wait for this one to end.
   pdl_trigger();
+  if (warp == kTmaWarp && lane == 0) {
+    // Maps, and the first weights as far as L2, while the kernel before ends (L2 holds
+    // what it may still write).
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    for (int i = 0; i < min(ns, t.stages); ++i) tma_prefetch_2d(&wmap, (s0 + i) * 128, n0);
+  }
   pdl_wait();
 
   // Results in fours, kUnits a thread at a time; their addends are read before the
@@ -697,6 +711,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
   const LinCtx c = {&sh, p.status, p.wait_limit};
   cluster_wait();  // both CTAs' barriers are ready, both hold Tensor Memory
   pdl_trigger();
+  if (warp == kTmaWarp && lane == 0) {  // as in k_linear
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
+    for (int i = 0; i < min(t.slices, t.stages); ++i) tma_prefetch_2d(&wmap, i * 128, ((pair % t.tiles_n) * 2 + rank) * kRows);
+  }
   pdl_wait();
 
   if (warp < kPairSfWarp0) {
@@ -756,7 +775,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
     for (int tile = pair; tile < t.tiles; tile += pairs, ++ti) {
       const int n = ((tile % t.tiles_n) * 2 + rank) * kRows + q * 32 + lane;
       const int64_t tt = (int64_t)(tile / t.tiles_n) * t.nt + part * t.xrows;
-      const int count = n < p.N ? (int)min((int64_t)t.xrows, p.T - tt) : 0;
+      const int count0 = n - lane < p.N ? (int)min((int64_t)t.xrows, p.T - tt) : 0, count = n < p.N ? count0 : 0;
+      if (p.add) {  // on their way to L2 while the MMAs run
+        const uint8_t* ad = (const uint8_t*)p.add + (tt * p.add_stride + n) * (OUT_BF16 ? 2 : 4);
+        for (int e = lane; e < count0; e += 32) prefetch_l2_line(ad + (int64_t)e * p.add_stride * (OUT_BF16 ? 2 : 4) - lane * (OUT_BF16 ? 2 : 4));
+      }
       if (!lin_warp_wait(c, &sh.sums, ti & 1)) break;
       tc_fence_after();
       uint32_t v[4][32];
