@@ -3,18 +3,22 @@
 //
 // With m the row's largest logit, S = sum e^(z - m) and U = sum e^(z - m) (z - m):
 //   logprob = z_t - m - log S,   entropy = log S - U / S.
-// Every thread keeps (m, S, U) of what it has seen and rescales them where m
-// grows; threads, warps and the CTAs of a row join theirs in a fixed order.
+// Sums are in base 2: with L = log2(e) and c = -m L rounded, a logit weighs
+// 2^(z L + c), one FMA with one rounding; the rounding of c is common to all and
+// cancels in every result, all of which are taken by the same FMA.  Every thread
+// keeps (m, c, S, U) of what it has seen and rescales them where m grows; threads,
+// warps and the CTAs of a row join theirs in a fixed order.
 //
-// The best alternatives come out of the same pass: the first tile of a piece
-// gives 128 maxima of disjoint groups of logits, and the top-th of those is a
-// bound that at least `top` logits reach; whatever is not below it goes to a list,
-// a few times `top` of a row in random order.  One comparison per eight logits
-// decides that there is nothing to list.  A list that overflows (rows that grow
-// with the index) is made again in small steps, thinned by the same bound.
+// One comparison per eight logits decides whether there is more to do with them: a
+// new maximum, logits ahead of the given token (which are counted one by one), or
+// candidates for the alternatives.  Those come from a bound that the first tile of a
+// piece gives: 128 maxima of disjoint groups of its logits, of which the top-th is
+// reached by at least `top` logits; whatever is not below it goes to a list, a few
+// times `top` of a row in random order.  A list that overflows (rows that grow with
+// the index) is made again in small steps, thinned by the same bound.
 //
 // A cluster of 1 to 8 CTAs takes a row; logits are read once.  Bound by HBM and by
-// the instructions of a logit (ten) alike for many rows, by latency for one.
+// the instructions of a logit (nine) alike for many rows, by latency for one.
 #include <cooperative_groups.h>
 
 #include "dense.cuh"
@@ -26,19 +30,21 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;                       // vectors of 8 logits a thread has in flight
+constexpr int kUnroll = 4;                       // vectors of 8 logits of a thread in the first tile, and in flight
 constexpr int kTile = kThreads * kUnroll;        // vectors
 constexpr int kList = 2048;
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxCl = 8;
 constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFar = -200.f;                   // e^-200 is 0 in fp32
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFar = -300.f;                   // 2^-300 is 0 in fp32
+constexpr float kPlain = 1048576.f;              // maxima beyond, whose c is rounded by 0.1 and more, are summed again at the end
 
 typedef unsigned long long Key;  // (order bits of a logit) << 32 | ~index: larger is better; 0: none
 
 struct Stats {
-  float m, s, u;
+  float m, c, s, u;
   int count;
 };
 
@@ -63,27 +69,47 @@ __device__ __forceinline__ Key key_of(float z, uint32_t index) {
   return z > -INFINITY ? ((Key)order_bits(z) << 32) | (uint32_t)~index : 0ull;
 }
 __device__ __forceinline__ Key key_max(Key a, Key b) { return a > b ? a : b; }
-__device__ __forceinline__ float exp_of(float d) {
+__device__ __forceinline__ float exp2_of(float t) {
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   return e;
 }
 
-// Statistics over a larger maximum M (m <= M; both may be -inf).
-__device__ __forceinline__ void raise(float M, float& m, float& s, float& u) {
-  const float d = fmaxf(m - M, kFar), f = exp_of(d);  // NaN (both infinite) as far
-  u = f * (u + s * d);
-  s *= f;
-  m = M;
+// Sums over a larger maximum.  Those around a far one (masked logits) may be
+// infinite; they leave nothing here.
+__device__ __forceinline__ void raise(float M, float C, Stats& a) {
+  const float d = fmaxf(C - a.c, kFar), f = exp2_of(d);
+  const bool left = a.m > -INFINITY && f > 0.f;
+  a.u = left ? f * (a.u + a.s * d) : 0.f;
+  a.s = left ? f * a.s : 0.f;
+  a.m = M;
+  a.c = C;
 }
+__device__ __forceinline__ float shift_of(float m) { return m > -INFINITY ? -m * kLog2e : 0.f; }
 __device__ __forceinline__ Stats join(Stats a, Stats b) {
-  const float M = fmaxf(a.m, b.m);
-  if (a.m != M) raise(M, a.m, a.s, a.u);
-  if (b.m != M) raise(M, b.m, b.s, b.u);
+  if (b.m > a.m) raise(b.m, b.c, a);
+  if (a.m > b.m) raise(a.m, a.c, b);
   a.s += b.s;
   a.u += b.u;
   a.count += b.count;
   return a;
+}
+__device__ __forceinline__ Stats other(const Stats& a, int o) {
+  Stats b;
+  b.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, o);
+  b.c = __shfl_xor_sync(0xFFFFFFFFu, a.c, o);
+  b.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+  b.u = __shfl_xor_sync(0xFFFFFFFFu, a.u, o);
+  b.count = __shfl_xor_sync(0xFFFFFFFFu, a.count, o);
+  return b;
+}
+__device__ __forceinline__ Stats warp_join(Stats st) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const Stats b = other(st, o);
+    st = (threadIdx.x & o) ? join(b, st) : join(st, b);
+  }
+  return st;
 }
 
 // The logits of a CTA's piece as vectors of eight from an address aligned to 16
@@ -193,101 +219,126 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     if (zt > -INFINITY) ahead_before = zt == 0.f ? __uint_as_float(0x80000001u) : order_float(order_bits(zt) - 1u);
   }
 
-  float m = -INFINITY, s = 0.f, u = 0.f;
-  int count = 0;
-  float bound_z = INFINITY;  // logits above are listed, after the first tile
-  for (int v0 = 0; v0 < in.vectors || v0 == 0; v0 += kTile) {
-    float x[kUnroll][8];
+  Stats st = {-INFINITY, 0.f, 0.f, 0.f, 0};
+  float bound_z = INFINITY;  // logits above are listed, behind the first tile
+  const float ahead = fminf(ahead_before, ahead_after);
+  float limit = -INFINITY;   // vectors up to here need nothing but their sums
+  // Eight logits from index i0 on.
+  auto sums = [&](const float (&x)[8]) {
+    float s2 = 0.f, u2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      // NaN, and -inf where nothing has been seen, as far.
+      const float t0 = fmaxf(fmaf(x[e], kLog2e, st.c), kFar), t1 = fmaxf(fmaf(x[e + 1], kLog2e, st.c), kFar);
+      const float w0 = exp2_of(t0), w1 = exp2_of(t1);
+      st.s += w0;
+      s2 += w1;
+      st.u = fmaf(w0, t0, st.u);
+      u2 = fmaf(w1, t1, u2);
+    }
+    st.s += s2;
+    st.u += u2;
+  };
+  auto counts = [&](const float (&x)[8], int i0) {
+    if (i0 <= token && i0 + 7 >= token) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i0 + e != token) st.count += x[e] > (i0 + e < token ? ahead_before : ahead_after);
+    } else {
+      const float a = i0 < token ? ahead_before : ahead_after;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st.count += x[e] > a;
+    }
+  };
+  {
+    float x[kUnroll][8], most[kUnroll];
     {
       Eight<BF16> raw[kUnroll];
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        const int v = v0 + j * kThreads + tid;
-        if (v < in.vectors && in.whole(v)) raw[j].load(in.base, v);
-      }
+      for (int j = 0; j < kUnroll; ++j)
+        if (in.whole(j * kThreads + tid)) raw[j].load(in.base, j * kThreads + tid);
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const int v = v0 + j * kThreads + tid;
-        if (v < in.vectors && in.whole(v))
+        if (in.whole(j * kThreads + tid))
           raw[j].get(x[j]);
         else
-          in.edge(v, x[j]);  // -inf past the end
+          in.edge(j * kThreads + tid, x[j]);  // -inf past the end
+        most[j] = max8(x[j]);
+        st.m = fmaxf(st.m, most[j]);
       }
     }
-    float most[kUnroll], all = -INFINITY;
+    st.c = shift_of(st.m);
+    Key bound = 0ull;
+    if (top) {
+      Key mine = 0ull;
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) most[j] = max8(x[j]), all = fmaxf(all, most[j]);
-    if (all > m) raise(all, m, s, u);
+      for (int j = kUnroll - 1; j >= 0; --j)
+        if (most[j] == st.m)
+#pragma unroll
+          for (int e = 7; e >= 0; --e)
+            if (x[j][e] == st.m) mine = key_of(st.m, in.first + 8 * (j * kThreads + tid) + e);
+      find_bound(sh, mine, top);
+      bound = sh.bound;
+      bound_z = bound ? order_float((uint32_t)(bound >> 32)) : -INFINITY;
+    }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
+      const uint32_t i0 = in.first + 8 * (j * kThreads + tid);
+      if (known && most[j] > ahead) counts(x[j], (int)i0);
+      if (top && most[j] >= bound_z)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = fmaxf(x[j][e] - m, kFar);  // NaN, and -inf less -inf, as far
-        const float w = exp_of(d);
-        s += w;
-        u = fmaf(w, d, u);
-      }
+        for (int e = 0; e < 8; ++e) {
+          const Key k = key_of(x[j][e], i0 + e);
+          if (k && k >= bound) list_add(sh, k);
+        }
+      sums(x[j]);
     }
-    if (known) {
+  }
+  limit = fminf(st.m, fminf(ahead, bound_z));
+  auto vector = [&](const float (&x)[8], int v) {
+    const float most = max8(x);
+    if (most > limit) {
+      const int i0 = (int)in.first + 8 * v;
+      if (most > st.m) raise(most, shift_of(most), st);
+      if (most > ahead) counts(x, i0);  // `ahead` is infinite without a token
+      if (most > bound_z) {
+        // Behind the first tile: an equal logit has a larger index and is not ahead.
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (x[e] > bound_z) list_add(sh, key_of(x[e], (uint32_t)(i0 + e)));
+      }
+      limit = fminf(st.m, fminf(ahead, bound_z));
+    }
+    sums(x);
+  };
+  {
+    // Whole vectors, kUnroll of them in flight; the last of the piece may be cut.
+    const int cut = in.vectors - (in.vectors > 0 && !in.whole(in.vectors - 1));
+    Eight<BF16> raw[kUnroll];
+    int v = kTile + tid;
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+      if (v + j * kThreads < cut) raw[j].load(in.base, v + j * kThreads);
+    for (; v < cut; v += kTile) {
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const int i0 = (int)in.first + 8 * (v0 + j * kThreads + tid);
-        if (i0 <= token && i0 + 7 >= token) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (i0 + e != token) count += x[j][e] > (i0 + e < token ? ahead_before : ahead_after);
-        } else {
-          const float ahead = i0 < token ? ahead_before : ahead_after;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) count += x[j][e] > ahead;
+        if (v + j * kThreads < cut) {
+          float x[8];
+          raw[j].get(x);
+          if (v + j * kThreads + kTile < cut) raw[j].load(in.base, v + j * kThreads + kTile);
+          vector(x, v + j * kThreads);
         }
       }
     }
-    if (top) {
-      if (v0 == 0) {
-        Key mine = 0ull;
-#pragma unroll
-        for (int j = kUnroll - 1; j >= 0; --j) {
-          const uint32_t i0 = in.first + 8 * (j * kThreads + tid);
-          if (most[j] == all)
-#pragma unroll
-            for (int e = 7; e >= 0; --e)
-              if (x[j][e] == all) mine = key_of(all, i0 + e);
-        }
-        find_bound(sh, mine, top);
-        const Key bound = sh.bound;
-        bound_z = bound ? order_float((uint32_t)(bound >> 32)) : -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-          if (most[j] >= bound_z)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const Key k = key_of(x[j][e], in.first + 8 * (j * kThreads + tid) + e);
-              if (k && k >= bound) list_add(sh, k);
-            }
-      } else {
-        // Indices behind the first tile's: an equal logit is not ahead.
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-          if (most[j] > bound_z)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (x[j][e] > bound_z) list_add(sh, key_of(x[j][e], in.first + 8 * (v0 + j * kThreads + tid) + e));
-      }
+    if (cut < in.vectors && cut >= kTile && tid == 0) {
+      float x[8];
+      in.edge(cut, x);
+      vector(x, cut);
     }
   }
 
   // Statistics: lanes, warps, CTAs.
-  Stats st = {m, s, u, count};
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    Stats b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-    b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-    b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-    b.count = __shfl_xor_sync(0xFFFFFFFFu, st.count, o);
-    st = (lane & o) ? join(b, st) : join(st, b);
-  }
+  st = warp_join(st);
   if (lane == 0) sh.warp[warp] = st;
   __syncthreads();
   if (top) {
@@ -323,18 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     }
     __syncthreads();
   }
-  if (warp == 0) {
-    st = lane < kWarps ? sh.warp[lane] : Stats{-INFINITY, 0.f, 0.f, 0};
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      Stats b;
-      b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-      b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-      b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-      b.count = __shfl_xor_sync(0xFFFFFFFFu, st.count, o);
-      st = (lane & o) ? join(b, st) : join(st, b);
-    }
-  }
+  if (warp == 0) st = warp_join(lane < kWarps ? sh.warp[lane] : Stats{-INFINITY, 0.f, 0.f, 0.f, 0});
   if (cl > 1) {
     cluster.sync();  // every CTA has started
     if (warp == 0) {
@@ -364,28 +404,45 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
   if (tid == 0) sh.cl[0] = st;
   __syncthreads();
   st = sh.cl[0];
-  float log_s = logf(st.s);
-  const bool infinite = st.m == INFINITY;
-  if (infinite) {  // those logits share the probability: their number
-    int c = 0;
-    for (int i = tid; i < p.vocab; i += kThreads)
-      c += (BF16 ? bf16_f32(__ldg((const uint16_t*)row + i)) : __ldg((const float*)row + i)) == INFINITY;
-    c = __reduce_add_sync(0xFFFFFFFFu, c);
-    if (lane == 0) sh.warp[warp].count = c;
+  const bool infinite = st.m == INFINITY, nothing = st.m == -INFINITY;
+  bool plain = true;  // base 2 and the common shift
+  if (!nothing && fabsf(st.m) > kPlain) {
+    // Infinite logits, which share the probability, are counted; those around a far
+    // maximum are summed by their differences.
+    plain = false;
+    float s = 0.f, u = 0.f;
+    for (int i = tid; i < p.vocab; i += kThreads) {
+      const float z = BF16 ? bf16_f32(__ldg((const uint16_t*)row + i)) : __ldg((const float*)row + i);
+      if (infinite) {
+        s += z == INFINITY ? 1.f : 0.f;
+      } else {
+        const float d = fmaxf((z - st.m) * kLog2e, kFar), w = exp2_of(d);
+        s += w;
+        u = fmaf(w, d, u);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    }
+    if (lane == 0) sh.warp[warp].s = s, sh.warp[warp].u = u;
     __syncthreads();
-    c = 0;
-    for (int w = 0; w < kWarps; ++w) c += sh.warp[w].count;
-    log_s = logf((float)c);
+    st.s = st.u = 0.f;
+    for (int w = 0; w < kWarps; ++w) st.s += sh.warp[w].s, st.u += sh.warp[w].u;
   }
   if (warp != 0) return;
+  const float log2_s = log2f(st.s);
   auto log_prob = [&](float z) {
-    if (infinite) return z == INFINITY ? -log_s : -INFINITY;
-    return z == -INFINITY ? -INFINITY : (z - st.m) - log_s;
+    if (infinite) return z == INFINITY ? -log2_s * kLn2 : -INFINITY;
+    if (z == -INFINITY) return -INFINITY;
+    if (plain && fabsf(z) <= kPlain) return (fmaf(z, kLog2e, st.c) - log2_s) * kLn2;
+    return (z - st.m) - log2_s * kLn2;
   };
   if (lane == 0) {
     if (p.logprob) p.logprob[r] = known ? log_prob(zt) : -INFINITY;
     if (p.rank) p.rank[r] = known ? st.count + (zt == -INFINITY ? token : 0) : -1;
-    if (p.entropy) p.entropy[r] = infinite ? log_s : st.m == -INFINITY ? 0.f : log_s - st.u / st.s;
+    if (p.entropy) p.entropy[r] = nothing ? 0.f : (log2_s - st.u / st.s) * kLn2;  // infinite: u = 0
   }
   if (lane < top) {
     const Key k = sh.best[lane];
