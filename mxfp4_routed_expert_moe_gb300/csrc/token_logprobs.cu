@@ -1,16 +1,18 @@
 // token_logprobs.cu — log probabilities of given tokens, ranks, entropies and
 // the best alternatives of rows of logits.
 //
-// With m the row's largest logit, S = sum e^(z - m) and U = sum e^(z - m) (z - m):
+// With S = sum e^(z - m) and U = sum e^(z - m) (z - m), whatever the reference m is,
 //   logprob = z_t - m - log S,   entropy = log S - U / S.
 // Sums are in base 2: with L = log2(e) and c = -m L rounded, a logit weighs
 // 2^(z L + c), one FMA with one rounding; the rounding of c is common to all and
-// cancels in every result, all of which are taken by the same FMA.  Every thread
-// keeps (m, c, S, U) of what it has seen and rescales them where m grows; threads,
-// warps and the CTAs of a row join theirs in a fixed order.
+// cancels in every result, all of which are taken by the same FMA.  A warp's
+// reference is the largest logit of its part of the first tile, and is raised only
+// for logits 40 above it: were it each thread's own maximum, some lane of a warp
+// would have a new one at nearly every step.  Threads, warps and the CTAs of a row
+// join their (m, c, S, U) in a fixed order.
 //
 // One comparison per eight logits decides whether there is more to do with them: a
-// new maximum, logits ahead of the given token (which are counted one by one), or
+// far new maximum, logits ahead of the given token (which are counted one by one), or
 // candidates for the alternatives.  Those come from a bound that the first tile of a
 // piece gives: 128 maxima of disjoint groups of its logits, of which the top-th is
 // reached by at least `top` logits; whatever is not below it goes to a list, a few
@@ -21,6 +23,8 @@
 // the instructions of a logit (nine) alike for many rows, by latency for one.
 #include <cooperative_groups.h>
 
+#include <cuda/std/type_traits>
+
 #include "dense.cuh"
 
 namespace moe {
@@ -30,8 +34,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;                       // vectors of 8 logits of a thread in the first tile, and in flight
-constexpr int kTile = kThreads * kUnroll;        // vectors
+constexpr int kUnroll = 2;                       // vectors of 8 logits that a thread has in flight (with 4 registers spill)
 constexpr int kList = 2048;
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxCl = 8;
@@ -39,7 +42,8 @@ constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -300.f;                   // 2^-300 is 0 in fp32
-constexpr float kPlain = 1048576.f;              // maxima beyond, whose c is rounded by 0.1 and more, are summed again at the end
+constexpr float kPlain = 1048576.f;              // references beyond, whose c is rounded by 0.1 and more, are summed again at the end
+constexpr float kAbove = 40.f;                   // logits this far above the reference raise it: weights below 2^58
 
 typedef unsigned long long Key;  // (order bits of a logit) << 32 | ~index: larger is better; 0: none
 
@@ -52,7 +56,7 @@ struct ScoreShared {
   Key list[kList];
   Key group[kGroups];
   Key best[kTop];
-  Key cl_best[kMaxCl][kTop];
+  Key cl_best[kMaxCl * kTop];  // [CTA][top]
   Stats warp[kWarps];
   Stats cl[kMaxCl];
   Key bound;
@@ -75,7 +79,26 @@ __device__ __forceinline__ float exp2_of(float t) {
   return e;
 }
 
-// Sums over a larger maximum.  Those around a far one (masked logits) may be
+// Two fp32 values in a register pair, for the packed FMA and add.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void apart(Two v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Sums over a larger reference.  Those around a far one (masked logits) may be
 // infinite; they leave nothing here.
 __device__ __forceinline__ void raise(float M, float C, Stats& a) {
   const float d = fmaxf(C - a.c, kFar), f = exp2_of(d);
@@ -144,6 +167,60 @@ __device__ __forceinline__ float max8(const float (&x)[8]) {
   return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 }
 
+// Largest of the logits of some vectors as they are held.
+__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float most_of(const Eight<true> (&raw)[N]) {
+  uint32_t m = 0xFF80FF80u;
+#pragma unroll
+  for (int j = 0; j < N; ++j) m = most2(m, most2(most2(raw[j].v.x, raw[j].v.y), most2(raw[j].v.z, raw[j].v.w)));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+template <int N>
+__device__ __forceinline__ float most_of(const Eight<false> (&raw)[N]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float x[8];
+    raw[j].get(x);
+    m = fmaxf(m, max8(x));
+  }
+  return m;
+}
+
+// f(key, rank) for each of n keys that differ (but for 0, none), a warp a key: rank is
+// the number of better ones.  Every lane calls f with the same.
+template <typename F>
+__device__ __forceinline__ void ranks(const Key* keys, int n, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (n <= 128) {  // a lane holds its share of them
+    Key other[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) other[j] = lane + 32 * j < n ? keys[lane + 32 * j] : 0ull;
+    for (int i = warp; i < n; i += kWarps) {
+      const Key key = keys[i];
+      int better = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) better += __popc(__ballot_sync(0xFFFFFFFFu, other[j] > key));
+      f(key, better);
+    }
+    return;
+  }
+  for (int i = warp; i < n; i += kWarps) {
+    const Key key = keys[i];
+    int better = 0;
+    for (int c = lane; c - lane < n; c += 32) {
+      const Key other = c < n ? keys[c] : 0ull;
+      better += __popc(__ballot_sync(0xFFFFFFFFu, other > key));
+    }
+    f(key, better);
+  }
+}
+
 // The top-th best of the 128 group maxima into sh.bound (0 where fewer groups
 // hold something), each thread giving the best key that it knows.  Barriers on
 // both sides.
@@ -153,13 +230,9 @@ __device__ __forceinline__ void find_bound(ScoreShared& sh, Key mine, int top) {
   if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = mine;
   if (threadIdx.x == 0) sh.bound = 0ull;
   __syncthreads();
-  if (threadIdx.x < kGroups) {
-    const Key k = sh.group[threadIdx.x];
-    int better = 0;
-#pragma unroll 8
-    for (int i = 0; i < kGroups; ++i) better += sh.group[i] > k;
-    if (better == top - 1 && k) sh.bound = k;  // keys differ: one thread at most
-  }
+  ranks(sh.group, kGroups, [&](Key k, int better) {
+    if (k && better == top - 1 && (threadIdx.x & 31) == 0) sh.bound = k;
+  });
   __syncthreads();
 }
 
@@ -189,8 +262,21 @@ __device__ void thin(ScoreShared& sh, int top) {
   __syncthreads();
 }
 
+// The top-th best key of the list so far into sh.bound, if it is short; at least
+// that many logits reach it.  All threads, barriers on both sides.
+__device__ __forceinline__ void tighten(ScoreShared& sh, int top) {
+  __syncthreads();
+  const int n = (int)sh.list_n;
+  if (n >= top && n <= kThreads)
+    ranks(sh.list, n, [&](Key k, int better) {
+      if (better == top - 1 && (threadIdx.x & 31) == 0) sh.bound = k;
+    });
+  __syncthreads();
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobParams p) {
+  constexpr int U = kUnroll, kTile = kThreads * U;
   __shared__ ScoreShared sh;
   pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
@@ -207,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
 
   // The given token: its logit, and the bounds above which a logit before or
   // after it in the row is ahead of it.
-  int token = p.tokens ? __ldg(&p.tokens[r]) : -1;
+  const int token = p.tokens ? __ldg(&p.tokens[r]) : -1;
   const bool known = token >= 0 && token < p.vocab;
   float zt = -INFINITY, ahead_before = INFINITY, ahead_after = INFINITY;
   if (known) {
@@ -220,24 +306,48 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
   }
 
   Stats st = {-INFINITY, 0.f, 0.f, 0.f, 0};
+  Two s2 = 0, u2 = 0;        // the sums, in two lanes
   float bound_z = INFINITY;  // logits above are listed, behind the first tile
-  const float ahead = fminf(ahead_before, ahead_after);
+  float ahead = fminf(ahead_before, ahead_after);
   float limit = -INFINITY;   // vectors up to here need nothing but their sums
-  // Eight logits from index i0 on.
-  auto sums = [&](const float (&x)[8]) {
-    float s2 = 0.f, u2 = 0.f;
+  const Two log2e2 = two(kLog2e, kLog2e);
+  auto sums = [&](const float (&x)[U][8]) {
+    const Two c2 = two(st.c, st.c);
+    Two s = s2, u = u2;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      // NaN, and -inf where nothing has been seen, as far.
-      const float t0 = fmaxf(fmaf(x[e], kLog2e, st.c), kFar), t1 = fmaxf(fmaf(x[e + 1], kLog2e, st.c), kFar);
-      const float w0 = exp2_of(t0), w1 = exp2_of(t1);
-      st.s += w0;
-      s2 += w1;
-      st.u = fmaf(w0, t0, st.u);
-      u2 = fmaf(w1, t1, u2);
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const Two t2 = fma2(two(x[j][e], x[j][e + 1]), log2e2, c2);
+        float t0, t1;
+        apart(t2, t0, t1);
+        const Two w2 = two(exp2_of(t0), exp2_of(t1));
+        s = add2(s, w2);
+        u = fma2(w2, t2, u);
+      }
+    float u0, u1;
+    apart(u, u0, u1);
+    if (!(u0 + u1 <= INFINITY)) {
+      // An infinity or a NaN among them (0 times -inf): again with those far away.
+      s = s2, u = u2;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float t0 = fmaxf(fmaf(x[j][e], kLog2e, st.c), kFar), t1 = fmaxf(fmaf(x[j][e + 1], kLog2e, st.c), kFar);
+          const Two w2 = two(exp2_of(t0), exp2_of(t1));
+          s = add2(s, w2);
+          u = fma2(w2, two(t0, t1), u);
+        }
     }
-    st.s += s2;
-    st.u += u2;
+    s2 = s, u2 = u;
+  };
+  auto gather = [&] {
+    float a, b;
+    apart(s2, a, b);
+    st.s = a + b;
+    apart(u2, a, b);
+    st.u = a + b;
   };
   auto counts = [&](const float (&x)[8], int i0) {
     if (i0 <= token && i0 + 7 >= token) {
@@ -250,15 +360,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
       for (int e = 0; e < 8; ++e) st.count += x[e] > a;
     }
   };
+  bool crowded;  // many logits are ahead of the token: counted without asking
   {
-    float x[kUnroll][8], most[kUnroll];
+    float x[U][8], most[U];
     {
-      Eight<BF16> raw[kUnroll];
+      Eight<BF16> raw[U];
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j)
+      for (int j = 0; j < U; ++j)
         if (in.whole(j * kThreads + tid)) raw[j].load(in.base, j * kThreads + tid);
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
+      for (int j = 0; j < U; ++j) {
         if (in.whole(j * kThreads + tid))
           raw[j].get(x[j]);
         else
@@ -267,75 +378,121 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
         st.m = fmaxf(st.m, most[j]);
       }
     }
-    st.c = shift_of(st.m);
     Key bound = 0ull;
     if (top) {
-      Key mine = 0ull;
+      uint32_t at = 0u;  // of the thread's largest
 #pragma unroll
-      for (int j = kUnroll - 1; j >= 0; --j)
-        if (most[j] == st.m)
+      for (int j = U - 1; j >= 0; --j)
 #pragma unroll
-          for (int e = 7; e >= 0; --e)
-            if (x[j][e] == st.m) mine = key_of(st.m, in.first + 8 * (j * kThreads + tid) + e);
-      find_bound(sh, mine, top);
+        for (int e = 7; e >= 0; --e) at = x[j][e] == st.m ? 8 * j * kThreads + e : at;
+      find_bound(sh, key_of(st.m, in.first + 8 * tid + at), top);
       bound = sh.bound;
       bound_z = bound ? order_float((uint32_t)(bound >> 32)) : -INFINITY;
     }
+    st.m = order_float(__reduce_max_sync(0xFFFFFFFFu, order_bits(st.m)));
+    st.c = shift_of(st.m);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const uint32_t i0 = in.first + 8 * (j * kThreads + tid);
       if (known && most[j] > ahead) counts(x[j], (int)i0);
-      if (top && most[j] >= bound_z)
+      if (top && most[j] >= bound_z) {
+        uint32_t which = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const Key k = key_of(x[j][e], i0 + e);
+        for (int e = 0; e < 8; ++e) which |= x[j][e] >= bound_z ? 1u << e : 0u;
+        for (; which; which &= which - 1) {
+          const int e = __ffs(which) - 1;
+          const Key k = key_of(in.one(8 * (j * kThreads + tid) + e), i0 + e);
           if (k && k >= bound) list_add(sh, k);
         }
-      sums(x[j]);
-    }
-  }
-  limit = fminf(st.m, fminf(ahead, bound_z));
-  auto vector = [&](const float (&x)[8], int v) {
-    const float most = max8(x);
-    if (most > limit) {
-      const int i0 = (int)in.first + 8 * v;
-      if (most > st.m) raise(most, shift_of(most), st);
-      if (most > ahead) counts(x, i0);  // `ahead` is infinite without a token
-      if (most > bound_z) {
-        // Behind the first tile: an equal logit has a larger index and is not ahead.
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (x[e] > bound_z) list_add(sh, key_of(x[e], (uint32_t)(i0 + e)));
       }
-      limit = fminf(st.m, fminf(ahead, bound_z));
     }
     sums(x);
-  };
-  {
-    // Whole vectors, kUnroll of them in flight; the last of the piece may be cut.
-    const int cut = in.vectors - (in.vectors > 0 && !in.whole(in.vectors - 1));
-    Eight<BF16> raw[kUnroll];
-    int v = kTile + tid;
+    // A step of a warp sees as many logits as this: one of them ahead each time costs
+    // more than counting all.
+    crowded = __any_sync(0xFFFFFFFFu, st.count > 0);
+  }
+  // The tiles behind the first, the next one's logits in flight.
+  auto pass = [&](auto count_all) {
+    constexpr bool ALL = decltype(count_all)::value;
+    auto set_limit = [&] { limit = fminf(st.m + kAbove, ALL ? bound_z : fminf(ahead, bound_z)); };
+    auto step = [&](const float (&x)[U][8], float all, int v0) {
+      if (ALL)
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-      if (v + j * kThreads < cut) raw[j].load(in.base, v + j * kThreads);
-    for (; v < cut; v += kTile) {
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        if (v + j * kThreads < cut) {
-          float x[8];
-          raw[j].get(x);
-          if (v + j * kThreads + kTile < cut) raw[j].load(in.base, v + j * kThreads + kTile);
-          vector(x, v + j * kThreads);
+        for (int j = 0; j < U; ++j) counts(x[j], (int)in.first + 8 * (v0 + j * kThreads));
+      if (all > limit) {
+        if (all > st.m + kAbove) {
+          gather();
+          raise(all, shift_of(all), st);
+          s2 = two(st.s, 0.f), u2 = two(st.u, 0.f);
         }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const float most = max8(x[j]);
+          const int v = v0 + j * kThreads, i0 = (int)in.first + 8 * v;
+          if (!ALL && most > ahead) counts(x[j], i0);  // `ahead` is infinite without a token
+          if (most > bound_z) {
+            // Behind the first tile: an equal logit has a larger index and is not ahead.
+            uint32_t which = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) which |= x[j][e] > bound_z ? 1u << e : 0u;
+            for (; which; which &= which - 1) {
+              const int e = __ffs(which) - 1;
+              list_add(sh, key_of(in.one(8 * v + e), (uint32_t)(i0 + e)));
+            }
+          }
+        }
+        set_limit();
+      }
+      sums(x);
+    };
+    set_limit();
+    // Tiles of whole vectors, then what is left of the piece.
+    const int tiles = in.vectors > 0 ? (in.vectors - !in.whole(in.vectors - 1)) / kTile : 0;
+    Eight<BF16> raw[U];
+    if (tiles > 1)
+#pragma unroll
+      for (int j = 0; j < U; ++j) raw[j].load(in.base, kTile + tid + j * kThreads);
+    for (int tile = 1; tile < tiles; ++tile) {
+      const int v0 = tile * kTile + tid;
+      float x[U][8];
+      const float all = most_of(raw);
+#pragma unroll
+      for (int j = 0; j < U; ++j) raw[j].get(x[j]);
+      if (tile + 1 < tiles)
+#pragma unroll
+        for (int j = 0; j < U; ++j) raw[j].load(in.base, v0 + kTile + j * kThreads);
+      step(x, all, v0);
+      // What is listed so far gives a better bound: of twice, four, .. times the first
+      // tile's logits.
+      if (top && (tile & (tile + 1)) == 0 && (tile + 1) * kTile < in.vectors) {
+        tighten(sh, top);
+        const Key bound = sh.bound;
+        if (bound) bound_z = fmaxf(bound_z, order_float((uint32_t)(bound >> 32)));
+        set_limit();
       }
     }
-    if (cut < in.vectors && cut >= kTile && tid == 0) {
-      float x[8];
-      in.edge(cut, x);
-      vector(x, cut);
+    if ((tiles > 1 ? tiles : 1) * kTile < in.vectors) {
+      const int v0 = (tiles > 1 ? tiles : 1) * kTile + tid;
+      float x[U][8], all = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int v = v0 + j * kThreads;
+        if (in.whole(v)) {
+          raw[j].load(in.base, v);
+          raw[j].get(x[j]);
+        } else {
+          in.edge(v, x[j]);  // -inf past the end
+        }
+        all = fmaxf(all, max8(x[j]));
+      }
+      step(x, all, v0);
     }
-  }
+  };
+  if (crowded)
+    pass(cuda::std::true_type{});
+  else
+    pass(cuda::std::false_type{});
+  gather();
 
   // Statistics: lanes, warps, CTAs.
   st = warp_join(st);
@@ -361,17 +518,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
       }
     }
     if (sh.list_n > kThreads) thin(sh, top);
-    // Ranks by counting: at most a key a thread.
-    const uint32_t listed = sh.list_n;
+    // Ranks by counting.
     if (tid < kTop) sh.best[tid] = 0ull;
     __syncthreads();
-    if (tid < (int)listed) {
-      const Key k = sh.list[tid];
-      int better = 0;
-#pragma unroll 4
-      for (uint32_t i = 0; i < listed; ++i) better += sh.list[i] > k;
-      if (better < top) sh.best[better] = k;
-    }
+    ranks(sh.list, (int)sh.list_n, [&](Key k, int better) {
+      if (better < top && lane == 0) sh.best[better] = k;
+    });
     __syncthreads();
   }
   if (warp == 0) st = warp_join(lane < kWarps ? sh.warp[lane] : Stats{-INFINITY, 0.f, 0.f, 0.f, 0});
@@ -380,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     if (warp == 0) {
       ScoreShared* o = cluster.map_shared_rank(&sh, 0);
       if (lane == 0) o->cl[rank] = st;
-      if (top) o->cl_best[rank][lane] = sh.best[lane];
+      if (lane < top) o->cl_best[rank * top + lane] = sh.best[lane];
     }
     cluster.sync();  // no remote access follows
     if (rank != 0) return;
@@ -391,14 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     if (top) {
       if (tid < kTop) sh.best[tid] = 0ull;
       __syncthreads();
-      if (tid < cl * kTop) {
-        const Key* all = &sh.cl_best[0][0];
-        const Key k = all[tid];
-        int better = 0;
-#pragma unroll 8
-        for (int i = 0; i < cl * kTop; ++i) better += all[i] > k;
-        if (k && better < top) sh.best[better] = k;
-      }
+      ranks(sh.cl_best, cl * top, [&](Key k, int better) {
+        if (k && better < top && lane == 0) sh.best[better] = k;
+      });
     }
   }
   if (tid == 0) sh.cl[0] = st;
