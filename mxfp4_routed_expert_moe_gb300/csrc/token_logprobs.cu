@@ -355,9 +355,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
       for (int e = 0; e < 8; ++e)
         if (i0 + e != token) st.count += x[e] > (i0 + e < token ? ahead_before : ahead_after);
     } else {
+      // By the sign of a - x, an addition of a shifted word each (44 against 41 us for
+      // 512 rows of 163,840 without alternatives).  NaN, as of equal infinities, comes
+      // without a sign.
       const float a = i0 < token ? ahead_before : ahead_after;
+      const Two a2 = two(a, a), minus = two(-1.f, -1.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st.count += x[e] > a;
+      for (int e = 0; e < 8; e += 2) {
+        float d0, d1;
+        apart(fma2(two(x[e], x[e + 1]), minus, a2), d0, d1);
+        st.count += (int)(__float_as_uint(d0) >> 31);
+        st.count += (int)(__float_as_uint(d1) >> 31);
+      }
     }
   };
   bool crowded;  // many logits are ahead of the token: counted without asking
@@ -462,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
 #pragma unroll
         for (int j = 0; j < U; ++j) raw[j].load(in.base, v0 + kTile + j * kThreads);
       step(x, all, v0);
-      // What is listed so far gives a better bound: of twice, four, .. times the first
+      // What is listed so far gives a better bound, of 2, 4 and 10 times the first
       // tile's logits.
-      if (top && (tile & (tile + 1)) == 0 && (tile + 1) * kTile < in.vectors) {
+      if (top && (tile == 1 || tile == 3 || tile == 9) && (tile + 1) * kTile < in.vectors) {
         tighten(sh, top);
         const Key bound = sh.bound;
         if (bound) bound_z = fmaxf(bound_z, order_float((uint32_t)(bound >> 32)));
