@@ -72,7 +72,7 @@ class MXMatrix:
             raise ValueError(f"codes of [{rows}][{cols}] need cols a multiple of 32 and scales [rows][cols / 32], not {tuple(s.shape)}")
         if q.get_device() != s.get_device():
             raise ValueError("q and s of an MX matrix must be on one device")
-        self.q, self.s, self.kind, self.rows, self.cols = q, s, kind, rows, cols
+        self.q, self.s, self.kind, self.rows, self.cols, self.shape = q, s, kind, rows, cols, (rows, cols)
         # One row has any stride.
         qs, ss = (q.stride(0), s.stride(0)) if rows > 1 else (q.shape[1] + -q.shape[1] % 32, cols // 32 + -(cols // 32) % 4)
         self.struct = _Mx(q.data_ptr(), s.data_ptr(), KINDS[kind], rows, cols, qs, ss)
@@ -89,10 +89,6 @@ class MXMatrix:
             raise ValueError("cols must be a multiple of 32")
         return cls(torch.empty(rows, cols if kind == "e4m3" else cols // 2, dtype=torch.uint8, device=device),
                    torch.empty(rows, cols // 32, dtype=torch.uint8, device=device), kind)
-
-    @property
-    def shape(self):
-        return self.rows, self.cols
 
     def get_device(self):
         return self.device
@@ -111,10 +107,12 @@ def _matrix(x, what, shape):
         raise TypeError(f"{what} must be torch.float32 or torch.bfloat16, not {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if x.is_contiguous():
+        return dt, shape[1]
     row, one = x.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError(f"{what} must be contiguous in the last dimension")
-    return dt, row if shape[0] > 1 else shape[1] + -shape[1] % 8
+    return dt, row if shape[0] > 1 else shape[1]
 
 
 def mx_quantize(x, out: MXMatrix, stream=None):
@@ -144,30 +142,35 @@ def rms_norm(x, out, weight=None, residual=None, residual_out=None, eps=1e-6, st
         raise ValueError("x must be [rows][cols]")
     dt, xs = _matrix(x, "x", shape)
     gpu = x.get_device()
+    fine = gpu >= 0
     rp = rop = wp = op = mp = None
     rdt = rs = odt = os = 0
     if residual is not None:
         if residual_out is None:
             raise ValueError("a residual needs residual_out (it may be the residual)")
         rdt, rs = _matrix(residual, "residual", shape)
-        if residual_out is not residual and (residual_out.dtype is not residual.dtype or _matrix(residual_out, "residual_out", shape)[1] != rs):
-            raise ValueError("residual_out must have the type and strides of residual")
-        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+        rp = rop = residual.data_ptr()
+        fine = fine and residual.get_device() == gpu
+        if residual_out is not residual:
+            if _matrix(residual_out, "residual_out", shape) != (rdt, rs):
+                raise ValueError("residual_out must have the type and strides of residual")
+            rop = residual_out.data_ptr()
+            fine = fine and residual_out.get_device() == gpu
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
-        if weight.dtype is not torch.float32 or weight.shape != (shape[1],) or not weight.is_contiguous():
+        if weight.dtype is not torch.float32 or weight.dim() != 1 or weight.shape[0] != shape[1] or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous torch.float32 [{shape[1]}]")
         wp = weight.data_ptr()
+        fine = fine and weight.get_device() == gpu
     if isinstance(out, MXMatrix):
-        if out.shape != tuple(shape):
+        if out.shape != shape:
             raise ValueError(f"out must have shape {tuple(shape)}, not {out.shape}")
         mp = out.ref
     else:
         odt, os = _matrix(out, "out", shape)
         op = out.data_ptr()
-    if not (gpu == out.get_device() and gpu >= 0 and (residual is None or gpu == residual.get_device() == residual_out.get_device())
-            and (weight is None or weight.get_device() == gpu)):
+    if not (fine and out.get_device() == gpu):
         _same_gpu(gpu, ((out, "out"), (residual, "residual"), (residual_out, "residual_out"), (weight, "weight")))
     _check(L.moe_rms_norm(shape[0], shape[1], x.data_ptr(), dt, xs, rp, rop, rdt, rs, wp, eps, op, odt, os, mp,
                           _stream(stream, x)), "moe_rms_norm")
