@@ -273,6 +273,12 @@ class ExpertTable:
         for j, n in enumerate(names):
             self.tensor(e, j).copy_(torch.from_numpy(ex[n]))
 
+    def quantize(self, e: int, gate, up, down, stream=None):
+        """Expert e from its fp32 or bf16 weights on the GPU: gate, up [I][H] and down [H][I], each rounded to MXFP4 as
+        :func:`mx_quantize` does it, straight into the table."""
+        for j, w in ((0, gate), (2, up), (4, down)):
+            mx_quantize(w, MXMatrix(self.tensor(e, j), self.tensor(e, j + 1)), stream=stream)
+
     @property
     def ptr(self) -> int:
         return self.desc.data_ptr()
