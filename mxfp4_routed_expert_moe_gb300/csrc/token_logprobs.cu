@@ -11,16 +11,19 @@
 // would have a new one at nearly every step.  Threads, warps and the CTAs of a row
 // join their (m, c, S, U) in a fixed order.
 //
-// One comparison per eight logits decides whether there is more to do with them: a
+// One comparison per 16 logits of a thread decides whether there is more to do with them: a
 // far new maximum, logits ahead of the given token (which are counted one by one), or
 // candidates for the alternatives.  Those come from a bound that the first tile of a
 // piece gives: 128 maxima of disjoint groups of its logits, of which the top-th is
 // reached by at least `top` logits; whatever is not below it goes to a list, a few
-// times `top` of a row in random order.  A list that overflows (rows that grow with
+// times `top` of a row in random order, which gives better bounds on the way.  A list that overflows (rows that grow with
 // the index) is made again in small steps, thinned by the same bound.
 //
-// A cluster of 1 to 8 CTAs takes a row; logits are read once.  Bound by HBM and by
-// the instructions of a logit (nine) alike for many rows, by latency for one.
+// A cluster of 1 to 8 CTAs takes a row; logits are read once.  Bound by instructions
+// (seven a logit, nine where the given token is not among the best, and 4 to 8 us of
+// barriers and latencies a row) for many rows: 512 of 163,840 in bf16 take 64 us with
+// 20 alternatives, 41 without (4.1 TB/s); by latency for one: 100,003 logits, 8.8 us.
+// More warps an SM, or logits on their way through shared memory, were not faster.
 #include <cooperative_groups.h>
 
 #include <cuda/std/type_traits>
@@ -32,11 +35,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 2;                       // vectors of 8 logits that a thread has in flight (with 4 registers spill)
-constexpr int kList = 2048;
-constexpr int kGroups = kThreads / 4;
+constexpr int kGroups = 128;                     // of the first bound
 constexpr int kMaxCl = 8;
 constexpr int kTop = MOE_LOGPROBS_MAX_TOP;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -52,12 +52,15 @@ struct Stats {
   int count;
 };
 
+// Of a CTA of T threads.
+template <int T>
 struct ScoreShared {
+  static constexpr int kList = 4 * T;
   Key list[kList];
   Key group[kGroups];
   Key best[kTop];
   Key cl_best[kMaxCl * kTop];  // [CTA][top]
-  Stats warp[kWarps];
+  Stats warp[T / 32];
   Stats cl[kMaxCl];
   Key bound;
   uint32_t list_n;
@@ -194,8 +197,9 @@ __device__ __forceinline__ float most_of(const Eight<false> (&raw)[N]) {
 
 // f(key, rank) for each of n keys that differ (but for 0, none), a warp a key: rank is
 // the number of better ones.  Every lane calls f with the same.
-template <typename F>
+template <int T, typename F>
 __device__ __forceinline__ void ranks(const Key* keys, int n, F f) {
+  constexpr int kWarps = T / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (n <= 128) {  // a lane holds its share of them
     Key other[4];
@@ -224,31 +228,36 @@ __device__ __forceinline__ void ranks(const Key* keys, int n, F f) {
 // The top-th best of the 128 group maxima into sh.bound (0 where fewer groups
 // hold something), each thread giving the best key that it knows.  Barriers on
 // both sides.
-__device__ __forceinline__ void find_bound(ScoreShared& sh, Key mine, int top) {
-  mine = key_max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
-  mine = key_max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 2));
-  if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = mine;
+template <int T>
+__device__ __forceinline__ void find_bound(ScoreShared<T>& sh, Key mine, int top) {
+  constexpr int kLanes = T / kGroups;
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) mine = key_max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, o));
+  if (threadIdx.x % kLanes == 0) sh.group[threadIdx.x / kLanes] = mine;
   if (threadIdx.x == 0) sh.bound = 0ull;
   __syncthreads();
-  ranks(sh.group, kGroups, [&](Key k, int better) {
+  ranks<T>(sh.group, kGroups, [&](Key k, int better) {
     if (k && better == top - 1 && (threadIdx.x & 31) == 0) sh.bound = k;
   });
   __syncthreads();
 }
 
-__device__ __forceinline__ void list_add(ScoreShared& sh, Key k) {
+template <int T>
+__device__ __forceinline__ void list_add(ScoreShared<T>& sh, Key k) {
   const uint32_t i = atomicAdd(&sh.list_n, 1u);
-  if (i < kList) sh.list[i] = k;
+  if (i < ScoreShared<T>::kList) sh.list[i] = k;
 }
 
-// Drops from a list of up to kList keys what is below the bound of its groups;
-// at most 16 keys of each of `top` groups stay.  All threads; barriers inside.
-__device__ void thin(ScoreShared& sh, int top) {
+// Drops from a list of up to 4 T keys what is below the bound of its groups; the
+// keys of `top` groups stay at most, 4 T / 128 each: T at most, a quarter of the list.
+// All threads; barriers inside.
+template <int T>
+__device__ void thin(ScoreShared<T>& sh, int top) {
   const uint32_t n = sh.list_n;
-  Key k[kList / kThreads], most = 0ull;
+  Key k[4], most = 0ull;
 #pragma unroll
-  for (int j = 0; j < kList / kThreads; ++j) {
-    const uint32_t i = threadIdx.x + j * kThreads;
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t i = threadIdx.x + j * T;
     k[j] = i < n ? sh.list[i] : 0ull;
     most = key_max(most, k[j]);
   }
@@ -257,27 +266,30 @@ __device__ void thin(ScoreShared& sh, int top) {
   __syncthreads();
   const Key bound = sh.bound;
 #pragma unroll
-  for (int j = 0; j < kList / kThreads; ++j)
+  for (int j = 0; j < 4; ++j)
     if (k[j] && k[j] >= bound) list_add(sh, k[j]);
   __syncthreads();
 }
 
 // The top-th best key of the list so far into sh.bound, if it is short; at least
 // that many logits reach it.  All threads, barriers on both sides.
-__device__ __forceinline__ void tighten(ScoreShared& sh, int top) {
+template <int T>
+__device__ __forceinline__ void tighten(ScoreShared<T>& sh, int top) {
   __syncthreads();
   const int n = (int)sh.list_n;
-  if (n >= top && n <= kThreads)
-    ranks(sh.list, n, [&](Key k, int better) {
+  if (n >= top && n <= T)
+    ranks<T>(sh.list, n, [&](Key k, int better) {
       if (better == top - 1 && (threadIdx.x & 31) == 0) sh.bound = k;
     });
   __syncthreads();
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobParams p) {
-  constexpr int U = kUnroll, kTile = kThreads * U;
-  __shared__ ScoreShared sh;
+template <bool BF16, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(const LogprobParams p) {
+  constexpr int U = kUnroll, kTile = kThreads * U, kWarps = kThreads / 32, T = kThreads;
+  typedef ScoreShared<T> Shared;
+  constexpr int kList = Shared::kList;
+  __shared__ Shared sh;
   pdl_trigger();
   cg::cluster_group cluster = cg::this_cluster();
   const int cl = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     // Ranks by counting.
     if (tid < kTop) sh.best[tid] = 0ull;
     __syncthreads();
-    ranks(sh.list, (int)sh.list_n, [&](Key k, int better) {
+    ranks<T>(sh.list, (int)sh.list_n, [&](Key k, int better) {
       if (better < top && lane == 0) sh.best[better] = k;
     });
     __syncthreads();
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
   if (cl > 1) {
     cluster.sync();  // every CTA has started
     if (warp == 0) {
-      ScoreShared* o = cluster.map_shared_rank(&sh, 0);
+      Shared* o = cluster.map_shared_rank(&sh, 0);
       if (lane == 0) o->cl[rank] = st;
       if (lane < top) o->cl_best[rank * top + lane] = sh.best[lane];
     }
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
     if (top) {
       if (tid < kTop) sh.best[tid] = 0ull;
       __syncthreads();
-      ranks(sh.cl_best, cl * top, [&](Key k, int better) {
+      ranks<T>(sh.cl_best, cl * top, [&](Key k, int better) {
         if (k && better < top && lane == 0) sh.best[better] = k;
       });
     }
@@ -607,17 +619,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprobs(const LogprobPar
   }
 }
 
-template <bool BF16>
+template <bool BF16, int T>
 cudaError_t launch(LogprobParams p, cudaStream_t s) {
-  // CTAs of a row: as many as run at once with all rows' others, down to 4,096
-  // logits each.
+  // CTAs of a row: as many as run at once with all rows' others, down to 8 logits a
+  // thread.
   int cl = 1;
   auto piece = [&](int c) { return (p.vocab + c - 1) / c; };
-  while (cl < kMaxCl && 2ll * cl * p.rows <= 2 * kNumSMs && piece(cl) > 4096) cl *= 2;
+  while (cl < kMaxCl && 2ll * cl * p.rows <= 2 * kNumSMs && piece(cl) > 8 * T) cl *= 2;
   p.chunk = (piece(cl) + 7) & ~7;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p.rows * cl));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(T);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -627,13 +639,20 @@ cudaError_t launch(LogprobParams p, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16>, p);
+  return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, T>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, cudaStream_t s) {
-  return dtype == MOE_DT_BF16 ? launch<true>(p, s) : launch<false>(p, s);
+  // Many short rows by small CTAs, whose barriers and latencies overlap.  With 20
+  // alternatives, us by CTAs of 128 / 256 / 512 threads: 4,096 rows of 1,000: 42 / 59 /
+  // 99, of 4,099: 75 / 74 / 104, of 16,000: 134 / 124 / 132, 1,024 of 64,000: 81 / 72 /
+  // 69, 320 of 163,840: 246 / 73 / 52.
+  const bool many = p.rows > 2 * kNumSMs;
+  if (many && p.vocab <= 2048) return dtype == MOE_DT_BF16 ? launch<true, 128>(p, s) : launch<false, 128>(p, s);
+  if (many && p.vocab <= 16384) return dtype == MOE_DT_BF16 ? launch<true, 256>(p, s) : launch<false, 256>(p, s);
+  return dtype == MOE_DT_BF16 ? launch<true, 512>(p, s) : launch<false, 512>(p, s);
 }
 
 }  // namespace moe
