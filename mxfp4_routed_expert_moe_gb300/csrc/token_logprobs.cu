@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
   float zt = -INFINITY, ahead_before = INFINITY, ahead_after = INFINITY;
   if (known) {
     zt = BF16 ? bf16_f32(__ldg((const uint16_t*)row + token)) : __ldg((const float*)row + token);
-    zt = fmaxf(zt, -INFINITY);  // NaN as -inf
+    zt = fmaxf(zt, -INFINITY) + 0.f;  // NaN as -inf, -0 as 0: a difference's sign tells what is ahead
     ahead_after = zt;
     // Logits before the token are ahead where they are equal, too: above the next
     // lower number.  (All of them, where the token's is -inf: added at the end.)

@@ -179,3 +179,45 @@ def test_outputs_one_by_one_and_repeat(moe):
     graph.replay()
     t.cuda.synchronize()
     assert np.array_equal(ref.host(logprob), run(moe, x, tokens.tolist(), 0)["logprob"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("token_at", [0, 7, 900, 2999])
+def test_signed_zeros_are_equal(moe, dtype, token_at):
+    """0 and -0 tie, whichever of them the token's is: the index decides."""
+    t = torch()
+    vocab = 3001
+    x = np.full((4, vocab), -1.0, dtype=np.float32)
+    x[0, ::3], x[1, ::3] = 0.0, -0.0
+    x[2], x[3] = np.where(np.arange(vocab) % 2, -0.0, 0.0), np.where(np.arange(vocab) % 2, 0.0, -0.0)
+    x[0, token_at], x[1, token_at] = -0.0, 0.0
+    logits = t.from_numpy(x).cuda().to(t.float32 if dtype == "f32" else t.bfloat16)
+    check(moe, logits, np.full(4, token_at), 20)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [37, 999, 2048, 2049, 9001, 16384])
+def test_awkward_rows_among_many(moe, dtype, vocab):
+    """Batches whose rows are short take smaller groups of threads: the same rows there, in turn."""
+    t = torch()
+    rng = np.random.default_rng(vocab)
+    rows = 330
+    x = rng.standard_normal((rows, vocab)).astype(np.float32)
+    at = np.arange(vocab)
+    for r in range(0, rows, 11):
+        x[r] = 0.25
+        x[r + 1] = at * 0.001
+        x[r + 2] = at * -0.001
+        x[r + 3] = -np.inf
+        x[r + 4] = np.where(at == (r * 17) % vocab, 3, -np.inf)
+        x[r + 5] = np.finfo(np.float32).min
+        x[r + 5, r % vocab] = 1
+        x[r + 6, [r % vocab, vocab - 1]] = np.inf
+        x[r + 7, rng.integers(0, vocab, vocab // 3)] = np.nan
+        x[r + 8] = rng.integers(-2, 3, vocab)
+        x[r + 9] *= 1e30
+    logits = t.from_numpy(x).cuda().to(t.float32 if dtype == "f32" else t.bfloat16)
+    tokens = rng.integers(0, vocab, rows)
+    tokens[5::22] = np.arange(5, rows, 22) % vocab
+    for top in (1, 32):
+        check(moe, logits, tokens, top)
