@@ -35,8 +35,8 @@ int check_rows(const void* x, int dtype, int64_t stride, int rows, int cols, boo
 
 MxRows rows_of(const moe_mx& a) { return {a.q, a.s, a.q_stride, a.s_stride}; }
 
-// Eights of values that one launch of the conversions covers.
-bool too_many(const moe_mx* a) { return (int64_t)a->rows * (a->cols / 8) >= ((int64_t)1 << 32) - 256; }
+// Eights of values that one launch of the conversions covers: its CTAs' last counts stay in 32 bits.
+bool too_many(const moe_mx* a) { return (int64_t)a->rows * (a->cols / 8) >= ((int64_t)1 << 32) - 1024; }
 
 }  // namespace
 

@@ -19,7 +19,8 @@ namespace {
 constexpr int kThreads = 256;
 
 // Unit u of eight values: row and place in the row.  WHOLE: rows follow one another
-// without gaps in all operands, and count as one.
+// without gaps in all operands, and count as one (of less than 2^34 values: a place
+// in it counts 16-byte vectors, two an eight, in 32 bits).
 template <bool WHOLE>
 __device__ __forceinline__ void place(uint32_t u, uint32_t per_row, uint32_t& row, uint32_t& c8) {
   row = WHOLE ? 0u : u / per_row;
@@ -127,8 +128,9 @@ template <typename D, bool BF16, bool E4M3>
 cudaError_t launch(const QuantizeParams& p, cudaStream_t s) {
   const uint32_t per_row = p.cols / 8;
   const uint32_t units = (uint32_t)((uint64_t)p.rows * per_row);
-  const bool whole = p.rows == 1 || (p.stride == (int64_t)p.cols * (BF16 ? 2 : 4) && p.mx.q_stride == (E4M3 ? p.cols : p.cols / 2) &&
-                                     p.mx.s_stride == p.cols / 32);
+  const bool whole = units < 1u << 31 &&
+                     (p.rows == 1 || (p.stride == (int64_t)p.cols * (BF16 ? 2 : 4) &&
+                                      p.mx.q_stride == (E4M3 ? p.cols : p.cols / 2) && p.mx.s_stride == p.cols / 32));
   const int per = units > 4u * kThreads * 4 * kNumSMs ? 4 : 1;
   auto kern = whole ? (per == 4 ? D::template kernel<BF16, E4M3, true, 4>() : D::template kernel<BF16, E4M3, true, 1>())
                     : (per == 4 ? D::template kernel<BF16, E4M3, false, 4>() : D::template kernel<BF16, E4M3, false, 1>());

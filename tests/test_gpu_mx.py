@@ -215,3 +215,94 @@ def test_norm_strides_graph_and_repeat(moe):
     graph.replay()
     t.cuda.synchronize()
     assert t.equal(out, first)
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_strided_matrices(moe, kind, dtype):
+    """Enough values for several a thread, in rows with gaps on either side."""
+    t = torch()
+    rows, cols = 2600, 7168
+    wide = t.randn(rows, cols + 64, generator=t.Generator("cuda").manual_seed(5), device="cuda").to(dtype_of(dtype))
+    per = cols if kind == "e4m3" else cols // 2
+    q = t.full((rows, per + 32), 0x77, dtype=t.uint8, device="cuda")
+    s = t.full((rows, cols // 32 + 1), 0x77, dtype=t.uint8, device="cuda")
+    out = moe.MXMatrix(q[:, :per], s[:, :cols // 32], kind)
+    moe.mx_quantize(wide[:, 32:32 + cols], out)
+    whole = moe.MXMatrix.empty(rows, cols, kind)
+    moe.mx_quantize(wide[:, 32:32 + cols].contiguous(), whole)
+    assert t.equal(out.q, whole.q) and t.equal(out.s, whole.s)
+    assert t.all(q[:, per:] == 0x77) and t.all(s[:, cols // 32:] == 0x77)
+    some = [0, 1, 777, rows - 1]
+    code, sc = ref.quantize(ref.host(wide[some, 32:32 + cols]), kind)
+    assert np.array_equal(out.q[some].cpu().numpy(), ref.pack(code, kind)) and np.array_equal(out.s[some].cpu().numpy(), sc)
+    y, back = t.empty(rows, cols, device="cuda"), t.full((rows, cols + 8), 5.0, device="cuda")
+    moe.mx_dequantize(whole, y)
+    moe.mx_dequantize(out, back[:, :cols])
+    assert t.equal(back[:, :cols], y) and t.all(back[:, cols:] == 5)
+    assert np.array_equal(ref.host(y[some]), ref.values(code, sc, kind))
+
+
+def test_more_than_2_to_34_values(moe):
+    """Offsets past 32 bits: the ends of a matrix of 64 GiB of fp32, to MXFP4 and back over itself."""
+    t = torch()
+    t.cuda.empty_cache()
+    if t.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GiB")
+    rows, cols, n = (1 << 20) + 32, 16384, 32
+    x = t.empty(rows, cols, device="cuda")
+    g = t.Generator("cuda").manual_seed(3)
+    ends = [slice(0, n), slice(rows - n, rows)]
+    for e in ends:
+        x[e] = t.randn(n, cols, generator=g, device="cuda")
+    want = [ref.quantize(ref.host(x[e]), "e2m1") for e in ends]
+    out = moe.MXMatrix.empty(rows, cols)
+    moe.mx_quantize(x, out)
+    for e, (code, s) in zip(ends, want):
+        assert np.array_equal(out.q[e].cpu().numpy(), ref.pack(code, "e2m1")) and np.array_equal(out.s[e].cpu().numpy(), s)
+    for e in ends:
+        x[e] = 0
+    moe.mx_dequantize(out, x)
+    for e, (code, s) in zip(ends, want):
+        assert np.array_equal(ref.host(x[e]), ref.values(code, s, "e2m1"))
+    del x, out
+    t.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("cols", [64, 256, 512, 768])
+def test_norm_of_extreme_narrow_rows(moe, cols):
+    """Rows that a warp takes: what one holds does not reach its neighbours."""
+    t = torch()
+    x = t.randn(21, cols, generator=t.Generator("cuda").manual_seed(cols), device="cuda")
+    x[1] *= 1e25
+    x[2] *= 3e37
+    x[4, 7] = float("inf")
+    x[5, 9] = float("nan")
+    x[8] = 0
+    x[20] *= 1e-30
+    out = t.empty_like(x)
+    moe.rms_norm(x, out)
+    h = ref.host(x)
+    rows = [r for r in range(21) if r not in (4, 5)]
+    y = h[rows] / np.sqrt((h[rows] ** 2).mean(1, keepdims=True) + 1e-6)
+    assert np.all(np.abs(ref.host(out)[rows] - y) <= FP32 * np.abs(y) + 1e-38)
+    assert out[4, 7].isnan() and t.all(out[4, :7] == 0) and t.all(out[4, 8:] == 0) and out[5].isnan().all()
+    mx = moe.MXMatrix.empty(21, cols, "e4m3")
+    moe.rms_norm(x, mx)
+    assert t.all(mx.s[5] == 255) and mx.s[4, 0] == 255 and t.all(mx.s[4, 1:] == 0) and t.all(mx.s[rows] != 255)
+
+
+@pytest.mark.parametrize("cols", [7, 40, 100, 1000])
+def test_norm_of_many_rows(moe, cols):
+    """More rows than CTAs at once, a broadcast x, the residual's place taken by the result."""
+    t = torch()
+    cols *= 8
+    g = t.Generator("cuda").manual_seed(cols)
+    x, res = t.randn(1, cols, generator=g, device="cuda").bfloat16(), t.randn(5003, cols, generator=g, device="cuda")
+    h = ref.host(x) + ref.host(res)
+    y = h / np.sqrt((h * h).mean(1, keepdims=True) + 1e-5)
+    ro = t.empty_like(res)
+    moe.rms_norm(x.expand(5003, cols), res, residual=res, residual_out=ro, eps=1e-5)
+    assert np.all(np.abs(ref.host(ro) - h) <= 2.0 ** -24 * np.abs(h))
+    # h, the sum, errs by 2^-24 of itself.
+    assert np.all(np.abs(ref.host(res) - y) <= FP32 * np.abs(y))
