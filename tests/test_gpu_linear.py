@@ -214,3 +214,57 @@ def test_a_wait_that_runs_out_is_reported(moe):
         status.zero_()
         moe.mx_linear(x, w, out, status=status)
         assert int(status.item()) == 0 and t.equal(out, good)
+
+
+@pytest.mark.parametrize("T,N,K,kind", [(65536, 130, 128, "e2m1"), (65536, 257, 256, "e4m3"), (3, 262144, 128, "e4m3"), (300, 262144, 128, "e2m1"),
+                                        (1, 1, 16384, "e4m3"), (2000, 1, 256, "e2m1"), (9000, 3, 128, "e4m3")])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_largest_and_thinnest(moe, T, N, K, kind, out):
+    """The largest counts of rows and results, and single columns, with one addend for all rows; rows at both ends and in
+    between are compared."""
+    t = torch()
+    rng = np.random.default_rng(T + N)
+    xc, xs = ref.random_mx(rng, T, K, kind)
+    wc, ws = ref.random_mx(rng, N, K, "e2m1")
+    dt = t.float32 if out == "f32" else t.bfloat16
+    bias = t.from_numpy(rng.standard_normal((1, N)).astype(np.float32) * 30).cuda().to(dt)
+    got = t.full((T, N), float("nan"), dtype=dt, device="cuda")
+    moe.mx_linear(ref.matrix(moe, xc, xs, kind), ref.matrix(moe, wc, ws, "e2m1"), got, add=bias.expand(T, N))
+    assert not got.isnan().any()
+    r = np.unique(np.r_[np.arange(min(T, 70)), rng.integers(0, T, 60), np.arange(max(T - 70, 0), T)])
+    c = np.unique(np.r_[np.arange(min(N, 300)), rng.integers(0, N, 60), np.arange(max(N - 300, 0), N)])
+    y, mag = product(ref.values(xc[r], xs[r], kind), ref.values(wc[c], ws[c], "e2m1"))
+    b = ref.host(bias)[:, c]
+    y, mag = y + b, mag + np.abs(b)
+    assert np.all(np.abs(ref.host(got[r][:, c]) - y) <= bound(kind, K, mag, y, out))
+
+
+def test_calls_at_once_on_two_streams(moe):
+    """Products of both forms side by side on two streams, many times, one of them captured: the same bits."""
+    t = torch()
+    rng = np.random.default_rng(12)
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    jobs = []
+    for T, N, K, kind in ((3, 7168, 2048, "e4m3"), (1100, 2600, 512, "e2m1"), (40, 1300, 7168, "e4m3"), (500, 7168, 256, "e4m3")):
+        xc, xs = ref.random_mx(rng, T, K, kind)
+        wc, ws = ref.random_mx(rng, N, K, "e2m1")
+        x, w = ref.matrix(moe, xc, xs, kind), ref.matrix(moe, wc, ws, "e2m1")
+        want = t.empty(T, N, device="cuda")
+        moe.mx_linear(x, w, want)
+        jobs.append((x, w, want, [t.zeros_like(want) for _ in streams]))
+    status = t.zeros(1, dtype=t.int32, device="cuda")
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph, stream=streams[0]):
+        for x, w, _, outs in jobs:
+            moe.mx_linear(x, w, outs[0], status=status)
+    t.cuda.synchronize()
+    for _ in range(20):
+        with t.cuda.stream(streams[0]):
+            graph.replay()
+        for x, w, _, outs in reversed(jobs):
+            moe.mx_linear(x, w, outs[1], status=status, stream=streams[1])
+    t.cuda.synchronize()
+    assert int(status.item()) == 0
+    for _, _, want, outs in jobs:
+        assert all(t.equal(o, want) for o in outs)
