@@ -168,7 +168,7 @@ template <bool XB, bool R, bool RB, int OUT>
 cudaError_t launch(const NormParams& p, cudaStream_t s) {
   const int per_row = p.cols / 8, eights = (per_row + 31) / 32;
   if (eights <= kWarpEights) {
-    const dim3 grid((unsigned)((p.rows + kWarpRows - 1) / kWarpRows)), block(kWarpRows * 32);
+    const dim3 grid(((unsigned)p.rows + kWarpRows - 1) / kWarpRows), block(kWarpRows * 32);
     if (eights <= 1) return launch_pdl(k_rms_norm<XB, R, RB, OUT, 1, true>, grid, block, 0, s, p);
     return launch_pdl(k_rms_norm<XB, R, RB, OUT, kWarpEights, true>, grid, block, 0, s, p);
   }

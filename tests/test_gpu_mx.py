@@ -306,3 +306,24 @@ def test_norm_of_many_rows(moe, cols):
     assert np.all(np.abs(ref.host(ro) - h) <= 2.0 ** -24 * np.abs(h))
     # h, the sum, errs by 2^-24 of itself.
     assert np.all(np.abs(ref.host(res) - y) <= FP32 * np.abs(y))
+
+
+def test_norm_of_the_most_rows(moe):
+    """2^31 - 1 rows, 32 GiB of bf16, in place: its ends."""
+    t = torch()
+    t.cuda.empty_cache()
+    if t.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GiB")
+    rows, n = (1 << 31) - 1, 1000
+    x = t.empty(rows, 8, dtype=t.bfloat16, device="cuda")
+    g = t.Generator("cuda").manual_seed(6)
+    ends = [slice(0, n), slice(rows - n, rows)]
+    for e in ends:
+        x[e] = t.randn(n, 8, generator=g, device="cuda").bfloat16()
+    h = [ref.host(x[e]) for e in ends]
+    moe.rms_norm(x, x)
+    for e, v in zip(ends, h):
+        y = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6)
+        assert np.all(np.abs(ref.host(x[e]) - y) <= (FP32 + STEP["bf16"]) * np.abs(y))
+    del x
+    t.cuda.empty_cache()
