@@ -98,7 +98,8 @@ int moe_rms_norm(int rows, int cols, const void* x, int x_dtype, int64_t x_strid
  *   w         [N][K], MOE_MX_E2M1
  *   add       NULL, or [T][N] of out's type; may be out itself
  *   out       [T][N], MOE_DT_F32 or MOE_DT_BF16, *_stride elements between rows
- *             (rows of out must not overlap); any alignment of its type
+ *             (rows of out must not overlap); any alignment of its type.  Other
+ *             overlaps of out with the operands are the caller's to avoid.
  *   status    a DEVICE int32 or NULL, as in moe_serve.h (MOE_ERR_TIMEOUT: a
  *             bounded wait gave up)
  * K: a multiple of 128.  Codes are 32-byte aligned with row strides a multiple

@@ -28,6 +28,7 @@
 
 #include <cuda/std/type_traits>
 
+#include "async.cuh"
 #include "dense.cuh"
 
 namespace moe {
@@ -272,16 +273,17 @@ __device__ void thin(ScoreShared<T>& sh, int top) {
 }
 
 // The top-th best key of the list so far into sh.bound, if it is short; at least
-// that many logits reach it.  All threads, barriers on both sides.
+// that many logits reach it.  All threads, barriers on both sides: named ones, which
+// warps may reach by different ways through the code.
 template <int T>
 __device__ __forceinline__ void tighten(ScoreShared<T>& sh, int top) {
-  __syncthreads();
+  named_sync(1, T);
   const int n = (int)sh.list_n;
   if (n >= top && n <= T)
     ranks<T>(sh.list, n, [&](Key k, int better) {
       if (better == top - 1 && (threadIdx.x & 31) == 0) sh.bound = k;
     });
-  __syncthreads();
+  named_sync(1, T);
 }
 
 template <bool BF16, int kThreads>
