@@ -148,6 +148,8 @@ __device__ __forceinline__ uint32_t remote_smem(const void* p, int rank) {
   return a;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// Without waiting for this thread's stores (1 to 2 us behind results).
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Tensor-map load into this CTA's shared memory, its bytes counted on a barrier of
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
 
   // Results in fours, kUnits a thread at a time; their addends are read before the
   // sums are waited for, and all before the first store, which may be to the same place.
-  constexpr int kUnits = 4;
+  constexpr int kUnits = 8;
   const int units = mine * (kRows / 4);
   const bool wide = wide_rows<OUT_BF16>(p);
   float4 add[kUnits];
@@ -598,12 +600,12 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
     const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
     float* stage = reinterpret_cast<float*>(ring);
     float* recv = reinterpret_cast<float*>(ring + t.recv_off);
-    for (int c0 = 0; c0 < valid; c0 += 16) {
-      uint32_t v[16];
-      tmem_ld16(tbase + (uint32_t)c0, v);
+    for (int c0 = 0; c0 < valid; c0 += 32) {
+      uint32_t v[32];
+      tmem_ld32(tbase + (uint32_t)c0, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
+      for (int e = 0; e < 32; ++e)
         if (c0 + e < valid) stage[(c0 + e) * kRows + q * 32 + lane] = fine ? __uint_as_float(v[e]) : 0.f;
     }
     tc_fence_before();
@@ -616,7 +618,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
           bulk_s2s(remote_smem(recv + (size_t)(rank < etid ? rank : rank - 1) * own * kRows, etid), stage + o0 * kRows,
                    (uint32_t)(n * kRows * 4), remote_smem(&sh.recv, etid));
       }
-      lin_warp_wait(c, &sh.recv, 0);
+      // No CTA leaves before all sums have arrived: told as soon as they have.
+      if (!lin_warp_wait(c, &sh.recv, 0)) let_copies_land(sh);
+      __syncwarp();
+      cluster_arrive_relaxed();
     }
     for (int i0 = etid; i0 < units; i0 += kUnits * kSfWarps * 32) {
       if (i0 != etid) addends(i0);
@@ -635,15 +640,14 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
         put4<OUT_BF16>(p, t0 + own0 + tt, n0 + r4, y, wide);
       }
     }
+  } else if (cl > 1) {
+    cluster_arrive_relaxed();
   }
   tc_fence_before();
   __syncthreads();
   let_copies_land(sh);
   __syncwarp();
-  if (cl > 1) {
-    cluster_arrive();
-    cluster_wait();  // no CTA leaves while its sums are being copied
-  }
+  if (cl > 1) cluster_wait();
   if (warp == kMmaWarp) {
     tc_fence_after();
     lin_dealloc<1>(tmem, t.tmem_cols);
