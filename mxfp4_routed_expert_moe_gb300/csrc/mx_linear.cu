@@ -403,56 +403,36 @@ __device__ __forceinline__ void let_copies_land(const LinShared& sh) {
   }
 }
 
-// Four neighbouring addends, or results, of a row from n on.
+// Four neighbouring addends, or results, as they are held.
 template <bool OUT_BF16>
-__device__ __forceinline__ float4 get4(const LinearParams& p, int64_t t, int n, bool wide) {
-  if (wide && n + 4 <= p.N) {
-    if (OUT_BF16) {
-      const uint2 a = *reinterpret_cast<const uint2*>((const uint16_t*)p.add + t * p.add_stride + n);
-      return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
-                         __uint_as_float(a.y & 0xFFFF0000u));
-    }
-    return *reinterpret_cast<const float4*>((const float*)p.add + t * p.add_stride + n);
+struct Four;
+template <>
+struct Four<true> {
+  typedef uint2 Raw;
+  typedef uint16_t One;
+  static __device__ __forceinline__ float4 get(const uint2& a) {
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                       __uint_as_float(a.y & 0xFFFF0000u));
   }
-  float v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = 0.f;
-    if (n + e < p.N)
-      v[e] = OUT_BF16 ? bf16_f32(((const uint16_t*)p.add)[t * p.add_stride + n + e]) : ((const float*)p.add)[t * p.add_stride + n + e];
-  }
-  return make_float4(v[0], v[1], v[2], v[3]);
-}
-template <bool OUT_BF16>
-__device__ __forceinline__ void put4(const LinearParams& p, int64_t t, int n, float4 y, bool wide) {
-  if (wide && n + 4 <= p.N) {
-    if (OUT_BF16)
-      *reinterpret_cast<uint2*>((uint16_t*)p.out + t * p.out_stride + n) = make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w));
-    else
-      *reinterpret_cast<float4*>((float*)p.out + t * p.out_stride + n) = y;
-    return;
-  }
-  const float v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (n + e < p.N) {
-      if (OUT_BF16)
-        ((uint16_t*)p.out)[t * p.out_stride + n + e] = (uint16_t)(bf16x2_rn(v[e], 0.f) & 0xFFFFu);
-      else
-        ((float*)p.out)[t * p.out_stride + n + e] = v[e];
-    }
-}
+  static __device__ __forceinline__ uint2 put(const float4& y) { return make_uint2(bf16x2_rn(y.x, y.y), bf16x2_rn(y.z, y.w)); }
+  static __device__ __forceinline__ float get1(uint16_t a) { return bf16_f32(a); }
+  static __device__ __forceinline__ uint16_t put1(float y) { return (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu); }
+};
+template <>
+struct Four<false> {
+  typedef float4 Raw;
+  typedef float One;
+  static __device__ __forceinline__ float4 get(const float4& a) { return a; }
+  static __device__ __forceinline__ float4 put(const float4& y) { return y; }
+  static __device__ __forceinline__ float get1(float a) { return a; }
+  static __device__ __forceinline__ float put1(float y) { return y; }
+};
 // One column's results of up to 32 rows from row t on.
 template <bool OUT_BF16>
 __device__ __forceinline__ void put_column(const LinearParams& p, int64_t t, int n, const uint32_t (&v)[32], int count) {
-  typedef typename std::conditional<OUT_BF16, uint16_t, float>::type T;
+  typedef typename Four<OUT_BF16>::One T;
   T* o = (T*)p.out + t * p.out_stride + n;
-  auto put = [&](int e, float y) {
-    if constexpr (OUT_BF16)
-      o[e * p.out_stride] = (uint16_t)(bf16x2_rn(y, 0.f) & 0xFFFFu);
-    else
-      o[e * p.out_stride] = y;
-  };
+  auto put = [&](int e, float y) { o[e * p.out_stride] = Four<OUT_BF16>::put1(y); };
   if (!p.add) {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
@@ -468,25 +448,19 @@ __device__ __forceinline__ void put_column(const LinearParams& p, int64_t t, int
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       a[e] = 0.f;
-      if (e0 + e < count) {
-        const T x = ad[(e0 + e) * p.add_stride];
-        if constexpr (OUT_BF16)
-          a[e] = bf16_f32(x);
-        else
-          a[e] = x;
-      }
+      if (e0 + e < count) a[e] = Four<OUT_BF16>::get1(ad[(e0 + e) * p.add_stride]);
     }
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       if (e0 + e < count) put(e0 + e, __uint_as_float(v[e0 + e]) + a[e]);
   }
 }
-// Whether all groups of four of all rows of out and the addend are aligned.
+// Whether rows of out and the addend are whole groups of four, all aligned.
 template <bool OUT_BF16>
 __device__ __forceinline__ bool wide_rows(const LinearParams& p) {
   const uintptr_t size = OUT_BF16 ? 2 : 4;
   const uintptr_t bits = (uintptr_t)p.out | (uintptr_t)(p.out_stride * size) | (p.add ? (uintptr_t)p.add | (uintptr_t)(p.add_stride * size) : 0);
-  return (bits & (4 * size - 1)) == 0;
+  return (bits & (4 * size - 1)) == 0 && p.N % 4 == 0;
 }
 
 // --------------------------------------------------------------------- clusters --
@@ -545,18 +519,22 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   }
   pdl_wait();
 
-  // Results in fours, kUnits a thread at a time; their addends are read before the
-  // sums are waited for, and all before the first store, which may be to the same place.
-  constexpr int kUnits = 8;
-  const int units = mine * (kRows / 4);
-  const bool wide = wide_rows<OUT_BF16>(p);
-  float4 add[kUnits];
-  auto addends = [&](int i0) {
+  // Results: a thread takes four neighbouring columns of rows 4 apart, kUnits rows at a
+  // time; their addends are read before the sums are waited for, and all before the
+  // first store, which may be to the same place.
+  typedef Four<OUT_BF16> F;
+  typedef typename F::Raw Raw;
+  constexpr int kUnits = 8, kApart = kSfWarps * 32 * 4 / kRows;
+  const int tt0 = (tid - kSfWarp0 * 32) / (kRows / 4), col4 = tid % (kRows / 4) * 4;
+  const bool wide = wide_rows<OUT_BF16>(p), live = n0 + col4 < p.N;
+  Raw add[kUnits];
+  auto addends = [&](int tb) {
+    const Raw* from = (const Raw*)((const typename F::One*)p.add + (int64_t)(t0 + own0 + tb) * p.add_stride + n0 + col4);
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      const int i = i0 + k * kSfWarps * 32;
-      add[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.add && i < units) add[k] = get4<OUT_BF16>(p, t0 + own0 + i / (kRows / 4), n0 + i % (kRows / 4) * 4, wide);
+      add[k] = Raw();
+      if (p.add && wide && live && tb + kApart * k < mine)
+        add[k] = *(const Raw*)((const typename F::One*)from + (int64_t)(kApart * k) * p.add_stride);
     }
   };
   bool fine = false;
@@ -588,7 +566,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       scales_of_tile<1, kSfWarp0, true>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
     else
       scales_of_tile<1, kSfWarp0, false>(p, t, c, swap, tmem, n0, t0, w0, steps, sf, step, ok);
-    addends(tid - kSfWarp0 * 32);
+    addends(tt0);
     fine = lin_warp_wait(c, &sh.sums, 0) && ns > 0;
     tc_fence_after();
   }
@@ -623,21 +601,48 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       __syncwarp();
       cluster_arrive_relaxed();
     }
-    for (int i0 = etid; i0 < units; i0 += kUnits * kSfWarps * 32) {
-      if (i0 != etid) addends(i0);
+    // In rank order.
+    auto part = [&](int j) { return j == rank ? stage + own0 * kRows : recv + (size_t)(j < rank ? j : j - 1) * own * kRows; };
+    auto results = [&](auto units) {
+      constexpr int U = decltype(units)::value;
+      for (int tb = tt0; live && tb < mine; tb += U * kApart) {
+        if (tb != tt0) addends(tb);
+        float4 y[U];
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        const int i = i0 + k * kSfWarps * 32;
-        if (i >= units) break;
-        const int tt = i / (kRows / 4), r4 = i % (kRows / 4) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < U; ++k) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int j = 0; j < cl; ++j) {
-          const float* from = j == rank ? stage + (own0 + tt) * kRows : recv + ((size_t)(j < rank ? j : j - 1) * own + tt) * kRows;
-          const float4 a = *reinterpret_cast<const float4*>(from + r4);
-          y.x += a.x, y.y += a.y, y.z += a.z, y.w += a.w;
+          const float* from = part(j) + tb * kRows + col4;
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            if (tb + kApart * k < mine) {
+              const float4 a = *reinterpret_cast<const float4*>(from + kApart * k * kRows);
+              y[k].x += a.x, y[k].y += a.y, y[k].z += a.z, y[k].w += a.w;
+            }
         }
-        y.x += add[k].x, y.y += add[k].y, y.z += add[k].z, y.w += add[k].w;
-        put4<OUT_BF16>(p, t0 + own0 + tt, n0 + r4, y, wide);
+        typename F::One* to = (typename F::One*)p.out + (int64_t)(t0 + own0 + tb) * p.out_stride + n0 + col4;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          if (tb + kApart * k < mine) {
+            const float4 a = F::get(add[k]);
+            y[k].x += a.x, y[k].y += a.y, y[k].z += a.z, y[k].w += a.w;
+            *(Raw*)(to + (int64_t)(kApart * k) * p.out_stride) = F::put(y[k]);
+          }
+      }
+    };
+    if (wide) {
+      if (mine <= kApart)
+        results(std::integral_constant<int, 1>());
+      else
+        results(std::integral_constant<int, kUnits>());
+    } else if (n0 + etid < p.N) {  // a column a thread
+#pragma unroll 1
+      for (int tt = 0; tt < mine; ++tt) {
+        const int64_t t1 = t0 + own0 + tt;
+        float y = 0.f;
+        for (int j = 0; j < cl; ++j) y += part(j)[tt * kRows + etid];
+        if (p.add) y += F::get1(((const typename F::One*)p.add)[t1 * p.add_stride + n0 + etid]);
+        ((typename F::One*)p.out)[t1 * p.out_stride + n0 + etid] = F::put1(y);
       }
     }
   } else if (cl > 1) {
