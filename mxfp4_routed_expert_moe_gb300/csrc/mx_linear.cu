@@ -878,16 +878,18 @@ cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cuda
     while (t.tmem_cols < t.nt + (uint32_t)(kSfRing * 16 * (1 + t.nb))) t.tmem_cols *= 2;
     return tiles_t;
   };
-  // Clusters where the inner size can be cut in two or more with all CTAs on the chip
-  // at once, in tiles of up to 64 activation rows; pairs otherwise, in the smallest
-  // tiles that still make one round of the chip.  Measured, inner size 7,168, MXFP8
-  // activations (us, clusters / pairs): 1 and 16 x 9,216: 9.7 / -, 10.3 / 16.5; 64 x
-  // 7,168: 12.5 / 16.4; 64 x 16,384 (no room for a cut): 21.0 / 17.9; 128 x 9,216:
-  // 18.5 / 17.4; 256 x 1,408: 11.3 / 25; 256 x 9,216: 26.4 / 19.5 (tiles of 128;
-  // 23.3 of 256).  MXFP4 activations: 64 x 9,216: 11.7 / 10.8; 256 x 7,168: 19.8 / 12.7.
+  // Clusters, of one CTA where the inner size is not cut, while all tiles of up to 64
+  // activation rows are on the chip at once (two an SM of up to 32 rows); pairs
+  // otherwise, in the smallest tiles that still make one round of the chip, and for
+  // MXFP4 activations of more than 32 rows where clusters would not cut.  Measured,
+  // inner size 7,168, MXFP8 activations (us, clusters / pairs): 16 x 9,216: 10.2 / 16.5;
+  // 64 x 7,168: 10.8 / 18.3; 256 x 1,408: 9.6 / 17.1; uncut, 1 x 16,384: 15.6 / 17.8;
+  // 64 x 19,456: 18.6 / 19.5; 128 x 9,216: 17.4 / 18.6.  MXFP4 activations: 64 x 9,216:
+  // 10.1 / 12.0; uncut, 1 x 16,384: 12.1 / 13.2; 64 x 19,456: 16.2 / 15.6.
   const int rows = up(p.N, kRows), pair_rows = up(p.N, 2 * kRows);
   const long long tiles = (long long)rows * up(p.T, 64);
-  if (2 * tiles > kNumSMs) {
+  const bool few = p.T <= 32, cut = 2 * tiles <= kNumSMs;
+  if (!(cut || (tiles <= kNumSMs && !F4) || (tiles <= 2 * kNumSMs && few))) {
     int nt = 32;
     while (nt < kMaxNt && (long long)pair_rows * up(p.T, nt) > kPairs) nt *= 2;
     const int tiles_t = shape(nt, 32, 2);
@@ -904,8 +906,8 @@ cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cuda
   t.tiles_n = rows;
   t.tiles = (int)tiles;
   // CTAs of a tile: as many as fit with one CTA an SM, or two where that leaves fewer
-  // SMs idle and the rings are small (1 x 7,168: 112 CTAs 9.2 us, 280 CTAs 7.7;
-  // 64 x 7,168: 12.5 and 14.2); two slices each at least.
+  // SMs idle and the rings are small (1 x 7,168: 112 CTAs 8.9 us, 280 CTAs 8.3;
+  // 64 x 7,168: 10.9 and 14.3); two slices each at least.
   auto fit = [&](int ctas) {
     int c = (int)(ctas / tiles);
     c = c < kMaxCl ? c : kMaxCl;
