@@ -881,7 +881,10 @@ cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cuda
   // Clusters, of one CTA where the inner size is not cut, while all tiles of up to 64
   // activation rows are on the chip at once (two an SM of up to 32 rows); pairs
   // otherwise, in the smallest tiles that still make one round of the chip, and for
-  // MXFP4 activations of more than 32 rows where clusters would not cut.  Measured,
+  // MXFP4 activations of more than 32 rows where clusters would not cut.  Up to 32 rows
+  // of MXFP8 take several rounds of the chip that way, too, if the inner size is long:
+  // a pair's MMAs do not get faster with fewer rows (1 x 163,840: 106 us, pairs 126;
+  // inner size 1,408, 30 x 262,144: 53 and 46).  Measured,
   // inner size 7,168, MXFP8 activations (us, clusters / pairs): 16 x 9,216: 10.2 / 16.5;
   // 64 x 7,168: 10.8 / 18.3; 256 x 1,408: 9.6 / 17.1; uncut, 1 x 16,384: 15.6 / 17.8;
   // 64 x 19,456: 18.6 / 19.5; 128 x 9,216: 17.4 / 18.6.  MXFP4 activations: 64 x 9,216:
@@ -889,7 +892,7 @@ cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cuda
   const int rows = up(p.N, kRows), pair_rows = up(p.N, 2 * kRows);
   const long long tiles = (long long)rows * up(p.T, 64);
   const bool few = p.T <= 32, cut = 2 * tiles <= kNumSMs;
-  if (!(cut || (tiles <= kNumSMs && !F4) || (tiles <= 2 * kNumSMs && few))) {
+  if (!(cut || (!F4 && tiles <= kNumSMs) || (few && (tiles <= 2 * kNumSMs || (!F4 && t.slices >= 16))))) {
     int nt = 32;
     while (nt < kMaxNt && (long long)pair_rows * up(p.T, nt) > kPairs) nt *= 2;
     const int tiles_t = shape(nt, 32, 2);
@@ -911,10 +914,11 @@ cudaError_t launch(const LinearParams& p, const moe_mx& x, const moe_mx& w, cuda
   auto fit = [&](int ctas) {
     int c = (int)(ctas / tiles);
     c = c < kMaxCl ? c : kMaxCl;
-    return c < t.slices / 2 ? c : (t.slices > 1 ? t.slices / 2 : 1);
+    c = c < t.slices / 2 ? c : t.slices / 2;
+    return c > 1 ? c : 1;
   };
   const int one = fit(kNumSMs), both = fit(2 * kNumSMs);
-  const bool two = t.nt <= 32 && tiles * both * 10 > tiles * one * 20 + kNumSMs;
+  const bool two = few && (tiles > kNumSMs || tiles * both * 10 > tiles * one * 20 + kNumSMs);
   const int cl = two ? both : one;
   t.per = up(t.slices, cl);
   // The CTA's sums lie in the ring, those that it receives behind.
