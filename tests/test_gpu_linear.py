@@ -217,7 +217,9 @@ def test_a_wait_that_runs_out_is_reported(moe):
 
 
 @pytest.mark.parametrize("T,N,K,kind", [(65536, 130, 128, "e2m1"), (65536, 257, 256, "e4m3"), (3, 262144, 128, "e4m3"), (300, 262144, 128, "e2m1"),
-                                        (1, 1, 16384, "e4m3"), (2000, 1, 256, "e2m1"), (9000, 3, 128, "e4m3")])
+                                        (1, 1, 16384, "e4m3"), (2000, 1, 256, "e2m1"), (9000, 3, 128, "e4m3"),
+                                        (30, 45001, 2048, "e4m3"), (1, 60000, 2176, "e4m3"), (7, 30000, 384, "e2m1"), (100, 9300, 384, "e4m3"),
+                                        (64, 19332, 256, "e4m3")])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_largest_and_thinnest(moe, T, N, K, kind, out):
     """The largest counts of rows and results, and single columns, with one addend for all rows; rows at both ends and in
