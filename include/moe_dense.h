@@ -115,12 +115,12 @@ int moe_mx_linear(const moe_mx* x, const moe_mx* w, const void* add, int64_t add
  *   rank    = tokens before t in the order by (logit descending, index)
  *   entropy = log S - sum exp(z_i - m) (z_i - m) / S
  *   top     = the first `top` tokens of that order and their log probabilities
- * Statistics are fp32.  NaN counts as -inf; if some logits are +inf, those share
- * the probability evenly and all others have none.  A token outside [0, vocab)
- * gives logprob -inf and rank -1 (padding).  Tokens of probability 0 by a logit
- * of -inf are not listed: where fewer than `top` are left, ids are -1 with
- * log probability -inf.  A row with nothing but -inf or NaN gives logprob -inf,
- * entropy 0 and no alternatives.
+ * Statistics are fp32, and logprob <= 0 <= entropy.  NaN counts as -inf; if some
+ * logits are +inf, those share the probability evenly and all others have none.  A
+ * token outside [0, vocab) gives logprob -inf and rank -1 (padding).  Tokens of
+ * probability 0 by a logit of -inf are not listed: where fewer than `top` are left,
+ * ids are -1 with log probability -inf.  A row with nothing but -inf or NaN gives
+ * logprob -inf, entropy 0 and no alternatives.
  *   logits       [rows][vocab], `stride` elements between rows, f32 or bf16
  *                (aligned to the element); vocab <= MOE_LOGPROBS_MAX_VOCAB
  *   tokens       [rows] int32, or NULL: entropy and alternatives only (logprob

@@ -7,9 +7,14 @@
 // 2^(z L + c), one FMA with one rounding; the rounding of c is common to all and
 // cancels in every result, all of which are taken by the same FMA.  A warp's
 // reference is the largest logit of its part of the first tile, and is raised only
-// for logits 40 above it: were it each thread's own maximum, some lane of a warp
-// would have a new one at nearly every step.  Threads, warps and the CTAs of a row
-// join their (m, c, S, U) in a fixed order.
+// for logits more than 3 above it: were it each thread's own maximum, some lane of a
+// warp would have a new one at nearly every step.  (512 rows of 163,840 without
+// alternatives: 40.4 us at 3, 41.2 at 2.)  It may not stay far below the maximum,
+// where log S and U / S would be large numbers with a small difference (40 below, an
+// entropy of 0 erred by 5e-6, to either side).  The reference is a logit of the row, so
+// that one token 3 above all others is at the reference, and otherwise the entropy is
+// no small number.  Threads, warps and the CTAs of a row join their (m, c, S, U) in a
+// fixed order.  What rounding leaves on the wrong side of 0 is 0.
 //
 // One comparison per 16 logits of a thread decides whether there is more to do with them: a
 // far new maximum, logits ahead of the given token (which are counted one by one), or
@@ -44,7 +49,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -300.f;                   // 2^-300 is 0 in fp32
 constexpr float kPlain = 1048576.f;              // references beyond, whose c is rounded by 0.1 and more, are summed again at the end
-constexpr float kAbove = 40.f;                   // logits this far above the reference raise it: weights below 2^58
+constexpr float kAbove = 3.f;                    // logits this far above the reference raise it: weights below 2^5
 
 typedef unsigned long long Key;  // (order bits of a logit) << 32 | ~index: larger is better; 0: none
 
@@ -103,10 +108,10 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
 }
 
 // Sums over a larger reference.  Those around a far one (masked logits) may be
-// infinite; they leave nothing here.
+// infinite or NaN; they leave nothing here.
 __device__ __forceinline__ void raise(float M, float C, Stats& a) {
   const float d = fmaxf(C - a.c, kFar), f = exp2_of(d);
-  const bool left = a.m > -INFINITY && f > 0.f;
+  const bool left = a.s > 0.f && f > 0.f;
   a.u = left ? f * (a.u + a.s * d) : 0.f;
   a.s = left ? f * a.s : 0.f;
   a.m = M;
@@ -517,7 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
     pass(cuda::std::false_type{});
   gather();
 
-  // Statistics: lanes, warps, CTAs.
+  // Statistics: lanes, of one reference, then warps, CTAs.
+  {
+    const float m = order_float(__reduce_max_sync(0xFFFFFFFFu, order_bits(st.m)));
+    raise(m, shift_of(m), st);
+  }
   st = warp_join(st);
   if (lane == 0) sh.warp[warp] = st;
   __syncthreads();
@@ -606,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
   auto log_prob = [&](float z) {
     if (infinite) return z == INFINITY ? -log2_s * kLn2 : -INFINITY;
     if (z == -INFINITY) return -INFINITY;
-    if (plain && fabsf(z) <= kPlain) return (fmaf(z, kLog2e, st.c) - log2_s) * kLn2;
+    if (plain && fabsf(z) <= kPlain) return fminf((fmaf(z, kLog2e, st.c) - log2_s) * kLn2, 0.f);
     return (z - st.m) - log2_s * kLn2;
   };
   if (lane == 0) {
     if (p.logprob) p.logprob[r] = known ? log_prob(zt) : -INFINITY;
     if (p.rank) p.rank[r] = known ? st.count + (zt == -INFINITY ? token : 0) : -1;
-    if (p.entropy) p.entropy[r] = nothing ? 0.f : (log2_s - st.u / st.s) * kLn2;  // infinite: u = 0
+    if (p.entropy) p.entropy[r] = nothing ? 0.f : fmaxf((log2_s - st.u / st.s) * kLn2, 0.f);  // infinite: u = 0
   }
   if (lane < top) {
     const Key k = sh.best[lane];
