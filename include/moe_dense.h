@@ -101,7 +101,7 @@ int moe_rms_norm(int rows, int cols, const void* x, int x_dtype, int64_t x_strid
  *             (rows of out must not overlap); any alignment of its type.  Other
  *             overlaps of out with the operands are the caller's to avoid.
  *   status    a DEVICE int32 or NULL, as in moe_serve.h (MOE_ERR_TIMEOUT: a
- *             bounded wait gave up)
+ *             bounded wait gave up; results without their whole sum are NaN)
  * K: a multiple of 128.  Codes are 32-byte aligned with row strides a multiple
  * of 32 bytes, scales 4-byte aligned with row strides a multiple of 4.  A row's
  * sum is taken in a fixed order for given sizes: results are the same from run

@@ -180,6 +180,7 @@ struct LinShared {
   uint64_t sf_full[kSfRing];    // scales stored: scale warps (a pair: the first CTA's)
   uint64_t sf_empty[kSfRing];   // used: commit
   uint64_t sums;                // a tile's MMAs have finished: commit
+  uint64_t ended;               // MMAs that a wait cut short have finished: commit
   uint64_t drained;             // pairs: the sums have been read
   uint64_t recv;                // clusters: the others' sums have arrived
   uint32_t tmem_base;
@@ -226,6 +227,24 @@ __device__ __forceinline__ bool lin_wait(const LinCtx& c, uint64_t* bar, uint32_
 }
 __device__ __forceinline__ bool lin_warp_wait(const LinCtx& c, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, lin_wait(c, bar, parity));
+}
+
+// Barrier of the scale warps, and whether all their threads have `own`.
+__device__ __forceinline__ bool sync_all_of(bool own) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.and.pred b, %2, %3, a;\n selp.u32 %0, 1, 0, b;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)own), "n"(kSfBarrier), "n"(kSfWarps * 32)
+      : "memory");
+  return all;
+}
+
+// To a pair's second CTA, which does not see this one's flag.
+__device__ __forceinline__ void tell_abort(const LinShared& sh, uint32_t one) {
+  if (one)
+    asm volatile("st.shared::cluster.u32 [%0], 1;\n fence.acq_rel.cluster;" ::"r"(remote_smem(&sh.abort_flag, 1)) : "memory");
+  __syncwarp();
 }
 
 // Place in a ring: index, and the parity of its current round.
@@ -455,6 +474,14 @@ __device__ __forceinline__ void put_column(const LinearParams& p, int64_t t, int
       if (e0 + e < count) put(e0 + e, __uint_as_float(v[e0 + e]) + a[e]);
   }
 }
+// The same rows where a wait gave up and there is no sum.
+template <bool OUT_BF16>
+__device__ __forceinline__ void put_nan(const LinearParams& p, int64_t t, int n, int count) {
+  typedef typename Four<OUT_BF16>::One T;
+  T* o = (T*)p.out + t * p.out_stride + n;
+#pragma unroll 1
+  for (int e = 0; e < count; ++e) o[e * p.out_stride] = Four<OUT_BF16>::put1(__int_as_float(0x7FC00000));
+}
 // Whether rows of out and the addend are whole groups of four, all aligned.
 template <bool OUT_BF16>
 __device__ __forceinline__ bool wide_rows(const LinearParams& p) {
@@ -496,6 +523,7 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
       mbar_init(&sh.sf_empty[i], 1);
     }
     mbar_init(&sh.sums, 1);
+    mbar_init(&sh.ended, 1);
     mbar_init(&sh.recv, 1);
     sh.abort_flag = 0;
     mbar_init_fence();
@@ -553,10 +581,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   } else if (warp == kMmaWarp) {
     Ring r, sf;
     const uint32_t one = elect_one();  // commits track the elected lane's MMAs
-    mmas_of_tile<F4, 1>(t, c, smem_u32(ring), tmem, ns, r, sf, one);
-    commit<1>(&sh.sums, one);
+    uint64_t* end = mmas_of_tile<F4, 1>(t, c, smem_u32(ring), tmem, ns, r, sf, one) ? &sh.sums : &sh.ended;
+    commit<1>(end, one);
     // Everything issued has finished before Tensor Memory is released.
-    if (!mbar_wait(&sh.sums, 0)) report(p.status);
+    if (!mbar_wait(end, 0)) report(p.status);
   } else {
     Ring sf;
     int step = 0;
@@ -588,9 +616,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
     }
     tc_fence_before();
     if (cl > 1) fence_async_smem();
-    named_sync(kSfBarrier, kSfWarps * 32);
+    const bool whole = sync_all_of(fine || ns == 0);
     if (cl > 1) {
-      if (etid < cl && etid != rank) {
+      // Where a wait gave up nothing is sent, and the others' waits give up as well.
+      if (etid < cl && etid != rank && whole) {
         const int o0 = min(etid * own, valid), n = min(own, valid - o0);
         if (n > 0)
           bulk_s2s(remote_smem(recv + (size_t)(rank < etid ? rank : rank - 1) * own * kRows, etid), stage + o0 * kRows,
@@ -650,7 +679,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
   }
   tc_fence_before();
   __syncthreads();
-  let_copies_land(sh);
+  if (sh.abort_flag) {
+    let_copies_land(sh);
+    if (tid < kRows && n0 + tid < p.N) put_nan<OUT_BF16>(p, t0 + own0, n0 + tid, mine);
+  }
   __syncwarp();
   if (cl > 1) cluster_wait();
   if (warp == kMmaWarp) {
@@ -709,6 +741,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
       mbar_init(&sh.sf_empty[i], 1);
     }
     mbar_init(&sh.sums, 1);
+    mbar_init(&sh.ended, 1);
     mbar_init(&sh.drained, 2 * kPairEpWarps);
     sh.abort_flag = 0;
     mbar_init_fence();
@@ -752,16 +785,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
       Ring r, sf;
       const uint32_t one = elect_one();
       int ti = 0;
-      for (int tile = pair; tile < t.tiles; tile += pairs) {
-        if (ti > 0 && !lin_warp_wait(c, &sh.drained, (ti - 1) & 1)) break;
+      bool ok = true;
+      for (int tile = pair; tile < t.tiles; tile += pairs, ++ti) {
+        ok = ti == 0 || lin_warp_wait(c, &sh.drained, (ti - 1) & 1);
         tc_fence_after();
-        const bool ok = mmas_of_tile<F4, 2>(t, c, smem_u32(ring), tmem, t.slices, r, sf, one);
-        commit<2>(&sh.sums, one);
-        ++ti;
+        ok = ok && mmas_of_tile<F4, 2>(t, c, smem_u32(ring), tmem, t.slices, r, sf, one);
         if (!ok) break;
+        commit<2>(&sh.sums, one);
+      }
+      if (!ok) {
+        tell_abort(sh, one);
+        commit<2>(&sh.ended, one);
       }
       // Everything issued has finished before Tensor Memory is released.
-      if (ti > 0 && !mbar_wait(&sh.sums, (ti - 1) & 1)) report(p.status);
+      if (!(ok ? mbar_wait(&sh.sums, (ti - 1) & 1) : mbar_wait(&sh.ended, 0))) report(p.status);
     }
   } else if (warp < kPairEpWarp0) {
     regs_dec<kRegsScale>();
@@ -781,8 +818,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
     regs_inc<kRegsEpilogue>();
     const int q = warp & 3, part = (warp - kPairEpWarp0) >> 2;  // lanes 32 q ..; half of the columns
     const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * t.xrows);
-    int ti = 0;
-    for (int tile = pair; tile < t.tiles; tile += pairs, ++ti) {
+    int ti = 0, tile = pair;
+    for (; tile < t.tiles; tile += pairs, ++ti) {
       const int n = ((tile % t.tiles_n) * 2 + rank) * kRows + q * 32 + lane;
       const int64_t tt = (int64_t)(tile / t.tiles_n) * t.nt + part * t.xrows;
       const int count0 = n - lane < p.N ? (int)min((int64_t)t.xrows, p.T - tt) : 0, count = n < p.N ? count0 : 0;
@@ -803,6 +840,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const LinearPar
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (32 * j < count) put_column<OUT_BF16>(p, tt + 32 * j, n, v[j], count - 32 * j);
+    }
+#pragma unroll 1
+    for (; tile < t.tiles; tile += pairs) {  // without sums
+      const int n = ((tile % t.tiles_n) * 2 + rank) * kRows + q * 32 + lane;
+      const int64_t tt = (int64_t)(tile / t.tiles_n) * t.nt + part * t.xrows;
+      if (n < p.N) put_nan<OUT_BF16>(p, tt, n, (int)min((int64_t)t.xrows, p.T - tt));
     }
   }
   tc_fence_before();
