@@ -1,5 +1,9 @@
 // dense.cuh — parameters of the kernels behind moe_dense.h and the MX block
 // arithmetic that they share.
+//
+// These kernels read operands by plain loads behind pdl_wait(): what the kernel before
+// writes while this one has started already is not read-only for it, as the
+// non-coherent path (ld.global.nc, __ldg) requires.
 #pragma once
 
 #include <cuda.h>

@@ -280,15 +280,15 @@ struct ScaleRow {
     if (WIDE) {
       asm volatile(
           "{\n .reg .pred q;\n setp.lt.s32 q, %5, %6;\n mov.b32 %0, %7;\n mov.b32 %1, %7;\n mov.b32 %2, %7;\n mov.b32 %3, %7;\n"
-          " @q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+          " @q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
           : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
           : "l"(p + w), "r"(w), "r"(words), "n"(one));
     } else {
       asm volatile(
           "{\n .reg .pred q0, q1, q2, q3;\n setp.lt.s32 q0, %5, %6;\n setp.lt.s32 q1, %7, %6;\n setp.lt.s32 q2, %8, %6;\n"
           " setp.lt.s32 q3, %9, %6;\n mov.b32 %0, %10;\n mov.b32 %1, %10;\n mov.b32 %2, %10;\n mov.b32 %3, %10;\n"
-          " @q0 ld.global.nc.u32 %0, [%4];\n @q1 ld.global.nc.u32 %1, [%4 + 4];\n @q2 ld.global.nc.u32 %2, [%4 + 8];\n"
-          " @q3 ld.global.nc.u32 %3, [%4 + 12];\n}"
+          " @q0 ld.global.u32 %0, [%4];\n @q1 ld.global.u32 %1, [%4 + 4];\n @q2 ld.global.u32 %2, [%4 + 8];\n"
+          " @q3 ld.global.u32 %3, [%4 + 12];\n}"
           : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
           : "l"(p + w), "r"(w), "r"(words), "r"(w + 1), "r"(w + 2), "r"(w + 3), "n"(one));
     }

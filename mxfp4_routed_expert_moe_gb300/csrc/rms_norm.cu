@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kMaxThreads) k_rms_nor
     const int c8 = first + j * step;
     if (c8 < per_row) {
       if (p.weight) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p.weight) + 2 * c8);
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p.weight) + 2 * c8 + 1);
+        const float4 a = reinterpret_cast<const float4*>(p.weight)[2 * c8];
+        const float4 b = reinterpret_cast<const float4*>(p.weight)[2 * c8 + 1];
         const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * factor * w[i];

@@ -164,7 +164,7 @@ struct Piece {
   __device__ __forceinline__ bool whole(int v) const { return 8 * v >= mis && 8 * v + 8 <= mis + n; }
   __device__ __forceinline__ float one(int i) const {
     if (i < mis || i >= mis + n) return -INFINITY;
-    return BF16 ? bf16_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i)) : __ldg(reinterpret_cast<const float*>(base) + i);
+    return BF16 ? bf16_f32(reinterpret_cast<const uint16_t*>(base)[i]) : reinterpret_cast<const float*>(base)[i];
   }
   __device__ __forceinline__ void edge(int v, float (&x)[8]) const {
 #pragma unroll
@@ -312,11 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
 
   // The given token: its logit, and the bounds above which a logit before or
   // after it in the row is ahead of it.
-  const int token = p.tokens ? __ldg(&p.tokens[r]) : -1;
+  const int token = p.tokens ? p.tokens[r] : -1;
   const bool known = token >= 0 && token < p.vocab;
   float zt = -INFINITY, ahead_before = INFINITY, ahead_after = INFINITY;
   if (known) {
-    zt = BF16 ? bf16_f32(__ldg((const uint16_t*)row + token)) : __ldg((const float*)row + token);
+    zt = BF16 ? bf16_f32(((const uint16_t*)row)[token]) : ((const float*)row)[token];
     zt = fmaxf(zt, -INFINITY) + 0.f;  // NaN as -inf, -0 as 0: a difference's sign tells what is ahead
     ahead_after = zt;
     // Logits before the token are ahead where they are equal, too: above the next
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_token_logprobs(co
     plain = false;
     float s = 0.f, u = 0.f;
     for (int i = tid; i < p.vocab; i += kThreads) {
-      const float z = BF16 ? bf16_f32(__ldg((const uint16_t*)row + i)) : __ldg((const float*)row + i);
+      const float z = BF16 ? bf16_f32(((const uint16_t*)row)[i]) : ((const float*)row)[i];
       if (infinite) {
         s += z == INFINITY ? 1.f : 0.f;
       } else {
