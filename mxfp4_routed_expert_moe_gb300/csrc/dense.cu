@@ -105,6 +105,9 @@ int moe_rms_norm(int rows, int cols, const void* x, int x_dtype, int64_t x_strid
   p.out_stride = ob;
   p.weight = weight;
   p.eps = eps;
+  // Also where eps beside the sum's mean leaves fp32's range.
+  const double room = (3.4028234e38 - eps) * cols * (1 - 0x1p-20);
+  p.most = room < 3.0e38 ? (float)room : 3.0e38f;
   return cuda_status(launch_rms_norm(p, x_dtype, res_dtype, mx ? 2 + mx->type : out_dtype, (cudaStream_t)stream));
 }
 

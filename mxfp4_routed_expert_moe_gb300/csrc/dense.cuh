@@ -152,6 +152,7 @@ struct NormParams {
   int64_t x_stride, res_stride, out_stride;  // bytes
   const float* weight;
   float eps;
+  float most;  // a sum of squares below it is taken as it is
   MxRows mx;
 };
 // out: MOE_DT_F32, MOE_DT_BF16, or 2 + moe_mx_type.

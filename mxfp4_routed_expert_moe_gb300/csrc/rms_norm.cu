@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : kMaxThreads) k_rms_nor
   }
   sum = row_add<WARP>(sum, sh);
   float factor = factor_of(sum, (float)p.cols, p.eps);
-  if (!(sum < 3.0e38f)) {
-    // Squares past fp32's range, an infinity or a NaN (uniform over the row): again
-    // with the row's largest magnitude brought near 1, if it is a number.
+  if (!(sum < p.most)) {
+    // Squares, or their mean and eps, past fp32's range, an infinity or a NaN (uniform
+    // over the row): again with the row's largest magnitude brought near 1, if it is a
+    // number.
     float m = 0.f;
     bool nan = false;
 #pragma unroll
