@@ -49,9 +49,13 @@ typedef struct {
   int64_t q_stride, s_stride;
 } moe_mx;
 
+/* What is beyond these is refused with MOE_ERR_UNSUPPORTED. */
 #define MOE_DENSE_MAX_COLS 16384     /* of moe_rms_norm, moe_mx_quantize, moe_mx_dequantize, moe_mx_linear's inner size */
+#define MOE_DENSE_MAX_STRIDE (1LL << 38) /* strides in elements stay below it to either side, of codes and scales below 4 times it in bytes */
+#define MOE_MX_MAX_VALUES 34359730144LL /* rows x cols of one conversion: 2^35 less 8,224 */
 #define MOE_LINEAR_MAX_ROWS 65536    /* rows of activations */
 #define MOE_LINEAR_MAX_OUTS 262144   /* rows of weights */
+#define MOE_LOGPROBS_MAX_ROWS 16777216
 #define MOE_LOGPROBS_MAX_VOCAB 262144
 #define MOE_LOGPROBS_MAX_TOP 32
 
@@ -62,12 +66,12 @@ typedef struct {
  * 255 and codes 0: all of it reads as NaN.
  *   x         [out->rows][out->cols] of type x_dtype (MOE_DT_F32 / MOE_DT_BF16),
  *             16-byte aligned, x_stride elements between rows (a multiple of 16
- *             bytes) */
+ *             bytes); at most MOE_MX_MAX_VALUES.  x and out must not overlap. */
 int moe_mx_quantize(const void* x, int x_dtype, int64_t x_stride, const moe_mx* out, void* stream);
 
 /* Dequantise: out = x, each value rounded once (fp32: exact where it is in
  * range; bf16: exact down to its subnormals).  `out` as x above; its rows must not
- * overlap. */
+ * overlap, nor x. */
 int moe_mx_dequantize(const moe_mx* x, void* out, int out_dtype, int64_t out_stride, void* stream);
 
 /* Residual sum and root-mean-square norm, row by row:
@@ -122,7 +126,8 @@ int moe_mx_linear(const moe_mx* x, const moe_mx* w, const void* add, int64_t add
  * ids are -1 with log probability -inf.  A row with nothing but -inf or NaN gives
  * logprob -inf, entropy 0 and no alternatives.
  *   logits       [rows][vocab], `stride` elements between rows, f32 or bf16
- *                (aligned to the element); vocab <= MOE_LOGPROBS_MAX_VOCAB
+ *                (aligned to the element); rows <= MOE_LOGPROBS_MAX_ROWS, vocab <=
+ *                MOE_LOGPROBS_MAX_VOCAB
  *   tokens       [rows] int32, or NULL: entropy and alternatives only (logprob
  *                and rank are then NULL too)
  *   logprob, entropy [rows] fp32 or NULL;  rank [rows] int32 or NULL

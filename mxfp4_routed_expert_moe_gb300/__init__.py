@@ -287,5 +287,6 @@ class ExpertTable:
 # The operators around the layer in a serving step.
 from .serve import (KVBatch, KVCache, SAMPLE_MAX_VOCAB, SERVE_EXPORTS, SERVE_MAX_BATCH, SERVE_MAX_LEN,  # noqa: E402
                     attention_workspace_bytes, kv_append, prefix_attention, rope_table, sample)
-from .dense import (DENSE_EXPORTS, DENSE_MAX_COLS, LINEAR_MAX_OUTS, LINEAR_MAX_ROWS, LOGPROBS_MAX_TOP,  # noqa: E402
-                    LOGPROBS_MAX_VOCAB, MXMatrix, mx_dequantize, mx_linear, mx_quantize, rms_norm, token_logprobs)
+from .dense import (DENSE_EXPORTS, DENSE_MAX_COLS, DENSE_MAX_STRIDE, LINEAR_MAX_OUTS, LINEAR_MAX_ROWS,  # noqa: E402
+                    LOGPROBS_MAX_ROWS, LOGPROBS_MAX_TOP, LOGPROBS_MAX_VOCAB, MX_MAX_VALUES, MXMatrix, mx_dequantize,
+                    mx_linear, mx_quantize, rms_norm, token_logprobs)

@@ -13,7 +13,7 @@ bool is_dtype(int d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 int64_t size_of(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
 int64_t magnitude(int64_t stride) { return stride < 0 ? -stride : stride; }
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // bytes: tensor maps, and products with a row that stay in range
+constexpr int64_t kMaxStride = 4 * MOE_DENSE_MAX_STRIDE;  // bytes: tensor maps, and products with a row that stay in range
 
 int check_mx(const moe_mx* a) {
   if (!a || !a->q || !a->s || !aligned(a->q, 16)) return MOE_ERR_INVALID_ARG;
@@ -35,8 +35,9 @@ int check_rows(const void* x, int dtype, int64_t stride, int rows, int cols, boo
 
 MxRows rows_of(const moe_mx& a) { return {a.q, a.s, a.q_stride, a.s_stride}; }
 
-// Eights of values that one launch of the conversions covers: its CTAs' last counts stay in 32 bits.
-bool too_many(const moe_mx* a) { return (int64_t)a->rows * (a->cols / 8) >= ((int64_t)1 << 32) - 1024; }
+// Values that one launch of the conversions covers: counts of eights, its last CTA's behind the end too, stay in 32 bits.
+bool too_many(const moe_mx* a) { return (int64_t)a->rows * a->cols > MOE_MX_MAX_VALUES; }
+static_assert(MOE_MX_MAX_VALUES / 8 < (1LL << 32) - 1024 && MOE_MX_MAX_VALUES / 8 + 4 >= (1LL << 32) - 1024, "blocks of 32");
 
 }  // namespace
 
@@ -154,7 +155,7 @@ int moe_token_logprobs(int rows, int vocab, const void* logits, int dtype, int64
   const void* words[] = {tokens, logprob, rank, entropy, top_ids, top_logprobs};
   for (const void* w : words)
     if (!aligned(w, 4)) return MOE_ERR_INVALID_ARG;
-  if (vocab > MOE_LOGPROBS_MAX_VOCAB || rows > (1 << 24) || top > MOE_LOGPROBS_MAX_TOP || magnitude(stride) >= kMaxStride / 4)
+  if (vocab > MOE_LOGPROBS_MAX_VOCAB || rows > MOE_LOGPROBS_MAX_ROWS || top > MOE_LOGPROBS_MAX_TOP || magnitude(stride) >= kMaxStride / 4)
     return MOE_ERR_UNSUPPORTED;
   LogprobParams p = {};
   p.rows = rows;

@@ -10,13 +10,17 @@ from . import serve
 from .serve import _same_gpu, _status, _stream
 
 __all__ = ["MXMatrix", "mx_quantize", "mx_dequantize", "mx_linear", "rms_norm", "token_logprobs", "DENSE_EXPORTS",
-           "DENSE_MAX_COLS", "LINEAR_MAX_ROWS", "LINEAR_MAX_OUTS", "LOGPROBS_MAX_VOCAB", "LOGPROBS_MAX_TOP"]
+           "DENSE_MAX_COLS", "DENSE_MAX_STRIDE", "MX_MAX_VALUES", "LINEAR_MAX_ROWS", "LINEAR_MAX_OUTS", "LOGPROBS_MAX_ROWS",
+           "LOGPROBS_MAX_VOCAB", "LOGPROBS_MAX_TOP"]
 
 # Every symbol moe_dense.h declares (checked by the tests against the .so).
 DENSE_EXPORTS = ("moe_mx_quantize", "moe_mx_dequantize", "moe_rms_norm", "moe_mx_linear", "moe_token_logprobs")
 DENSE_MAX_COLS = 16384          # MOE_DENSE_MAX_COLS
+DENSE_MAX_STRIDE = 1 << 38      # MOE_DENSE_MAX_STRIDE
+MX_MAX_VALUES = 34359730144     # MOE_MX_MAX_VALUES
 LINEAR_MAX_ROWS = 65536         # MOE_LINEAR_MAX_ROWS
 LINEAR_MAX_OUTS = 262144        # MOE_LINEAR_MAX_OUTS
+LOGPROBS_MAX_ROWS = 16777216    # MOE_LOGPROBS_MAX_ROWS
 LOGPROBS_MAX_VOCAB = 262144     # MOE_LOGPROBS_MAX_VOCAB
 LOGPROBS_MAX_TOP = 32           # MOE_LOGPROBS_MAX_TOP
 
