@@ -11,9 +11,9 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 bool is_dtype(int d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 int64_t size_of(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
-int64_t magnitude(int64_t stride) { return stride < 0 ? -stride : stride; }
+uint64_t magnitude(int64_t stride) { return stride < 0 ? -(uint64_t)stride : (uint64_t)stride; }
 
-constexpr int64_t kMaxStride = 4 * MOE_DENSE_MAX_STRIDE;  // bytes: tensor maps, and products with a row that stay in range
+constexpr uint64_t kMaxStride = 4 * MOE_DENSE_MAX_STRIDE;  // bytes: tensor maps, and products with a row that stay in range
 
 int check_mx(const moe_mx* a) {
   if (!a || !a->q || !a->s || !aligned(a->q, 16)) return MOE_ERR_INVALID_ARG;
@@ -21,15 +21,15 @@ int check_mx(const moe_mx* a) {
   if (a->rows < 1 || a->cols < 32 || a->cols % 32) return MOE_ERR_INVALID_ARG;
   const int64_t row = a->type == MOE_MX_E4M3 ? a->cols : a->cols / 2;
   if (a->q_stride % 16 || a->q_stride < row || a->s_stride < a->cols / 32) return MOE_ERR_INVALID_ARG;
-  if (a->cols > MOE_DENSE_MAX_COLS || a->q_stride >= kMaxStride || a->s_stride >= kMaxStride) return MOE_ERR_UNSUPPORTED;
+  if (a->cols > MOE_DENSE_MAX_COLS || magnitude(a->q_stride) >= kMaxStride || magnitude(a->s_stride) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 // Rows of `cols` elements at 16-byte vectors; apart: an output's.
 int check_rows(const void* x, int dtype, int64_t stride, int rows, int cols, bool apart) {
-  if (!x || !is_dtype(dtype) || !aligned(x, 16) || (stride * size_of(dtype)) % 16) return MOE_ERR_INVALID_ARG;
+  if (!x || !is_dtype(dtype) || !aligned(x, 16) || (uint64_t)stride * size_of(dtype) % 16) return MOE_ERR_INVALID_ARG;
   if (magnitude(stride) >= kMaxStride / 4) return MOE_ERR_UNSUPPORTED;
-  if (apart && rows > 1 && magnitude(stride) < cols) return MOE_ERR_INVALID_ARG;
+  if (apart && rows > 1 && magnitude(stride) < (uint64_t)cols) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -121,7 +121,7 @@ int moe_mx_linear(const moe_mx* x, const moe_mx* w, const void* add, int64_t add
   if (!aligned(out, size) || !aligned(add, size) || (status && !aligned(status, 4))) return MOE_ERR_INVALID_ARG;
   for (const moe_mx* a : {x, w})
     if (!aligned(a->q, 32) || a->q_stride % 32 || !aligned(a->s, 4) || a->s_stride % 4) return MOE_ERR_INVALID_ARG;
-  if (x->rows > 1 && magnitude(out_stride) < w->rows) return MOE_ERR_INVALID_ARG;
+  if (x->rows > 1 && magnitude(out_stride) < (uint64_t)w->rows) return MOE_ERR_INVALID_ARG;
   // In place: every row over itself.
   if (add == out && x->rows > 1 && add_stride != out_stride) return MOE_ERR_INVALID_ARG;
   if (w->type != MOE_MX_E2M1 || x->cols % 128 || x->rows > MOE_LINEAR_MAX_ROWS || w->rows > MOE_LINEAR_MAX_OUTS)
@@ -148,7 +148,7 @@ int moe_token_logprobs(int rows, int vocab, const void* logits, int dtype, int64
                        float* logprob, int32_t* rank, float* entropy, int top, int32_t* top_ids, float* top_logprobs,
                        void* stream) {
   if (rows < 1 || vocab < 1 || !logits || !is_dtype(dtype) || !aligned(logits, size_of(dtype))) return MOE_ERR_INVALID_ARG;
-  if (rows > 1 && magnitude(stride) < vocab) return MOE_ERR_INVALID_ARG;
+  if (rows > 1 && magnitude(stride) < (uint64_t)vocab) return MOE_ERR_INVALID_ARG;
   if (!tokens && (logprob || rank)) return MOE_ERR_INVALID_ARG;
   if (top < 0 || (top > 0) != (top_ids != nullptr) || (top > 0) != (top_logprobs != nullptr)) return MOE_ERR_INVALID_ARG;
   if (!logprob && !rank && !entropy && !top) return MOE_ERR_INVALID_ARG;

@@ -44,3 +44,13 @@ def test_refused_beyond_each_limit(moe, dense):
         assert scores(dense, stride=stride) == 2
     for stride in (4 * far, 1 << 62):
         assert quantize(dense, mx(dense, q_stride=stride)) == quantize(dense, mx(dense, s_stride=stride)) == 2
+
+
+def test_the_lowest_stride_is_refused(moe, dense):
+    """-2^63 has no magnitude in 64 bits."""
+    w = mx(dense, type=0, q_stride=128)
+    assert quantize(dense, mx(dense), stride=INT64_MIN) == 2
+    assert dequantize(dense, mx(dense), stride=INT64_MIN) == 2
+    assert norm(dense, xs=INT64_MIN) == norm(dense, rs=INT64_MIN) == norm(dense, os=INT64_MIN) == 2
+    assert linear(dense, mx(dense), w, os=INT64_MIN) == linear(dense, mx(dense), w, add=1 << 21, adds=INT64_MIN) == 2
+    assert scores(dense, stride=INT64_MIN) == 2
