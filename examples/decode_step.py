@@ -124,13 +124,20 @@ class Model:
         return torch.nn.functional.rms_norm(h, (self.hidden,)).bfloat16() @ self.head.T
 
 
-def score(model: Model, text, top=0):
+def score(model: Model, text, top=0, pages=None):
     """Of a text's tokens but the first: log probability, rank and the distribution's entropy, and with ``top`` the
-    best alternatives' ids and log probabilities."""
+    best alternatives' ids and log probabilities.  The text's keys and values are written to ``pages`` (ids; the cache's
+    first pages without), whatever those held: between decode steps, pages that no sequence uses."""
     n, size = text.shape[0], model.page_size
+    need = -(-n // size)
+    pages = list(range(need)) if pages is None else [int(p) for p in pages]
+    if n < 2 or n > model.rope.shape[0]:
+        raise ValueError(f"a text of 2 to {model.rope.shape[0]} tokens, not {n}")
+    if len(pages) < need or len(set(pages)) < len(pages) or not all(0 <= p < model.pages for p in pages):
+        raise ValueError(f"a text of {n} tokens takes {need} different pages of {model.pages}, not {pages}")
     i32, f32 = dict(dtype=torch.int32, device="cuda"), dict(device="cuda")
-    pages = torch.arange(-(-n // size), **i32)
-    batch = moe.KVBatch(torch.full((1,), n, **i32), pages[None], tokens=n, max_q=n, q_start=torch.tensor([0, n], **i32))
+    table = torch.tensor([pages[:need]], **i32)
+    batch = moe.KVBatch(torch.full((1,), n, **i32), table, tokens=n, max_q=n, q_start=torch.tensor([0, n], **i32))
     logits = model.forward(text, batch)[:-1]
     out = dict(logprob=torch.empty(n - 1, **f32), rank=torch.empty(n - 1, **i32), entropy=torch.empty(n - 1, **f32))
     if top:
