@@ -704,8 +704,10 @@ __global__ void __launch_bounds__(kThreads) k_linear(const LinearParams p, const
 // Eight epilogue warps take a tile's sums to registers at once (128 a thread) and
 // give Tensor Memory back; addends and stores go on beside the next tile's MMAs
 // (4,096 x 9,216 x 7,168: 206 -> 176 us, MXFP4 activations 146 -> 112).  The
-// registers come from the other warpgroups.  That product now takes 150 us, 3.6
-// PFLOP/s with the tensor pipe 78 % busy, and 99 us, 5.4 PFLOP/s and 56 %.
+// registers come from the other warpgroups.  That product now takes 148 to 155 us in
+// some hundred calls (3.5 PFLOP/s; the tensor pipe 79 % busy) and 174 to 179 in
+// thousands, which the power limit holds at 1.53 GHz; with MXFP4 activations 98 to 101
+// (5.4 PFLOP/s, 56 %) either way.
 constexpr int kPairSfWarp0 = 4, kPairEpWarp0 = 8, kPairEpWarps = 8;
 constexpr int kPairThreads = (kPairEpWarp0 + kPairEpWarps) * 32;
 constexpr int kRegsLaunch = 128, kRegsCopy = 56, kRegsScale = 120, kRegsEpilogue = 168;

@@ -24,11 +24,16 @@
 // times `top` of a row in random order, which gives better bounds on the way.  A list that overflows (rows that grow with
 // the index) is made again in small steps, thinned by the same bound.
 //
-// A cluster of 1 to 8 CTAs takes a row; logits are read once.  Bound by instructions
-// (seven a logit, nine where the given token is not among the best, and 4 to 8 us of
-// barriers and latencies a row) for many rows: 512 of 163,840 in bf16 take 64 us with
-// 20 alternatives, 41 without (4.1 TB/s); by latency for one: 100,003 logits, 8.8 us.
-// More warps an SM, or logits on their way through shared memory, were not faster.
+// A cluster of 1 to 8 CTAs takes a row; logits are read once.  512 rows of 163,840 in
+// bf16 with given tokens take 63 us with 20 alternatives (2.7 TB/s; 15.5 warp
+// instructions per 32 logits, issue slots 58 % busy) and 40 without (4.2 TB/s; 9.6, 55
+// %): bound by instructions on the half of an SM's warps that 64 registers a thread
+// leave, and by two rounds of CTAs (512 on 304 places) with barriers and latencies at
+// each row's end.  What is above the alternatives' bound costs the instructions between
+// the two.  Logits of -inf (a masked vocabulary) have the 16 of their thread summed
+// twice: with a third of them, 54 and 78 us.  One row is bound by latency: 100,003
+// logits, 8.8 us.  More warps an SM, or logits on their way through shared memory, were
+// not faster.
 #include <cooperative_groups.h>
 
 #include <cuda/std/type_traits>
