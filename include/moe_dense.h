@@ -127,9 +127,9 @@ int moe_mx_linear(const moe_mx* x, const moe_mx* w, const void* add, int64_t add
  * probability 0 by a logit of -inf are not listed: where fewer than `top` are left,
  * ids are -1 with log probability -inf.  A row with nothing but -inf or NaN gives
  * logprob -inf, entropy 0 and no alternatives.
- *   logits       [rows][vocab], `stride` elements between rows, f32 or bf16
- *                (aligned to the element); rows <= MOE_LOGPROBS_MAX_ROWS, vocab <=
- *                MOE_LOGPROBS_MAX_VOCAB
+ *   logits       [rows][vocab], f32 or bf16 (aligned to the element), `stride`
+ *                elements between rows, which do not overlap; rows <=
+ *                MOE_LOGPROBS_MAX_ROWS, vocab <= MOE_LOGPROBS_MAX_VOCAB
  *   tokens       [rows] int32, or NULL: entropy and alternatives only (logprob
  *                and rank are then NULL too)
  *   logprob, entropy [rows] fp32 or NULL;  rank [rows] int32 or NULL
